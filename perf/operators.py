@@ -85,7 +85,8 @@ def draw(rng):
     p = rng.choice([0.0, 0.1, 0.2, rng.uniform(0.0, 0.9)])
     if op == "dropout":
         dtype = rng.choice(["bf16", "f32"])
-        return {"op": op, "back": back, "n": _log_int(rng, 1, 1 << (26 if dtype == "bf16" else 25)),
+        # (from 64 elements on: of fewer, a large p leaves none, whatever the inputs)
+        return {"op": op, "back": back, "n": _log_int(rng, 64, 1 << (26 if dtype == "bf16" else 25)),
                 "dtype": dtype, "residual": not back and rng.random() < 0.5, "p": p}
     if op == "join":
         cols = _log_int(rng, 33, 8192)
