@@ -1,0 +1,126 @@
+/*
+ * lowbit_train.h -- C ABI of liblowbit's training-step operators on AMD
+ * Instinct MI355X (gfx950): the steps between which a data-parallel rank's
+ * gradients come into being before the codec of lowbit.h compresses them.
+ *
+ *   dropout      : y = residual + D(x), and its gradient; the mask is drawn
+ *                  from the library's counter hash and never stored
+ *   block join   : between two blocks of a residual network,
+ *                      x_out = a x + gate * D(norm(f)),  z = norm(x_out),
+ *                  and its gradient
+ *
+ * The mask.  Element i of a buffer (for a matrix of `cols` columns, row r's
+ * column c counts as i = r * (cols + cols mod 2) + c) belongs to pair i / 2,
+ * whose word is h = fmix32(lo32(i / 2) ^ fmix32(hi32(i / 2) ^ K(seed))), fmix32
+ * and K as in lowbit.h; its draw is the low half of h for even i, the high half
+ * for odd i.  With t = p * 65536 rounded to nearest (ties to even), D keeps the
+ * elements whose draw is at least t, multiplied by 65536 / (65536 - t) (by 0 if
+ * t = 65536), and gives +0 elsewhere, whatever stood there.
+ *
+ * Conventions of lowbit.h hold: device pointers, element buffers (x, y, f,
+ * w, gradients, parameters, gate, lse, ...) aligned to 16 bytes, targets to 8;
+ * asynchronous launches on `stream`; argument errors returned before anything
+ * is launched; outputs must not overlap inputs or each other unless stated.
+ * Matrices are dense and row-major.  The library allocates nothing: calls with
+ * scratch take `workspace`, aligned to 16 bytes, of at least the bytes that the
+ * matching *_workspace function gives.  It holds nothing between calls, and two
+ * calls that may run at the same time need one each.  All arithmetic is binary32
+ * with each output rounded once; sums run in a fixed order, so that equal
+ * calls give equal bits.  Every call can be captured into a HIP graph.
+ */
+#ifndef LOWBIT_TRAIN_H
+#define LOWBIT_TRAIN_H
+
+#include "lowbit.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * Dropout:  y = residual + D(x)   (residual NULL: y = D(x)).
+ *   x, residual, y : n elements of type t; y may be x or residual itself
+ *   p              : in [0, 1]
+ *   index_offset   : index of element 0 in the mask, a multiple of 8, so that a
+ *                    buffer split at such places draws the same mask
+ * EINVAL: n < 0 or above 2^48, p not in [0, 1], bad index_offset, unknown type,
+ * NULL or misaligned pointer with n > 0.
+ */
+lowbit_status lowbit_dropout(const void* x, const void* residual, lowbit_dtype t, int64_t n,
+                             double p, uint64_t seed, uint64_t index_offset, void* y,
+                             hipStream_t stream);
+
+/* Its gradient: dx = D(dy) with the forward call's p, seed and index_offset
+ * (the residual's gradient is dy itself). */
+lowbit_status lowbit_dropout_backward(const void* dy, lowbit_dtype t, int64_t n, double p,
+                                      uint64_t seed, uint64_t index_offset, void* dx,
+                                      hipStream_t stream);
+
+#define LOWBIT_NORM_RMS 0     /* v / sqrt(mean(v^2) + eps)                        */
+#define LOWBIT_NORM_LAYER 1   /* (v - mean(v)) / sqrt(var(v) + eps), var over cols */
+
+typedef struct {
+    int64_t rows;
+    int64_t cols;             /* 1 .. 16384                                    */
+    int64_t rows_per_gate;    /* consecutive rows that share a row of the gate;
+                                 used only where a gate is given               */
+    int32_t norm;             /* LOWBIT_NORM_*                                 */
+    int32_t block_type;       /* lowbit_dtype of f, z and their gradients      */
+    int32_t stream_type;      /* of x, x_out and their gradients: block_type
+                                 or LOWBIT_F32                                 */
+    int32_t param_type;       /* of weights, biases and gate: block_type or
+                                 LOWBIT_F32                                    */
+    float   eps;              /* >= 0                                          */
+    float   residual_scale;   /* a                                             */
+    double  p;                /* dropout, in [0, 1]; 0: none                   */
+    uint64_t seed;
+} lowbit_join_params;
+
+/*
+ * Block join.  For every row
+ *     u     = norm(f) * post_weight + post_bias
+ *     x_out = a x + gate[row / rows_per_gate] * D(u)
+ *     z     = norm(x_out) * pre_weight + pre_bias
+ * the second norm taken before x_out is rounded.  post_weight, post_bias,
+ * gate, pre_weight, pre_bias may be NULL (1, 0, 1, 1, 0).
+ *   f, x       : rows x cols;  weights and biases: cols
+ *   gate       : ceil(rows / rows_per_gate) x cols
+ *   x_out, z   : rows x cols (written); x_out may be x, z may be f
+ *   stats      : rows x 4 binary32 (written): mean and 1/sqrt(var + eps) of f's
+ *                row, then of x_out's (means 0 for LOWBIT_NORM_RMS)
+ * EINVAL: p == NULL, a size, type or option outside its range, NULL or
+ * misaligned pointer with rows > 0.  EUNSUPPORTED: more than 16384 columns.
+ */
+lowbit_status lowbit_block_join(const void* f, const void* x, const void* post_weight,
+                                const void* post_bias, const void* gate, const void* pre_weight,
+                                const void* pre_bias, const lowbit_join_params* p, void* x_out,
+                                void* z, float* stats, hipStream_t stream);
+
+/* Bytes of workspace that lowbit_block_join_backward needs, or -1 for invalid
+ * params. */
+int64_t lowbit_block_join_backward_workspace(const lowbit_join_params* p);
+
+/*
+ * Gradient of the block join, from the gradients of x_out and z, the forward
+ * call's f, x_out and stats and its parameters (p and seed redraw the mask).
+ *   df, dx : rows x cols (written); df may be dz, dx may be dx_out
+ *   dpost_weight, dpost_bias, dpre_weight, dpre_bias : cols binary32 each;
+ *   dgate  : ceil(rows / rows_per_gate) x cols binary32 (only with a gate).
+ * Any of these five may be NULL and is then not computed; those given are
+ * written whatever parameters are NULL (the gradient at 1 or 0), with zeros for
+ * rows == 0.
+ */
+lowbit_status lowbit_block_join_backward(const void* dx_out, const void* dz, const void* f,
+                                         const void* x_out, const float* stats,
+                                         const void* post_weight, const void* post_bias,
+                                         const void* gate, const void* pre_weight,
+                                         const lowbit_join_params* p, void* df, void* dx,
+                                         float* dpost_weight, float* dpost_bias, float* dgate,
+                                         float* dpre_weight, float* dpre_bias, void* workspace,
+                                         int64_t workspace_bytes, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* LOWBIT_TRAIN_H */

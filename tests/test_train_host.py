@@ -1,0 +1,163 @@
+"""Host-side checks of the training-step operators' C ABI and binding (no GPU
+needed): declared entry points, refusals before any HIP call, workspace sizes,
+and the plain forms that the GPU tests compare with."""
+import ctypes
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+import train_ref as R
+from weight_communication_compression_amd import lowbit as L
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK16 = ctypes.c_void_p(0x1000)          # never read: every call here is refused
+OFF = ctypes.c_void_p(0x1008)
+
+
+def test_library_exports_every_declared_symbol():
+    text = open(os.path.join(ROOT, "include", "lowbit_train.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    names = set(re.findall(r"\b(lowbit_[a-z0-9_]+)\s*\(", text))
+    assert "lowbit_dropout" in names and "lowbit_block_join_backward" in names
+    lib = ctypes.CDLL(L.library_path)
+    for name in names:
+        assert hasattr(lib, name), name
+
+
+def test_reference_draws():
+    """The draws against the scalar definition, across 2^32 pairs too."""
+    for first, seed in ((0, 0), (2 ** 33 - 6, 12345678901234567890), (2 ** 40, 7)):
+        got = R.draws(first, 13, seed)
+        for i in range(13):
+            pair = (first + i) // 2
+            h = R.fmix((pair & 0xFFFFFFFF) ^ R.fmix((pair >> 32) ^ R.seed_key(seed)))
+            assert got[i] == (h >> 16 if (first + i) % 2 else h & 0xFFFF)
+
+
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+def test_reference_join_gradient(norm):
+    """The 64-bit gradient against torch's own differentiation of the formula."""
+    g = np.random.default_rng(1)
+    rows, cols, group, p, seed, a, eps = 5, 11, 2, 0.3, 99, 0.7, 1e-5
+    t = {k: torch.from_numpy(g.standard_normal(sh)).requires_grad_() for k, sh in
+         (("f", (rows, cols)), ("x", (rows, cols)), ("post_w", cols), ("post_b", cols),
+          ("gate", (3, cols)), ("pre_w", cols), ("pre_b", cols))}
+    dxo, dz = (torch.from_numpy(g.standard_normal((rows, cols))) for _ in range(2))
+
+    def normed(v):
+        c = v - v.mean(1, keepdim=True) if norm == "layer" else v
+        return c / torch.sqrt((c * c).mean(1, keepdim=True) + eps)
+
+    keep = torch.from_numpy(R.keep_rows(rows, cols, p, seed) * R.cut_and_factor(p)[1])
+    y = a * t["x"] + t["gate"][torch.arange(rows) // group] * keep * \
+        (normed(t["f"]) * t["post_w"] + t["post_b"])
+    z = normed(y) * t["pre_w"] + t["pre_b"]
+    grads = torch.autograd.grad((y * dxo).sum() + (z * dz).sum(), list(t.values()))
+    n = {k: v.detach().numpy() for k, v in t.items()}
+    y2, z2, stats, _ = R.join(n["f"], n["x"], n["post_w"], n["post_b"], n["gate"], group,
+                              n["pre_w"], n["pre_b"], norm, a, eps, p, seed)
+    assert np.allclose(y2, y.detach().numpy(), rtol=1e-12)
+    assert np.allclose(z2, z.detach().numpy(), rtol=1e-11)
+    got = R.join_back(dxo.numpy(), dz.numpy(), n["f"], y2, stats, n["post_w"], n["post_b"],
+                      n["gate"], group, n["pre_w"], norm, a, p, seed)
+    for name, want in zip(("df", "dx", "dpost_weight", "dpost_bias", "dgate", "dpre_weight",
+                           "dpre_bias"), grads):
+        assert np.allclose(got[name][0], want.numpy(), rtol=1e-9, atol=1e-11), name
+
+
+def _drop(x=OK16, r=None, t=0, n=100, p=0.1, offset=0, y=OK16):
+    return L.lib().lowbit_dropout(x, r, t, n, p, 1, offset, y, None)
+
+
+def test_dropout_refusals():
+    for bad in (dict(x=None), dict(y=None), dict(x=OFF), dict(y=OFF), dict(r=OFF), dict(t=2),
+                dict(t=-1), dict(n=-1), dict(n=2 ** 50), dict(p=-0.1), dict(p=1.5),
+                dict(p=float("nan")), dict(offset=4), dict(offset=1)):
+        assert _drop(**bad) == L.EINVAL, bad
+    assert _drop(n=0, x=None, y=None) == L.OK
+    back = L.lib().lowbit_dropout_backward
+    assert back(None, 0, 10, 0.1, 1, 0, OK16, None) == L.EINVAL
+    assert back(OK16, 0, 10, 0.1, 1, 12, OK16, None) == L.EINVAL
+    assert back(None, 0, 0, 0.1, 1, 0, None, None) == L.OK
+
+
+def _params(**kw):
+    d = dict(rows=10, cols=64, rows_per_gate=5, norm=0, block_type=1, stream_type=1, param_type=1,
+             eps=1e-6, residual_scale=1.0, p=0.1, seed=3)
+    d.update(kw)
+    return L.JoinParams(**d)
+
+
+def _join(q, f=OK16, x=OK16, pw=None, pb=None, gate=None, w2=None, b2=None, xo=OK16, z=OK16,
+          st=OK16):
+    return L.lib().lowbit_block_join(f, x, pw, pb, gate, w2, b2, q, xo, z, st, None)
+
+
+def _join_back(q, ptr=OK16, gate=None, dgate=None, ws=OK16, nbytes=1 << 40, dw=OK16):
+    return L.lib().lowbit_block_join_backward(ptr, ptr, ptr, ptr, ptr, None, None, gate, None, q,
+                                              ptr, ptr, dw, None, dgate, None, None, ws, nbytes,
+                                              None)
+
+
+BAD_JOIN = [dict(rows=-1), dict(cols=0), dict(cols=-3), dict(norm=2), dict(block_type=2),
+            dict(stream_type=5), dict(param_type=-1), dict(block_type=0, stream_type=1),
+            dict(block_type=0, stream_type=0, param_type=1), dict(eps=-1.0),
+            dict(eps=float("nan")), dict(p=1.1), dict(p=-1.0), dict(rows=2 ** 47)]
+
+
+@pytest.mark.parametrize("bad", BAD_JOIN, ids=str)
+def test_join_refuses_options(bad):
+    q = _params(**bad)
+    assert _join(q) == L.EINVAL
+    assert _join_back(q) == L.EINVAL
+    assert L.lib().lowbit_block_join_backward_workspace(q) == -1
+
+
+def test_join_refusals():
+    assert _join(None) == L.EINVAL and _join_back(None) == L.EINVAL
+    assert L.lib().lowbit_block_join_backward_workspace(None) == -1
+    wide = _params(cols=16385)
+    assert _join(wide) == L.EUNSUPPORTED and _join_back(wide) == L.EUNSUPPORTED
+    q = _params()
+    for name in ("f", "x", "xo", "z", "st"):
+        assert _join(q, **{name: None}) == L.EINVAL, name
+        assert _join(q, **{name: OFF}) == L.EINVAL, name
+    for name in ("pw", "pb", "gate", "w2", "b2"):
+        assert _join(q, **{name: OFF}) == L.EINVAL, name
+    assert _join(_params(rows_per_gate=0), gate=OK16) == L.EINVAL
+    assert _join(_params(rows=0), f=None, x=None, xo=None, z=None, st=None) == L.OK
+    for bad in (dict(ptr=None), dict(ptr=OFF), dict(ws=None), dict(ws=OFF), dict(nbytes=0),
+                dict(dgate=OK16), dict(gate=OK16, dgate=OFF), dict(gate=OFF), dict(dw=OFF)):
+        assert _join_back(q, **bad) == L.EINVAL, bad
+    need = L.lib().lowbit_block_join_backward_workspace(q)
+    assert need > 0 and _join_back(q, nbytes=need - 1) == L.EINVAL
+    assert _join_back(_params(rows=0), ptr=None, ws=None, nbytes=0, dw=None) == L.OK
+
+
+def test_binding_refuses():
+    """Tensors that do not fit, on the host: no launch."""
+    f = torch.zeros(4, 8)
+    w = torch.zeros(8)
+    for call in (lambda: L.dropout(f, 0.1, 1),                              # host tensor
+                 lambda: L.dropout(f.half(), 0.1, 1),                       # type
+                 lambda: L.dropout(f, 0.1, 1, residual=torch.zeros(31)),
+                 lambda: L.dropout(f, 0.1, 1, out=torch.zeros(32, dtype=torch.bfloat16)),
+                 lambda: L.dropout_backward(f, 0.1, 1, out=torch.zeros(33)),
+                 lambda: L.block_join(f, f),
+                 lambda: L.block_join(f, torch.zeros(8, 4)),
+                 lambda: L.block_join(f, f, norm="batch"),
+                 lambda: L.block_join(f, f, post_weight=torch.zeros(7)),
+                 lambda: L.block_join(f, f, post_weight=w, pre_weight=w.bfloat16()),
+                 lambda: L.block_join(f, f, gate=w),
+                 lambda: L.block_join(f, f, gate=w, rows_per_gate=3),
+                 lambda: L.block_join(f, f, post_weight=w.half()),
+                 lambda: L.block_join(f, f, x_out=torch.zeros(31)),
+                 lambda: L.block_join_backward(f, f.bfloat16(), f, f, torch.zeros(4, 4)),
+                 lambda: L.block_join_backward(f, f, f, f, torch.zeros(4, 3)),
+                 lambda: L.block_join_backward(f, f, f, f, torch.zeros(4, 4),
+                                               workspace=torch.zeros(3, dtype=torch.uint8))):
+        with pytest.raises(L.LowbitError):
+            call()

@@ -2,8 +2,8 @@
 
     python -m weight_communication_compression_amd.build [--force]
 
-Every translation unit under ``csrc/`` is compiled separately (in parallel)
-and linked into ``weight_communication_compression_amd/liblowbit.so``.
+Every translation unit under ``csrc/`` (the codec) and ``csrc_train/`` (the
+training-step operators) is compiled separately (in parallel) and linked into ``weight_communication_compression_amd/liblowbit.so``.
 """
 from __future__ import annotations
 
@@ -16,12 +16,14 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+CSRC_TRAIN = os.path.join(PKG, "csrc_train")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "liblowbit.so")
 
 SOURCES = ["api.cpp", "quantize_plain.hip", "quantize_ef.hip", "quantize_wdiff.hip",
            "quantize_ef21.hip", "quantize_hadamard.hip", "reduce.hip", "reduce_ef.hip", "reduce_mixed.hip",
-           "dequant.hip", "measure.hip"]
+           "dequant.hip", "measure.hip",
+           "../csrc_train/train_api.cpp", "../csrc_train/dropout.hip", "../csrc_train/join.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 
@@ -37,7 +39,7 @@ HIPFLAGS = [
 
 
 def _compile(src: str, extra: list[str], build_dir: str = BUILD) -> str:
-    obj = os.path.join(build_dir, os.path.splitext(src)[0] + ".o")
+    obj = os.path.join(build_dir, os.path.splitext(os.path.basename(src))[0] + ".o")
     cmd = [HIPCC, *HIPFLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -54,8 +56,9 @@ def build(force: bool = True, extra: list[str] | None = None, jobs: int | None =
     extra = list(extra or [])
     os.makedirs(build_dir, exist_ok=True)
     if not force and os.path.exists(out):
-        newest = max(os.path.getmtime(os.path.join(CSRC, f)) for f in os.listdir(CSRC))
-        newest = max(newest, os.path.getmtime(os.path.join(ROOT, "include", "lowbit.h")))
+        newest = max(os.path.getmtime(os.path.join(d, f))
+                     for d in (CSRC, CSRC_TRAIN, os.path.join(ROOT, "include"))
+                     for f in os.listdir(d))
         if os.path.getmtime(out) >= newest:
             return out
     jobs = jobs or min(len(SOURCES), max(1, os.cpu_count() or 1))

@@ -1,7 +1,8 @@
-"""Thin ctypes binding of liblowbit (the C ABI in ``include/lowbit.h``).
+"""Thin ctypes binding of liblowbit (the C ABI in ``include/lowbit.h`` and, for
+the training-step operators, ``include/lowbit_train.h``).
 
-Argument marshalling only: every step of the codec runs in the gfx950 HIP
-kernels behind the C ABI.  torch is used for device memory (tensors) and for
+Argument marshalling only: every step runs in the gfx950 HIP kernels behind the
+C ABI.  torch is used for device memory (tensors) and for
 the current HIP stream.  If the library is missing or a call fails, a
 ``LowbitError`` is raised -- there is no CPU fallback.
 
@@ -13,7 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -21,6 +22,8 @@ __all__ = [
     "LowbitError", "lib", "library_path", "num_words", "num_blocks", "QParams",
     "quantize_pack", "unpack_dequant", "ef_compress", "reduce_requant",
     "wdiff_compress", "wdiff_apply", "copy_f32", "xor_streams", "add_inplace_f32", "fold_f32",
+    "dropout", "dropout_backward", "block_join", "block_join_backward", "BlockJoin",
+    "BlockJoinGrads", "JoinParams",
     "stream_probe", "PROBE_READ", "PROBE_WRITE", "PROBE_COPY",
     "OK", "EINVAL", "EUNSUPPORTED", "EDEVICE", "F32", "BF16", "HINT_INPUT_REUSED",
 ]
@@ -49,6 +52,16 @@ class QParams(ctypes.Structure):
                 ("seed", ctypes.c_uint64), ("index_offset", ctypes.c_uint64)]
 
 
+class JoinParams(ctypes.Structure):
+    """lowbit_join_params"""
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("rows_per_gate", ctypes.c_int64), ("norm", ctypes.c_int32),
+                ("block_type", ctypes.c_int32), ("stream_type", ctypes.c_int32),
+                ("param_type", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("p", ctypes.c_double),
+                ("seed", ctypes.c_uint64)]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -60,7 +73,8 @@ def lib() -> ctypes.CDLL:
             raise LowbitError(-1, f"{library_path} is not built (run __graft_entry__.build())")
         L = ctypes.CDLL(library_path)
         P, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
-        QP = ctypes.POINTER(QParams)
+        f64, u64 = ctypes.c_double, ctypes.c_uint64
+        QP, JP = ctypes.POINTER(QParams), ctypes.POINTER(JoinParams)
         sigs = {
             "lowbit_num_words": (i64, [i64, i32]),
             "lowbit_num_blocks": (i64, [i64, i32]),
@@ -80,6 +94,11 @@ def lib() -> ctypes.CDLL:
             "lowbit_xor_streams_u32": (ctypes.c_int, [P, i32, i64, P, P]),
             "lowbit_add_inplace_f32": (ctypes.c_int, [P, P, i64, P]),
             "lowbit_fold_f32": (ctypes.c_int, [P, i64, i32, P, P]),
+            "lowbit_dropout": (ctypes.c_int, [P, P, ctypes.c_int, i64, f64, u64, u64, P, P]),
+            "lowbit_dropout_backward": (ctypes.c_int, [P, ctypes.c_int, i64, f64, u64, u64, P, P]),
+            "lowbit_block_join": (ctypes.c_int, [P] * 7 + [JP] + [P] * 4),
+            "lowbit_block_join_backward_workspace": (i64, [JP]),
+            "lowbit_block_join_backward": (ctypes.c_int, [P] * 9 + [JP] + [P] * 8 + [i64, P]),
             "lowbit_stream_probe_u32": (ctypes.c_int, [i32, P, P, i64, ctypes.c_uint32, i32, i32, P]),
         }
         for name, (res, args) in sigs.items():
@@ -442,3 +461,180 @@ def stream_probe(op: int, dst: torch.Tensor, src: Optional[torch.Tensor] = None,
                                          int(value) & 0xFFFFFFFF, int(waves), int(bool(nontemporal)),
                                          _stream(dst)), "lowbit_stream_probe_u32")
     return dst
+
+
+# ------------------------------------------------ training-step operators --
+_U64 = 2 ** 64 - 1
+_NORMS = {"rms": 0, "layer": 1}
+
+
+def _opt(t: Optional[torch.Tensor], what: str) -> Optional[int]:
+    return None if t is None else _dev(t, what)
+
+
+def _out_like(t: torch.Tensor, out: Optional[torch.Tensor], what: str) -> torch.Tensor:
+    if out is None:
+        return torch.empty_like(t)
+    if out.dtype != t.dtype or out.numel() != t.numel() or out.device != t.device:
+        raise LowbitError(EINVAL, f"{what} must match the input in dtype, size and device")
+    return out
+
+
+def _scratch(nbytes: int, like: torch.Tensor, workspace: Optional[torch.Tensor], what: str):
+    """The workspace given, or one of nbytes from torch's allocator."""
+    if nbytes < 0:
+        raise LowbitError(EINVAL, what)
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if workspace.dtype != torch.uint8 or workspace.numel() < nbytes \
+            or workspace.device != like.device:
+        raise LowbitError(EINVAL, f"workspace must be uint8 with >= {nbytes} elements")
+    return workspace
+
+
+def dropout(x: torch.Tensor, p: float, seed: int, residual: Optional[torch.Tensor] = None,
+            index_offset: int = 0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """residual + D(x) (or D(x)) of float32 or bfloat16 tensors: elements are
+    dropped with probability p, rounded to a multiple of 2^-16, by a mask that
+    seed alone fixes and that is never stored; the others are divided by 1 - p.
+
+    index_offset (a multiple of 8): the mask's index of element 0, for a tensor
+    that is a piece of a larger one.  `out` may be x or residual."""
+    if residual is not None and (residual.dtype != x.dtype or residual.numel() != x.numel()
+                                 or residual.device != x.device):
+        raise LowbitError(EINVAL, "residual must match x in dtype, size and device")
+    dt = _dtype_code(x)
+    out = _out_like(x, out, "out")
+    _check(lib().lowbit_dropout(_dev(x, "x"), _opt(residual, "residual"), dt, x.numel(), p,
+                                int(seed) & _U64, int(index_offset), _dev(out, "out"), _stream(x)),
+           "lowbit_dropout")
+    return out
+
+
+def dropout_backward(dy: torch.Tensor, p: float, seed: int, index_offset: int = 0,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of `dropout` by x, with its p, seed and index_offset: D(dy).
+    (The residual's gradient is dy.)  `out` may be dy."""
+    dt = _dtype_code(dy)
+    out = _out_like(dy, out, "out")
+    _check(lib().lowbit_dropout_backward(_dev(dy, "dy"), dt, dy.numel(), p, int(seed) & _U64,
+                                         int(index_offset), _dev(out, "out"), _stream(dy)),
+           "lowbit_dropout_backward")
+    return out
+
+
+class BlockJoin(NamedTuple):
+    """What block_join returns; stats is float32 (rows, 4)."""
+    x_out: torch.Tensor
+    z: torch.Tensor
+    stats: torch.Tensor
+
+
+class BlockJoinGrads(NamedTuple):
+    """What block_join_backward returns; the parameters' gradients are float32,
+    None for parameters that were not given."""
+    df: torch.Tensor
+    dx: torch.Tensor
+    dpost_weight: Optional[torch.Tensor]
+    dpost_bias: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+    dpre_weight: Optional[torch.Tensor]
+    dpre_bias: Optional[torch.Tensor]
+
+
+def _join_params(f, x, named, rows_per_gate, norm, residual_scale, eps, p, seed) -> JoinParams:
+    """Checks of the tensors' types and sizes, which the C ABI cannot see."""
+    if f.dim() < 1 or f.shape != x.shape:
+        raise LowbitError(EINVAL, "f and x must have the same shape, (..., columns)")
+    cols = f.shape[-1]
+    rows = f.numel() // cols if cols else 0
+    if norm not in _NORMS:
+        raise LowbitError(EINVAL, "norm must be 'rms' or 'layer'")
+    pt = None
+    for name, t in named:
+        if t is None:
+            continue
+        if t.device != f.device or (pt is not None and t.dtype != pt):
+            raise LowbitError(EINVAL, "weights, biases and gate must have one dtype and f's device")
+        pt = t.dtype
+        want = cols
+        if name == "gate":
+            if rows_per_gate < 1:
+                raise LowbitError(EINVAL, "a gate needs rows_per_gate >= 1")
+            want = -(-rows // rows_per_gate) * cols
+        if t.numel() != want:
+            raise LowbitError(EINVAL, f"{name} must have {want} elements")
+    if x.device != f.device:
+        raise LowbitError(EINVAL, "f and x must be on one device")
+    ft = _dtype_code(f)
+    return JoinParams(rows, cols, int(rows_per_gate), _NORMS[norm], ft, _dtype_code(x),
+                      ft if pt is None else (F32 if pt == torch.float32 else
+                                             BF16 if pt == torch.bfloat16 else -1),
+                      eps, residual_scale, p, int(seed) & _U64)
+
+
+def block_join(f: torch.Tensor, x: torch.Tensor, post_weight: Optional[torch.Tensor] = None,
+               post_bias: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+               rows_per_gate: int = 0, pre_weight: Optional[torch.Tensor] = None,
+               pre_bias: Optional[torch.Tensor] = None, norm: str = "rms",
+               residual_scale: float = 1.0, eps: float = 1e-6, p: float = 0.0, seed: int = 0,
+               x_out: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None) -> BlockJoin:
+    """What stands between two blocks of a residual network, in one pass:
+
+        x_out = residual_scale * x + gate * D(norm(f) * post_weight + post_bias)
+        z     = norm(x_out) * pre_weight + pre_bias
+
+    f (..., columns): a block's output; x: the residual stream, of f's dtype or
+    float32; z: the next block's input, of f's dtype.  Weights and biases
+    (columns), gate (ceil(rows / rows_per_gate), columns): of f's dtype or
+    float32, all the same; absent ones are 1 and 0.  norm: "rms" or "layer".
+    p, seed: dropout as by `dropout`, each row beginning at an even draw.
+    `x_out` may be x, `z` may be f.  stats feeds block_join_backward."""
+    named = (("post_weight", post_weight), ("post_bias", post_bias), ("gate", gate),
+             ("pre_weight", pre_weight), ("pre_bias", pre_bias))
+    q = _join_params(f, x, named, rows_per_gate, norm, residual_scale, eps, p, seed)
+    x_out = _out_like(x, x_out, "x_out")
+    z = _out_like(f, z, "z")
+    stats = torch.empty(q.rows, 4, dtype=torch.float32, device=f.device)
+    _check(lib().lowbit_block_join(_dev(f, "f"), _dev(x, "x"), *[_opt(t, n) for n, t in named], q,
+                                   _dev(x_out, "x_out"), _dev(z, "z"), _dev(stats, "stats"),
+                                   _stream(f)), "lowbit_block_join")
+    return BlockJoin(x_out, z, stats)
+
+
+def block_join_backward(dx_out: torch.Tensor, dz: torch.Tensor, f: torch.Tensor,
+                        x_out: torch.Tensor, stats: torch.Tensor,
+                        post_weight: Optional[torch.Tensor] = None,
+                        post_bias: Optional[torch.Tensor] = None,
+                        gate: Optional[torch.Tensor] = None, rows_per_gate: int = 0,
+                        pre_weight: Optional[torch.Tensor] = None,
+                        pre_bias: Optional[torch.Tensor] = None, norm: str = "rms",
+                        residual_scale: float = 1.0, eps: float = 1e-6, p: float = 0.0,
+                        seed: int = 0, df: Optional[torch.Tensor] = None,
+                        dx: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None) -> BlockJoinGrads:
+    """Gradients of `block_join` from those of x_out and z, with the forward
+    call's f, x_out, stats and options.  `df` may be dz, `dx` may be dx_out."""
+    named = (("post_weight", post_weight), ("post_bias", post_bias), ("gate", gate),
+             ("pre_weight", pre_weight), ("pre_bias", pre_bias))
+    q = _join_params(f, x_out, named, rows_per_gate, norm, residual_scale, eps, p, seed)
+    for t, like, what in ((dx_out, x_out, "dx_out"), (dz, f, "dz")):
+        if t.dtype != like.dtype or t.numel() != like.numel() or t.device != f.device:
+            raise LowbitError(EINVAL, f"{what} does not match the forward call")
+    if stats.dtype != torch.float32 or stats.numel() != 4 * q.rows or stats.device != f.device:
+        raise LowbitError(EINVAL, "stats must be the forward call's")
+    df = _out_like(f, df, "df")
+    dx = _out_like(x_out, dx, "dx")
+    grads = [None if t is None else torch.empty(t.shape, dtype=torch.float32, device=f.device)
+             for _, t in named]
+    L = lib()
+    nbytes = L.lowbit_block_join_backward_workspace(q)
+    if nbytes < 0 and q.cols > 16384:
+        raise LowbitError(EUNSUPPORTED, "block_join_backward: more than 16384 columns")
+    ws = _scratch(nbytes, f, workspace, "block_join_backward")
+    _check(L.lowbit_block_join_backward(
+        _dev(dx_out, "dx_out"), _dev(dz, "dz"), _dev(f, "f"), _dev(x_out, "x_out"),
+        _dev(stats, "stats"), *[_opt(t, n) for n, t in named[:4]], q, _dev(df, "df"),
+        _dev(dx, "dx"), *[None if g is None else g.data_ptr() for g in grads],
+        _dev(ws, "workspace"), ws.numel(), _stream(f)), "lowbit_block_join_backward")
+    return BlockJoinGrads(df, dx, *grads)
