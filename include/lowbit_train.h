@@ -8,6 +8,8 @@
  *   block join   : between two blocks of a residual network,
  *                      x_out = a x + gate * D(norm(f)),  z = norm(x_out),
  *                  and its gradient
+ *   linear xent  : softmax cross entropy of x w^T over a large vocabulary
+ *                  without keeping the logits, and its gradient
  *
  * The mask.  Element i of a buffer (for a matrix of `cols` columns, row r's
  * column c counts as i = r * (cols + cols mod 2) + c) belongs to pair i / 2,
@@ -118,6 +120,50 @@ lowbit_status lowbit_block_join_backward(const void* dx_out, const void* dz, con
                                          float* dpost_weight, float* dpost_bias, float* dgate,
                                          float* dpre_weight, float* dpre_bias, void* workspace,
                                          int64_t workspace_bytes, hipStream_t stream);
+
+typedef struct {
+    int64_t rows;             /* tokens, up to 2^31 - 1                        */
+    int64_t vocab;            /* 1 .. 2^31 - 1                                 */
+    int64_t hidden;           /* 1 .. 2^20                                     */
+    int64_t ignore_index;     /* rows with this target are left out            */
+    int32_t type;             /* lowbit_dtype of x, w and their gradients      */
+} lowbit_xent_params;
+
+/* Bytes of workspace that the forward (backward = 0) or the backward call
+ * (backward = 1) needs, or -1 for invalid params. */
+int64_t lowbit_linear_xent_workspace(const lowbit_xent_params* p, int32_t backward);
+
+/*
+ * Softmax cross entropy of the logits l = x w^T:
+ *     lse[r] = log sum_v exp(l[r, v]),   loss[r] = lse[r] - l[r, targets[r]]
+ * and 0 for both in rows that are left out.  A target outside [0, vocab) that
+ * is not ignore_index gives NaN for both.
+ *   x : rows x hidden;  w : vocab x hidden;  targets : rows int64
+ *   loss, lse : rows binary32 (written)
+ * Logits are binary32 sums of exact products.
+ * EINVAL: p == NULL, a size or type outside its range, NULL or misaligned
+ * pointer with rows > 0, workspace too small.
+ */
+lowbit_status lowbit_linear_xent(const void* x, const void* w, const int64_t* targets,
+                                 const lowbit_xent_params* p, float* loss, float* lse,
+                                 void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Its gradient, from the forward call's lse and the gradients of loss and lse
+ * (dlse NULL: zero; one is there for losses that use lse, as mean(lse^2)).  With
+ *     d[r, v] = exp(l[r, v] - lse[r]) (dloss[r] + dlse[r]) - dloss[r] [v = targets[r]]
+ * it gives  dx = d w  and  dw = d^T x; d is formed in pieces of the vocabulary in
+ * the workspace.  For LOWBIT_BF16 d is kept there in bfloat16, scaled so that
+ * the largest |dloss| counts as 1.  Rows that are left out give dx = 0 and add
+ * nothing to dw; a target out of range gives NaN.
+ *   dx : rows x hidden, dw : vocab x hidden, of type p->type; either may be NULL
+ *        and is then not computed.  rows == 0 still writes dw (zeros).
+ */
+lowbit_status lowbit_linear_xent_backward(const void* x, const void* w, const int64_t* targets,
+                                          const float* lse, const float* dloss, const float* dlse,
+                                          const lowbit_xent_params* p, void* dx, void* dw,
+                                          void* workspace, int64_t workspace_bytes,
+                                          hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -137,10 +137,69 @@ def test_join_refusals():
     assert _join_back(_params(rows=0), ptr=None, ws=None, nbytes=0, dw=None) == L.OK
 
 
+def _xp(**kw):
+    d = dict(rows=10, vocab=100, hidden=64, ignore_index=-100, type=1)
+    d.update(kw)
+    return L.XentParams(**d)
+
+
+def _xent(q, x=OK16, w=OK16, t=OK16, loss=OK16, lse=OK16, ws=OK16, nbytes=1 << 40):
+    return L.lib().lowbit_linear_xent(x, w, t, q, loss, lse, ws, nbytes, None)
+
+
+def _xent_back(q, x=OK16, w=OK16, t=OK16, lse=OK16, dloss=OK16, dlse=None, dx=OK16, dw=OK16,
+               ws=OK16, nbytes=1 << 40):
+    return L.lib().lowbit_linear_xent_backward(x, w, t, lse, dloss, dlse, q, dx, dw, ws, nbytes,
+                                               None)
+
+
+@pytest.mark.parametrize("bad", [dict(rows=-1), dict(rows=2 ** 31), dict(vocab=0),
+                                 dict(vocab=2 ** 31), dict(hidden=0), dict(hidden=2 ** 20 + 1),
+                                 dict(type=2), dict(type=-1)], ids=str)
+def test_xent_refuses_options(bad):
+    q = _xp(**bad)
+    assert _xent(q) == L.EINVAL and _xent_back(q) == L.EINVAL
+    assert L.lib().lowbit_linear_xent_workspace(q, 0) == -1
+    assert L.lib().lowbit_linear_xent_workspace(q, 1) == -1
+
+
+def test_xent_refusals():
+    assert _xent(None) == L.EINVAL and _xent_back(None) == L.EINVAL
+    assert L.lib().lowbit_linear_xent_workspace(None, 0) == -1
+    q = _xp()
+    for name in ("x", "w", "loss", "lse", "ws"):
+        assert _xent(q, **{name: None}) == L.EINVAL, name
+        assert _xent(q, **{name: OFF}) == L.EINVAL, name
+    odd = ctypes.c_void_p(0x1004)
+    assert _xent(q, t=None) == L.EINVAL and _xent(q, t=odd) == L.EINVAL
+    for name in ("x", "w", "lse", "dloss", "ws"):
+        assert _xent_back(q, **{name: None}) == L.EINVAL, name
+        assert _xent_back(q, **{name: OFF}) == L.EINVAL, name
+    for name in ("dlse", "dx", "dw"):
+        assert _xent_back(q, **{name: OFF}) == L.EINVAL, name
+    assert _xent_back(q, t=odd) == L.EINVAL
+    for back, call in ((0, _xent), (1, _xent_back)):
+        need = L.lib().lowbit_linear_xent_workspace(q, back)
+        assert need > 0 and call(q, nbytes=need - 1) == L.EINVAL
+    assert _xent(_xp(rows=0), x=None, t=None, loss=None, lse=None, ws=None) == L.OK
+    assert _xent_back(q, dx=None, dw=None, w=None) == L.OK          # nothing asked for
+    assert _xent_back(_xp(rows=0), dw=None, w=None, x=None) == L.OK
+
+
+def test_xent_workspace_stays_far_below_the_logits():
+    for rows, vocab in ((8192, 50257), (65536, 131072), (1 << 20, 1 << 18)):
+        need = L.lib().lowbit_linear_xent_workspace(_xp(rows=rows, vocab=vocab, hidden=4096), 1)
+        row_copies = rows * 4096 * (2 + 4)
+        assert need < (600 << 20) + max(row_copies, 2 * rows * 1024) + rows * 2100
+        assert need < rows * vocab * 4
+        need = L.lib().lowbit_linear_xent_workspace(_xp(rows=rows, vocab=vocab, hidden=4096), 0)
+        assert need < rows * 4096 * 2 + rows * vocab // 8 + (1 << 20) + rows * 64
+
+
 def test_binding_refuses():
     """Tensors that do not fit, on the host: no launch."""
     f = torch.zeros(4, 8)
-    w = torch.zeros(8)
+    w, t4 = torch.zeros(8), torch.zeros(4, dtype=torch.int64)
     for call in (lambda: L.dropout(f, 0.1, 1),                              # host tensor
                  lambda: L.dropout(f.half(), 0.1, 1),                       # type
                  lambda: L.dropout(f, 0.1, 1, residual=torch.zeros(31)),
@@ -158,6 +217,16 @@ def test_binding_refuses():
                  lambda: L.block_join_backward(f, f.bfloat16(), f, f, torch.zeros(4, 4)),
                  lambda: L.block_join_backward(f, f, f, f, torch.zeros(4, 3)),
                  lambda: L.block_join_backward(f, f, f, f, torch.zeros(4, 4),
-                                               workspace=torch.zeros(3, dtype=torch.uint8))):
+                                               workspace=torch.zeros(3, dtype=torch.uint8)),
+                 lambda: L.linear_xent(f, torch.zeros(5, 8), t4),                       # host
+                 lambda: L.linear_xent(f, torch.zeros(5, 7), t4),
+                 lambda: L.linear_xent(f, torch.zeros(5, 8).bfloat16(), t4),
+                 lambda: L.linear_xent(f, torch.zeros(5, 8), t4.int()),
+                 lambda: L.linear_xent(f, torch.zeros(5, 8), t4[:3]),
+                 lambda: L.linear_xent(f.half(), torch.zeros(5, 8).half(), t4),
+                 lambda: L.linear_xent_backward(f, torch.zeros(5, 8), t4, t4, w[:4]),
+                 lambda: L.linear_xent_backward(f, torch.zeros(5, 8), t4, w[:4], w[:3]),
+                 lambda: L.linear_xent_backward(f, torch.zeros(5, 8), t4, w[:4], w[:4],
+                                                dx=torch.zeros(4, 7))):
         with pytest.raises(L.LowbitError):
             call()

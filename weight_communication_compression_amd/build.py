@@ -23,7 +23,8 @@ LIB = os.path.join(PKG, "liblowbit.so")
 SOURCES = ["api.cpp", "quantize_plain.hip", "quantize_ef.hip", "quantize_wdiff.hip",
            "quantize_ef21.hip", "quantize_hadamard.hip", "reduce.hip", "reduce_ef.hip", "reduce_mixed.hip",
            "dequant.hip", "measure.hip",
-           "../csrc_train/train_api.cpp", "../csrc_train/dropout.hip", "../csrc_train/join.hip"]
+           "../csrc_train/train_api.cpp", "../csrc_train/dropout.hip", "../csrc_train/join.hip",
+           "../csrc_train/xent_rows.hip", "../csrc_train/xent_tile.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 

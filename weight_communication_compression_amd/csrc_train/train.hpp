@@ -68,4 +68,72 @@ lowbit_status launch_join_back(int ft, int st, int pt, bool layer, const JoinSha
                                const JoinBackArgs& a, hipStream_t s);
 lowbit_status launch_join_sums(const JoinSumArgs& a, hipStream_t s);
 
+// ---------------------------------------------------------- linear xent --
+// The rows that count are taken together: compact row i stands for row map[i].
+struct XentRows {
+  const int64_t* targets;
+  const float *lse, *dloss, *dlse;   // backward; dlse may be null
+  int64_t n, vocab, ignore;
+  int32_t* pos;              // n: compact row of a row, or -1
+  int32_t* map;              // padded rows: row of a compact row, or -1
+  // padded rows: lse, dloss + dlse, dloss, target (bits; -1: none); zeros beyond
+  // the rows that count
+  float4* info;
+  int32_t* count;            // how many count
+  float* scale;              // the largest finite |dloss| or |dloss + dlse|, or 1
+  int64_t padded;
+};
+
+struct XentGather {
+  const void* x;
+  void* xc;                  // compact rows, zeros beyond the count
+  void* dx;                  // backward: rows that are left out are set to 0; may be null
+  const int32_t *pos, *map, *count;
+  int64_t n, padded;
+  int32_t hidden, ld;        // of x and dx; of xc
+};
+
+struct XentJoin {
+  const float2* part;        // compact row x parts: maximum, sum of exp(l - maximum)
+  const float* hit;          // the target's logit
+  const int64_t* targets;
+  const int32_t* pos;
+  int64_t n, vocab;
+  int32_t parts;
+  float *loss, *lse;
+};
+
+// A product of the loss: C[m, n] = sum_k A[m, k] B[n, k].
+enum XentKind : int {
+  kXentStats = 0,            // logits -> parts of the softmax
+  kXentProb = 1,             // logits -> d, a piece of the vocabulary
+  kXentDx = 2,               // dx += d w
+  kXentDw = 3,               // dw = d^T x
+};
+
+struct XentTileArgs {
+  const void *a, *b;         // a[m lda + k], or a[k lda + m] where the kind has it so
+  int64_t lda, ldb;
+  int64_t m, n, k;           // m, n of the output, k summed over; a dimension of
+                             // rows is the padded count, cut to the real one
+  const int32_t* count;
+  const int32_t* map;
+  const float4* info;
+  const float* scale;
+  int64_t col0;              // vocabulary column of n = 0 (logits)
+  float2* part;
+  float* hit;
+  int32_t parts;
+  void* out;                 // d, dx or dw
+  int64_t ldo;
+  float* acc;                // dx over several pieces: their sum so far
+  int32_t first, last;       // piece of the vocabulary
+};
+
+lowbit_status launch_xent_rows(const XentRows& a, hipStream_t s);
+lowbit_status launch_xent_gather(int dt, const XentGather& a, hipStream_t s);
+lowbit_status launch_xent_join(const XentJoin& a, hipStream_t s);
+lowbit_status launch_xent_tile(int dt, int kind, const XentTileArgs& a, hipStream_t s);
+constexpr int kXentTile = 128;   // of the tile kernel, both ways
+
 }  // namespace lowbit

@@ -91,6 +91,102 @@ int64_t join_part_bytes(const JoinShape& g, int64_t cols, int rows_each) {
   return (g.blocks * rows_each * cols * 4 + 255) / 256 * 256;
 }
 
+constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1, kMaxHidden = (int64_t)1 << 20;
+// d of a piece of the vocabulary takes at most this much, so that the loss
+// needs far less than its logits; all of the vocabulary in one piece where it fits
+constexpr int64_t kXentPieceBytes = (int64_t)512 << 20;
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+bool check_xent(const lowbit_xent_params* p) {
+  return p && p->rows >= 0 && p->rows <= kMaxRows && p->vocab >= 1 && p->vocab <= kMaxRows &&
+         p->hidden >= 1 && p->hidden <= kMaxHidden && valid_dtype(p->type);
+}
+
+// Offsets into the workspace.
+struct XentPlan {
+  int64_t padded, ld, parts, piece, pieces;
+  int64_t pos, map, info, count, xc, part, hit, d, acc, bytes;
+};
+
+XentPlan xent_plan(const lowbit_xent_params* p, bool backward) {
+  XentPlan w{};
+  const int64_t es = p->type == LOWBIT_F32 ? 4 : 2;
+  auto take = [&](int64_t bytes) {
+    const int64_t at = w.bytes;
+    w.bytes += up(bytes, 256);
+    return at;
+  };
+  w.padded = up(p->rows > 0 ? p->rows : 1, kXentTile);
+  w.ld = up(p->hidden, 8);
+  w.pos = take(p->rows * 4);
+  w.map = take(w.padded * 4);
+  w.info = take(w.padded * 16);
+  w.count = take(8);                       // and the scale
+  w.xc = take(w.padded * w.ld * es);
+  if (backward) {
+    int64_t most = kXentPieceBytes / (w.padded * es) / kXentTile * kXentTile;
+    if (most < 8 * kXentTile) most = 8 * kXentTile;
+    w.pieces = (p->vocab + most - 1) / most;
+    w.piece = up((p->vocab + w.pieces - 1) / w.pieces, kXentTile);
+    w.pieces = (p->vocab + w.piece - 1) / w.piece;
+    w.d = take(w.padded * w.piece * es);
+    if (w.pieces > 1) w.acc = take(w.padded * p->hidden * 4);
+  } else {
+    w.parts = (p->vocab + kXentTile - 1) / kXentTile;
+    w.part = take(w.padded * w.parts * 8);
+    w.hit = take(w.padded * 4);
+  }
+  return w;
+}
+
+template <typename T>
+T* at(void* base, int64_t offset) {
+  return reinterpret_cast<T*>(static_cast<char*>(base) + offset);
+}
+
+// Numbers the rows that count and copies them together.
+lowbit_status xent_rows(const XentPlan& w, const lowbit_xent_params* p, void* ws, const void* x,
+                        const int64_t* targets, const float* lse, const float* dloss,
+                        const float* dlse, void* dx, hipStream_t s) {
+  XentRows r{};
+  r.targets = targets;
+  r.lse = lse;
+  r.dloss = dloss;
+  r.dlse = dlse;
+  r.n = p->rows;
+  r.vocab = p->vocab;
+  r.ignore = p->ignore_index;
+  r.pos = at<int32_t>(ws, w.pos);
+  r.map = at<int32_t>(ws, w.map);
+  r.info = at<float4>(ws, w.info);
+  r.count = at<int32_t>(ws, w.count);
+  r.scale = at<float>(ws, w.count + 4);
+  r.padded = w.padded;
+  const lowbit_status st = launch_xent_rows(r, s);
+  if (st != LOWBIT_OK) return st;
+  XentGather g{};
+  g.x = x;
+  g.xc = at<char>(ws, w.xc);
+  g.dx = dx;
+  g.pos = r.pos;
+  g.map = r.map;
+  g.n = p->rows;
+  g.padded = w.padded;
+  g.hidden = (int32_t)p->hidden;
+  g.ld = (int32_t)w.ld;
+  return launch_xent_gather(p->type, g, s);
+}
+
+XentTileArgs xent_tile(const XentPlan& w, void* ws) {
+  XentTileArgs t{};
+  t.count = at<int32_t>(ws, w.count);
+  t.scale = at<float>(ws, w.count + 4);
+  t.map = at<int32_t>(ws, w.map);
+  t.info = at<float4>(ws, w.info);
+  return t;
+}
+
 }  // namespace
 
 }  // namespace lowbit
@@ -209,6 +305,111 @@ lowbit_status lowbit_block_join_backward(const void* dx_out, const void* dz, con
   const lowbit_status st = launch_join_back(p->block_type, p->stream_type, p->param_type,
                                             p->norm == LOWBIT_NORM_LAYER, g, b, stream);
   return st == LOWBIT_OK ? launch_join_sums(sums, stream) : st;
+}
+
+int64_t lowbit_linear_xent_workspace(const lowbit_xent_params* p, int32_t backward) {
+  return check_xent(p) ? xent_plan(p, backward != 0).bytes : -1;
+}
+
+lowbit_status lowbit_linear_xent(const void* x, const void* w, const int64_t* targets,
+                                 const lowbit_xent_params* p, float* loss, float* lse,
+                                 void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  if (!check_xent(p)) return LOWBIT_EINVAL;
+  if (p->rows == 0) return LOWBIT_OK;
+  if (!good(x) || !good(w) || !targets || !aligned(targets, 8) || !good(loss) || !good(lse))
+    return LOWBIT_EINVAL;
+  const XentPlan q = xent_plan(p, false);
+  if (!good(workspace) || workspace_bytes < q.bytes) return LOWBIT_EINVAL;
+  lowbit_status st =
+      xent_rows(q, p, workspace, x, targets, nullptr, nullptr, nullptr, nullptr, stream);
+  if (st != LOWBIT_OK) return st;
+  XentTileArgs t = xent_tile(q, workspace);
+  t.a = at<char>(workspace, q.xc);
+  t.lda = q.ld;
+  t.b = w;
+  t.ldb = p->hidden;
+  t.m = q.padded;
+  t.n = p->vocab;
+  t.k = p->hidden;
+  t.part = at<float2>(workspace, q.part);
+  t.hit = at<float>(workspace, q.hit);
+  t.parts = (int32_t)q.parts;
+  st = launch_xent_tile(p->type, kXentStats, t, stream);
+  if (st != LOWBIT_OK) return st;
+  XentJoin j{};
+  j.part = t.part;
+  j.hit = t.hit;
+  j.targets = targets;
+  j.pos = at<int32_t>(workspace, q.pos);
+  j.n = p->rows;
+  j.vocab = p->vocab;
+  j.parts = t.parts;
+  j.loss = loss;
+  j.lse = lse;
+  return launch_xent_join(j, stream);
+}
+
+lowbit_status lowbit_linear_xent_backward(const void* x, const void* w, const int64_t* targets,
+                                          const float* lse, const float* dloss, const float* dlse,
+                                          const lowbit_xent_params* p, void* dx, void* dw,
+                                          void* workspace, int64_t workspace_bytes,
+                                          hipStream_t stream) {
+  if (!check_xent(p)) return LOWBIT_EINVAL;
+  if (!good_or_null(dx) || !good_or_null(dw)) return LOWBIT_EINVAL;
+  if (!dw && (!dx || p->rows == 0)) return LOWBIT_OK;
+  if (p->rows > 0 && (!good(x) || !targets || !aligned(targets, 8) || !good(lse) ||
+                      !good(dloss) || !good_or_null(dlse)))
+    return LOWBIT_EINVAL;
+  const XentPlan q = xent_plan(p, true);
+  if (!good(w) || !good(workspace) || workspace_bytes < q.bytes) return LOWBIT_EINVAL;
+  lowbit_status st = xent_rows(q, p, workspace, x, targets, lse, dloss, dlse, dx, stream);
+  const int64_t es = p->type == LOWBIT_F32 ? 4 : 2;
+  for (int64_t k = 0; k < q.pieces && st == LOWBIT_OK; ++k) {
+    const int64_t col0 = k * q.piece;
+    const int64_t cols = col0 + q.piece < p->vocab ? q.piece : p->vocab - col0;
+    XentTileArgs t = xent_tile(q, workspace);
+    char* const xc = at<char>(workspace, q.xc);
+    char* const d = at<char>(workspace, q.d);
+    const char* const wk = static_cast<const char*>(w) + col0 * p->hidden * es;
+    t.a = xc;
+    t.lda = q.ld;
+    t.b = wk;
+    t.ldb = p->hidden;
+    t.m = q.padded;
+    t.n = cols;
+    t.k = p->hidden;
+    t.col0 = col0;
+    t.out = d;
+    t.ldo = q.piece;
+    st = launch_xent_tile(p->type, kXentProb, t, stream);
+    if (st == LOWBIT_OK && dx) {
+      t.a = d;
+      t.lda = q.piece;
+      t.b = wk;
+      t.ldb = p->hidden;
+      t.n = p->hidden;
+      t.k = cols;
+      t.out = dx;
+      t.ldo = p->hidden;
+      t.acc = q.pieces > 1 ? at<float>(workspace, q.acc) : nullptr;
+      t.first = k == 0;
+      t.last = k == q.pieces - 1;
+      st = launch_xent_tile(p->type, kXentDx, t, stream);
+    }
+    if (st == LOWBIT_OK && dw) {
+      t.a = d;
+      t.lda = q.piece;
+      t.b = xc;
+      t.ldb = q.ld;
+      t.m = cols;
+      t.n = p->hidden;
+      t.k = q.padded;
+      t.out = static_cast<char*>(dw) + col0 * p->hidden * es;
+      t.ldo = p->hidden;
+      st = launch_xent_tile(p->type, kXentDw, t, stream);
+    }
+  }
+  return st;
 }
 
 }  // extern "C"

@@ -23,7 +23,8 @@ __all__ = [
     "quantize_pack", "unpack_dequant", "ef_compress", "reduce_requant",
     "wdiff_compress", "wdiff_apply", "copy_f32", "xor_streams", "add_inplace_f32", "fold_f32",
     "dropout", "dropout_backward", "block_join", "block_join_backward", "BlockJoin",
-    "BlockJoinGrads", "JoinParams",
+    "BlockJoinGrads", "JoinParams", "linear_xent", "linear_xent_backward", "LinearXent",
+    "LinearXentGrads", "XentParams",
     "stream_probe", "PROBE_READ", "PROBE_WRITE", "PROBE_COPY",
     "OK", "EINVAL", "EUNSUPPORTED", "EDEVICE", "F32", "BF16", "HINT_INPUT_REUSED",
 ]
@@ -62,6 +63,12 @@ class JoinParams(ctypes.Structure):
                 ("seed", ctypes.c_uint64)]
 
 
+class XentParams(ctypes.Structure):
+    """lowbit_xent_params"""
+    _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("hidden", ctypes.c_int64),
+                ("ignore_index", ctypes.c_int64), ("type", ctypes.c_int32)]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -75,6 +82,7 @@ def lib() -> ctypes.CDLL:
         P, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
         f64, u64 = ctypes.c_double, ctypes.c_uint64
         QP, JP = ctypes.POINTER(QParams), ctypes.POINTER(JoinParams)
+        XP = ctypes.POINTER(XentParams)
         sigs = {
             "lowbit_num_words": (i64, [i64, i32]),
             "lowbit_num_blocks": (i64, [i64, i32]),
@@ -99,6 +107,9 @@ def lib() -> ctypes.CDLL:
             "lowbit_block_join": (ctypes.c_int, [P] * 7 + [JP] + [P] * 4),
             "lowbit_block_join_backward_workspace": (i64, [JP]),
             "lowbit_block_join_backward": (ctypes.c_int, [P] * 9 + [JP] + [P] * 8 + [i64, P]),
+            "lowbit_linear_xent_workspace": (i64, [XP, i32]),
+            "lowbit_linear_xent": (ctypes.c_int, [P, P, P, XP, P, P, P, i64, P]),
+            "lowbit_linear_xent_backward": (ctypes.c_int, [P] * 6 + [XP] + [P] * 3 + [i64, P]),
             "lowbit_stream_probe_u32": (ctypes.c_int, [i32, P, P, i64, ctypes.c_uint32, i32, i32, P]),
         }
         for name, (res, args) in sigs.items():
@@ -638,3 +649,71 @@ def block_join_backward(dx_out: torch.Tensor, dz: torch.Tensor, f: torch.Tensor,
         _dev(dx, "dx"), *[None if g is None else g.data_ptr() for g in grads],
         _dev(ws, "workspace"), ws.numel(), _stream(f)), "lowbit_block_join_backward")
     return BlockJoinGrads(df, dx, *grads)
+
+
+class LinearXent(NamedTuple):
+    """What linear_xent returns: float32, one value for each row."""
+    loss: torch.Tensor
+    lse: torch.Tensor
+
+
+class LinearXentGrads(NamedTuple):
+    """What linear_xent_backward returns; None for what was not asked for."""
+    dx: Optional[torch.Tensor]
+    dw: Optional[torch.Tensor]
+
+
+def _xent_params(x, w, targets, ignore_index) -> XentParams:
+    if w.dim() != 2 or x.dim() < 1 or x.shape[-1] != w.shape[1]:
+        raise LowbitError(EINVAL, "x must be (..., hidden) and w (vocab, hidden)")
+    vocab, hidden = w.shape
+    rows = x.numel() // hidden if hidden else 0
+    if w.dtype != x.dtype or w.device != x.device or targets.device != x.device:
+        raise LowbitError(EINVAL, "x and w must match in dtype, x, w and targets in device")
+    if targets.dtype != torch.int64 or targets.numel() != rows:
+        raise LowbitError(EINVAL, "targets must be int64, one for each row of x")
+    return XentParams(rows, vocab, hidden, int(ignore_index), _dtype_code(x))
+
+
+def linear_xent(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
+                workspace: Optional[torch.Tensor] = None) -> LinearXent:
+    """Softmax cross entropy of the logits x w^T, which are not kept:
+    lse = logsumexp of a row's logits, loss = lse - the target's logit, each
+    float32 and of targets' shape; 0 where targets is ignore_index, NaN where
+    a target lies outside the vocabulary.
+
+    x (..., hidden), w (vocab, hidden): float32 or bfloat16; targets: int64.
+    Mean loss: loss.sum() / (targets != ignore_index).sum()."""
+    q = _xent_params(x, w, targets, ignore_index)
+    L = lib()
+    ws = _scratch(L.lowbit_linear_xent_workspace(q, 0), x, workspace, "linear_xent")
+    loss = torch.empty(targets.shape, dtype=torch.float32, device=x.device)
+    lse = torch.empty_like(loss)
+    _check(L.lowbit_linear_xent(_dev(x, "x"), _dev(w, "w"), _dev(targets, "targets"), q,
+                                loss.data_ptr(), lse.data_ptr(), _dev(ws, "workspace"), ws.numel(),
+                                _stream(x)), "lowbit_linear_xent")
+    return LinearXent(loss, lse)
+
+
+def linear_xent_backward(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
+                         lse: torch.Tensor, dloss: torch.Tensor,
+                         dlse: Optional[torch.Tensor] = None, ignore_index: int = -100,
+                         dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
+                         need_dx: bool = True, need_dw: bool = True,
+                         workspace: Optional[torch.Tensor] = None) -> LinearXentGrads:
+    """Gradients of `linear_xent` by x and w, from its lse and the gradients of
+    loss and (where the whole loss uses it) of lse, float32 for each row."""
+    q = _xent_params(x, w, targets, ignore_index)
+    for t, what in ((lse, "lse"), (dloss, "dloss"), (dlse, "dlse")):
+        if t is not None and (t.dtype != torch.float32 or t.numel() != q.rows
+                              or t.device != x.device):
+            raise LowbitError(EINVAL, f"{what} must be float32, one for each row of x")
+    dx = _out_like(x, dx, "dx") if need_dx else None
+    dw = _out_like(w, dw, "dw") if need_dw else None
+    L = lib()
+    ws = _scratch(L.lowbit_linear_xent_workspace(q, 1), x, workspace, "linear_xent_backward")
+    _check(L.lowbit_linear_xent_backward(
+        _dev(x, "x"), _dev(w, "w"), _dev(targets, "targets"), _dev(lse, "lse"),
+        _dev(dloss, "dloss"), _opt(dlse, "dlse"), q, _opt(dx, "dx"), _opt(dw, "dw"),
+        _dev(ws, "workspace"), ws.numel(), _stream(x)), "lowbit_linear_xent_backward")
+    return LinearXentGrads(dx, dw)
