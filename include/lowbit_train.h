@@ -122,7 +122,7 @@ lowbit_status lowbit_block_join_backward(const void* dx_out, const void* dz, con
                                          int64_t workspace_bytes, hipStream_t stream);
 
 typedef struct {
-    int64_t rows;             /* tokens, up to 2^31 - 1                        */
+    int64_t rows;             /* tokens, up to 2^30                            */
     int64_t vocab;            /* 1 .. 2^31 - 1                                 */
     int64_t hidden;           /* 1 .. 2^20                                     */
     int64_t ignore_index;     /* rows with this target are left out            */

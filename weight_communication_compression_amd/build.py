@@ -24,7 +24,8 @@ SOURCES = ["api.cpp", "quantize_plain.hip", "quantize_ef.hip", "quantize_wdiff.h
            "quantize_ef21.hip", "quantize_hadamard.hip", "reduce.hip", "reduce_ef.hip", "reduce_mixed.hip",
            "dequant.hip", "measure.hip",
            "../csrc_train/train_api.cpp", "../csrc_train/dropout.hip", "../csrc_train/join.hip",
-           "../csrc_train/xent_rows.hip", "../csrc_train/xent_tile.hip"]
+           "../csrc_train/xent_rows.hip", "../csrc_train/xent_tile_bf16.hip",
+           "../csrc_train/xent_tile_f32.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 

@@ -93,6 +93,14 @@ struct XentGather {
   int32_t hidden, ld;        // of x and dx; of xc
 };
 
+// Rows of w with a multiple of 16 bytes each, zeros at their ends.
+struct XentPack {
+  const void* w;
+  void* to;
+  int64_t rows;
+  int32_t hidden, ld;
+};
+
 struct XentJoin {
   const float2* part;        // compact row x parts: maximum, sum of exp(l - maximum)
   const float* hit;          // the target's logit
@@ -113,7 +121,7 @@ enum XentKind : int {
 
 struct XentTileArgs {
   const void *a, *b;         // a[m lda + k], or a[k lda + m] where the kind has it so
-  int64_t lda, ldb;
+  int64_t lda, ldb;          // multiples of 16 bytes
   int64_t m, n, k;           // m, n of the output, k summed over; a dimension of
                              // rows is the padded count, cut to the real one
   const int32_t* count;
@@ -123,17 +131,29 @@ struct XentTileArgs {
   int64_t col0;              // vocabulary column of n = 0 (logits)
   float2* part;
   float* hit;
-  int32_t parts;
+  int32_t parts, part0;      // of a row; the first of n = 0
   void* out;                 // d, dx or dw
   int64_t ldo;
   float* acc;                // dx over several pieces: their sum so far
+  int64_t ldacc;
   int32_t first, last;       // piece of the vocabulary
+  float* partial;            // sums of tiles that are cut along k (dx, dw)
 };
 
 lowbit_status launch_xent_rows(const XentRows& a, hipStream_t s);
 lowbit_status launch_xent_gather(int dt, const XentGather& a, hipStream_t s);
+lowbit_status launch_xent_pack(int dt, const XentPack& a, hipStream_t s);
 lowbit_status launch_xent_join(const XentJoin& a, hipStream_t s);
-lowbit_status launch_xent_tile(int dt, int kind, const XentTileArgs& a, hipStream_t s);
-constexpr int kXentTile = 128;   // of the tile kernel, both ways
+lowbit_status launch_xent_tile_bf16(int form, int kind, const XentTileArgs& a, hipStream_t s);
+lowbit_status launch_xent_tile_f32(int form, int kind, const XentTileArgs& a, hipStream_t s);
+
+// The tile kernels' forms: rows and columns of a tile, and how many of its
+// workgroups the chip holds at one time.
+struct XentForm {
+  int tm, tn, slots;
+};
+constexpr XentForm kXentForms[4] = {{256, 256, 256}, {128, 128, 512}, {64, 128, 768}, {32, 128, 1024}};
+constexpr int64_t kXentPad = 256;  // rows and pieces of the vocabulary: multiples of every tile's
+int xent_form(int dt, int kind, int64_t m, int64_t n);
 
 }  // namespace lowbit

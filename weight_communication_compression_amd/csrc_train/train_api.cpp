@@ -4,6 +4,7 @@
 // nothing here allocates device memory or keeps any state.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <stdint.h>
 
@@ -91,23 +92,40 @@ int64_t join_part_bytes(const JoinShape& g, int64_t cols, int rows_each) {
   return (g.blocks * rows_each * cols * 4 + 255) / 256 * 256;
 }
 
-constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1, kMaxHidden = (int64_t)1 << 20;
+constexpr int64_t kMaxRows = (int64_t)1 << 30, kMaxVocab = ((int64_t)1 << 31) - 1;
+constexpr int64_t kMaxHidden = (int64_t)1 << 20;
 // d of a piece of the vocabulary takes at most this much, so that the loss
 // needs far less than its logits; all of the vocabulary in one piece where it fits
 constexpr int64_t kXentPieceBytes = (int64_t)512 << 20;
+// copies of w's rows, where they are no multiples of 16 bytes; 64 Mi keep the
+// chip busy for several rounds of tiles in each piece
+constexpr int64_t kXentPackBytes = (int64_t)64 << 20;
+constexpr int64_t kXentTiles = (int64_t)1 << 22;       // of a launch, at most
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 bool check_xent(const lowbit_xent_params* p) {
-  return p && p->rows >= 0 && p->rows <= kMaxRows && p->vocab >= 1 && p->vocab <= kMaxRows &&
+  return p && p->rows >= 0 && p->rows <= kMaxRows && p->vocab >= 1 && p->vocab <= kMaxVocab &&
          p->hidden >= 1 && p->hidden <= kMaxHidden && valid_dtype(p->type);
 }
 
-// Offsets into the workspace.
+// The pieces of the vocabulary, and offsets into the workspace.
 struct XentPlan {
   int64_t padded, ld, parts, piece, pieces;
-  int64_t pos, map, info, count, xc, part, hit, d, acc, bytes;
+  bool packs;                              // w's rows are copied to rows of ld
+  int form[4];                             // of each kind of product, in every piece
+  int64_t pos, map, info, count, xc, wc, part, hit, d, acc, partial, bytes;
 };
+
+// Sums of the tiles that a product cuts along k: one tile for each slot, and
+// four steps of k for each part.
+int64_t xent_partial_bytes(int dt, const XentForm& f, int64_t m, int64_t n, int64_t k) {
+  const int64_t step = dt == LOWBIT_F32 ? 32 : 64, quarter = up(k, step) / step / 4;
+  const int64_t tiles = (m + f.tm - 1) / f.tm * ((n + f.tn - 1) / f.tn);
+  if (quarter < 2) return 0;
+  const int64_t slots = tiles < f.slots && tiles * quarter < f.slots ? tiles * quarter : f.slots;
+  return slots * f.tm * f.tn * 4;
+}
 
 XentPlan xent_plan(const lowbit_xent_params* p, bool backward) {
   XentPlan w{};
@@ -117,24 +135,40 @@ XentPlan xent_plan(const lowbit_xent_params* p, bool backward) {
     w.bytes += up(bytes, 256);
     return at;
   };
-  w.padded = up(p->rows > 0 ? p->rows : 1, kXentTile);
-  w.ld = up(p->hidden, 8);
+  w.padded = up(p->rows > 0 ? p->rows : 1, kXentPad);
+  w.ld = up(p->hidden, 16 / es);
+  w.packs = w.ld != p->hidden;
   w.pos = take(p->rows * 4);
   w.map = take(w.padded * 4);
   w.info = take(w.padded * 16);
   w.count = take(8);                       // and the scale
   w.xc = take(w.padded * w.ld * es);
+  int64_t most = up(p->vocab, kXentPad);
+  auto cut = [&](int64_t cols) {
+    if (cols < most) most = cols > kXentPad ? cols / kXentPad * kXentPad : kXentPad;
+  };
+  w.form[kXentStats] = xent_form(p->type, kXentStats, p->rows, p->vocab);
+  const XentForm& f = kXentForms[w.form[kXentStats]];
+  if (backward) cut(std::max(kXentPieceBytes / (w.padded * es), (int64_t)1024));
+  if (w.packs) cut(std::max(kXentPackBytes / (w.ld * es), (int64_t)1024));
+  cut(kXentTiles / (w.padded / f.tm) * f.tn);
+  w.pieces = (p->vocab + most - 1) / most;
+  w.piece = up((p->vocab + w.pieces - 1) / w.pieces, kXentPad);
+  w.pieces = (p->vocab + w.piece - 1) / w.piece;
+  if (w.packs) w.wc = take(w.piece * w.ld * es);
   if (backward) {
-    int64_t most = kXentPieceBytes / (w.padded * es) / kXentTile * kXentTile;
-    if (most < 8 * kXentTile) most = 8 * kXentTile;
-    w.pieces = (p->vocab + most - 1) / most;
-    w.piece = up((p->vocab + w.pieces - 1) / w.pieces, kXentTile);
-    w.pieces = (p->vocab + w.piece - 1) / w.piece;
     w.d = take(w.padded * w.piece * es);
-    if (w.pieces > 1) w.acc = take(w.padded * p->hidden * 4);
+    if (w.pieces > 1) w.acc = take(p->rows * w.ld * 4);
+    const int64_t cols = w.piece < p->vocab ? w.piece : p->vocab;
+    w.form[kXentProb] = xent_form(p->type, kXentProb, p->rows, cols);
+    w.form[kXentDx] = xent_form(p->type, kXentDx, p->rows, p->hidden);
+    w.form[kXentDw] = xent_form(p->type, kXentDw, cols, p->hidden);
+    w.partial = take(std::max(
+        xent_partial_bytes(p->type, kXentForms[w.form[kXentDx]], p->rows, p->hidden, cols),
+        xent_partial_bytes(p->type, kXentForms[w.form[kXentDw]], cols, p->hidden, p->rows)));
   } else {
-    w.parts = (p->vocab + kXentTile - 1) / kXentTile;
-    w.part = take(w.padded * w.parts * 8);
+    w.parts = (p->vocab + f.tn - 1) / f.tn;
+    w.part = take(p->rows * w.parts * 8);
     w.hit = take(w.padded * 4);
   }
   return w;
@@ -178,16 +212,50 @@ lowbit_status xent_rows(const XentPlan& w, const lowbit_xent_params* p, void* ws
   return launch_xent_gather(p->type, g, s);
 }
 
-XentTileArgs xent_tile(const XentPlan& w, void* ws) {
-  XentTileArgs t{};
+lowbit_status xent_product(const lowbit_xent_params* p, const XentPlan& w, int kind,
+                           const XentTileArgs& t, hipStream_t s) {
+  return p->type == LOWBIT_F32 ? launch_xent_tile_f32(w.form[kind], kind, t, s)
+                               : launch_xent_tile_bf16(w.form[kind], kind, t, s);
+}
+
+// The logits' product over piece k of the vocabulary, w's rows copied if they
+// have to be; its kind and outputs are left to the caller.
+lowbit_status xent_logits(const XentPlan& w, const lowbit_xent_params* p, void* ws, const void* weights,
+                          int64_t k, XentTileArgs& t, hipStream_t s) {
+  const int64_t es = p->type == LOWBIT_F32 ? 4 : 2;
+  t = XentTileArgs{};
   t.count = at<int32_t>(ws, w.count);
   t.scale = at<float>(ws, w.count + 4);
   t.map = at<int32_t>(ws, w.map);
   t.info = at<float4>(ws, w.info);
-  return t;
+  t.col0 = k * w.piece;
+  t.a = at<char>(ws, w.xc);
+  t.b = static_cast<const char*>(weights) + t.col0 * p->hidden * es;
+  t.lda = t.ldb = t.k = w.ld;
+  t.m = w.padded;
+  t.n = t.col0 + w.piece < p->vocab ? w.piece : p->vocab - t.col0;
+  if (!w.packs) return LOWBIT_OK;
+  XentPack c{};
+  c.w = t.b;
+  c.to = at<char>(ws, w.wc);
+  c.rows = t.n;
+  c.hidden = (int32_t)p->hidden;
+  c.ld = (int32_t)w.ld;
+  t.b = c.to;
+  return launch_xent_pack(p->type, c, s);
 }
 
 }  // namespace
+
+// The largest form that the rows fill, unless it leaves too few tiles.
+int xent_form(int dt, int kind, int64_t m, int64_t n) {
+  int f = m > 128 && dt == LOWBIT_BF16 ? 0 : m > 64 ? 1 : m > 32 ? 2 : 3;
+  const int64_t want = kind == kXentStats || kind == kXentProb ? 192 : 64;
+  while (f < 3 && ((m + kXentForms[f].tm - 1) / kXentForms[f].tm) *
+                          ((n + kXentForms[f].tn - 1) / kXentForms[f].tn) < want)
+    ++f;
+  return f;
+}
 
 }  // namespace lowbit
 
@@ -323,18 +391,15 @@ lowbit_status lowbit_linear_xent(const void* x, const void* w, const int64_t* ta
   lowbit_status st =
       xent_rows(q, p, workspace, x, targets, nullptr, nullptr, nullptr, nullptr, stream);
   if (st != LOWBIT_OK) return st;
-  XentTileArgs t = xent_tile(q, workspace);
-  t.a = at<char>(workspace, q.xc);
-  t.lda = q.ld;
-  t.b = w;
-  t.ldb = p->hidden;
-  t.m = q.padded;
-  t.n = p->vocab;
-  t.k = p->hidden;
-  t.part = at<float2>(workspace, q.part);
-  t.hit = at<float>(workspace, q.hit);
-  t.parts = (int32_t)q.parts;
-  st = launch_xent_tile(p->type, kXentStats, t, stream);
+  XentTileArgs t{};
+  for (int64_t k = 0; k < q.pieces && st == LOWBIT_OK; ++k) {
+    st = xent_logits(q, p, workspace, w, k, t, stream);
+    t.part = at<float2>(workspace, q.part);
+    t.hit = at<float>(workspace, q.hit);
+    t.parts = (int32_t)q.parts;
+    t.part0 = (int32_t)(t.col0 / kXentForms[q.form[kXentStats]].tn);
+    if (st == LOWBIT_OK) st = xent_product(p, q, kXentStats, t, stream);
+  }
   if (st != LOWBIT_OK) return st;
   XentJoin j{};
   j.part = t.part;
@@ -365,48 +430,36 @@ lowbit_status lowbit_linear_xent_backward(const void* x, const void* w, const in
   lowbit_status st = xent_rows(q, p, workspace, x, targets, lse, dloss, dlse, dx, stream);
   const int64_t es = p->type == LOWBIT_F32 ? 4 : 2;
   for (int64_t k = 0; k < q.pieces && st == LOWBIT_OK; ++k) {
-    const int64_t col0 = k * q.piece;
-    const int64_t cols = col0 + q.piece < p->vocab ? q.piece : p->vocab - col0;
-    XentTileArgs t = xent_tile(q, workspace);
-    char* const xc = at<char>(workspace, q.xc);
-    char* const d = at<char>(workspace, q.d);
-    const char* const wk = static_cast<const char*>(w) + col0 * p->hidden * es;
-    t.a = xc;
-    t.lda = q.ld;
-    t.b = wk;
-    t.ldb = p->hidden;
-    t.m = q.padded;
-    t.n = cols;
-    t.k = p->hidden;
-    t.col0 = col0;
-    t.out = d;
+    XentTileArgs t{};
+    st = xent_logits(q, p, workspace, w, k, t, stream);
+    if (st != LOWBIT_OK) return st;
+    const int64_t cols = t.n;
+    const void* const wk = t.b;
+    t.out = at<char>(workspace, q.d);
     t.ldo = q.piece;
-    st = launch_xent_tile(p->type, kXentProb, t, stream);
+    st = xent_product(p, q, kXentProb, t, stream);
+    t.partial = at<float>(workspace, q.partial);
+    t.n = p->hidden;
+    t.ldb = q.ld;
+    t.lda = q.piece;
+    t.a = at<char>(workspace, q.d);
+    t.ldo = p->hidden;
     if (st == LOWBIT_OK && dx) {
-      t.a = d;
-      t.lda = q.piece;
       t.b = wk;
-      t.ldb = p->hidden;
-      t.n = p->hidden;
       t.k = cols;
       t.out = dx;
-      t.ldo = p->hidden;
       t.acc = q.pieces > 1 ? at<float>(workspace, q.acc) : nullptr;
+      t.ldacc = q.ld;
       t.first = k == 0;
       t.last = k == q.pieces - 1;
-      st = launch_xent_tile(p->type, kXentDx, t, stream);
+      st = xent_product(p, q, kXentDx, t, stream);
     }
     if (st == LOWBIT_OK && dw) {
-      t.a = d;
-      t.lda = q.piece;
-      t.b = xc;
-      t.ldb = q.ld;
+      t.b = at<char>(workspace, q.xc);
       t.m = cols;
-      t.n = p->hidden;
       t.k = q.padded;
-      t.out = static_cast<char*>(dw) + col0 * p->hidden * es;
-      t.ldo = p->hidden;
-      st = launch_xent_tile(p->type, kXentDw, t, stream);
+      t.out = static_cast<char*>(dw) + t.col0 * p->hidden * es;
+      st = xent_product(p, q, kXentDw, t, stream);
     }
   }
   return st;

@@ -105,6 +105,16 @@ __global__ void __launch_bounds__(256) xent_gather_kernel(XentGather a) {
   }
 }
 
+template <int DT>
+__global__ void __launch_bounds__(256) xent_pack_kernel(XentPack a) {
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    const char* from = static_cast<const char*>(a.w) + r * a.hidden * elem_size<DT>();
+    char* to = static_cast<char*>(a.to) + r * a.ld * elem_size<DT>();
+    for (int c = 8 * threadIdx.x; c < a.ld; c += 8 * 256)
+      store8<DT>(to, c, a.ld, load8<DT>(from, c, a.hidden));
+  }
+}
+
 // lse and loss of a row from its parts: a wave a row.
 __global__ void __launch_bounds__(kBlockThreads) xent_join_kernel(XentJoin a) {
   const int lane = lane_id();
@@ -147,6 +157,12 @@ lowbit_status launch_xent_gather(int dt, const XentGather& a, hipStream_t s) {
   if (blocks == 0) return LOWBIT_OK;
   return launch(dt == kF32 ? &xent_gather_kernel<kF32> : &xent_gather_kernel<kBF16>, blocks, 256,
                 s, a);
+}
+
+lowbit_status launch_xent_pack(int dt, const XentPack& a, hipStream_t s) {
+  const int64_t blocks = a.rows < (1 << 22) ? a.rows : (1 << 22);
+  return launch(dt == kF32 ? &xent_pack_kernel<kF32> : &xent_pack_kernel<kBF16>, blocks, 256, s,
+                a);
 }
 
 lowbit_status launch_xent_join(const XentJoin& a, hipStream_t s) {

@@ -1,0 +1,14 @@
+// linear xent: the products of binary32
+#include "xent_tile.hpp"
+
+namespace lowbit {
+
+lowbit_status launch_xent_tile_f32(int form, int kind, const XentTileArgs& g, hipStream_t s) {
+  switch (form) {
+    case 1: return launch_form<Form<kF32, 128, 128, 2, 2, kXentForms[1].slots>>(kind, g, s);
+    case 2: return launch_form<Form<kF32, 64, 128, 1, 4, kXentForms[2].slots>>(kind, g, s);
+    default: return launch_form<Form<kF32, 32, 128, 1, 4, kXentForms[3].slots>>(kind, g, s);
+  }
+}
+
+}  // namespace lowbit
