@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "../../include/lowbit_train.h"
+#include "xent_cut.hpp"
 
 namespace lowbit {
 
@@ -111,14 +112,6 @@ struct XentJoin {
   float *loss, *lse;
 };
 
-// A product of the loss: C[m, n] = sum_k A[m, k] B[n, k].
-enum XentKind : int {
-  kXentStats = 0,            // logits -> parts of the softmax
-  kXentProb = 1,             // logits -> d, a piece of the vocabulary
-  kXentDx = 2,               // dx += d w
-  kXentDw = 3,               // dw = d^T x
-};
-
 struct XentTileArgs {
   const void *a, *b;         // a[m lda + k], or a[k lda + m] where the kind has it so
   int64_t lda, ldb;          // multiples of 16 bytes
@@ -134,8 +127,7 @@ struct XentTileArgs {
   int32_t parts, part0;      // of a row; the first of n = 0
   void* out;                 // d, dx or dw
   int64_t ldo;
-  float* acc;                // dx over several pieces: their sum so far
-  int64_t ldacc;
+  float* acc;                // dx over several pieces: their sum so far, tile by tile
   int32_t first, last;       // piece of the vocabulary
   float* partial;            // sums of tiles that are cut along k (dx, dw)
 };
@@ -147,12 +139,6 @@ lowbit_status launch_xent_join(const XentJoin& a, hipStream_t s);
 lowbit_status launch_xent_tile_bf16(int form, int kind, const XentTileArgs& a, hipStream_t s);
 lowbit_status launch_xent_tile_f32(int form, int kind, const XentTileArgs& a, hipStream_t s);
 
-// The tile kernels' forms: rows and columns of a tile, and how many of its
-// workgroups the chip holds at one time.
-struct XentForm {
-  int tm, tn, slots;
-};
-constexpr XentForm kXentForms[4] = {{256, 256, 256}, {128, 128, 512}, {64, 128, 768}, {32, 128, 1024}};
 constexpr int64_t kXentPad = 256;  // rows and pieces of the vocabulary: multiples of every tile's
 int xent_form(int dt, int kind, int64_t m, int64_t n);
 

@@ -117,14 +117,8 @@ struct XentPlan {
   int64_t pos, map, info, count, xc, wc, part, hit, d, acc, partial, bytes;
 };
 
-// Sums of the tiles that a product cuts along k: one tile for each slot, and
-// four steps of k for each part.
-int64_t xent_partial_bytes(int dt, const XentForm& f, int64_t m, int64_t n, int64_t k) {
-  const int64_t step = dt == LOWBIT_F32 ? 32 : 64, quarter = up(k, step) / step / 4;
-  const int64_t tiles = (m + f.tm - 1) / f.tm * ((n + f.tn - 1) / f.tn);
-  if (quarter < 2) return 0;
-  const int64_t slots = tiles < f.slots && tiles * quarter < f.slots ? tiles * quarter : f.slots;
-  return slots * f.tm * f.tn * 4;
+int64_t xent_partial_bytes(int64_t es, const XentForm& f, int64_t m, int64_t n, int64_t k) {
+  return xent_slots(f, m, n, xent_steps(k, (int)es)) * f.tm * f.tn * 4;
 }
 
 XentPlan xent_plan(const lowbit_xent_params* p, bool backward) {
@@ -158,14 +152,16 @@ XentPlan xent_plan(const lowbit_xent_params* p, bool backward) {
   if (w.packs) w.wc = take(w.piece * w.ld * es);
   if (backward) {
     w.d = take(w.padded * w.piece * es);
-    if (w.pieces > 1) w.acc = take(p->rows * w.ld * 4);
     const int64_t cols = w.piece < p->vocab ? w.piece : p->vocab;
     w.form[kXentProb] = xent_form(p->type, kXentProb, p->rows, cols);
     w.form[kXentDx] = xent_form(p->type, kXentDx, p->rows, p->hidden);
     w.form[kXentDw] = xent_form(p->type, kXentDw, cols, p->hidden);
+    const XentForm& fx = kXentForms[w.form[kXentDx]];
+    if (w.pieces > 1) w.acc = take(up(p->rows, fx.tm) * up(p->hidden, fx.tn) * 4);
     w.partial = take(std::max(
-        xent_partial_bytes(p->type, kXentForms[w.form[kXentDx]], p->rows, p->hidden, cols),
-        xent_partial_bytes(p->type, kXentForms[w.form[kXentDw]], cols, p->hidden, p->rows)));
+        {xent_partial_bytes(es, kXentForms[w.form[kXentProb]], p->rows, cols, p->hidden),
+         xent_partial_bytes(es, fx, p->rows, p->hidden, cols),
+         xent_partial_bytes(es, kXentForms[w.form[kXentDw]], cols, p->hidden, p->rows)}));
   } else {
     w.parts = (p->vocab + f.tn - 1) / f.tn;
     w.part = take(p->rows * w.parts * 8);
@@ -435,10 +431,10 @@ lowbit_status lowbit_linear_xent_backward(const void* x, const void* w, const in
     if (st != LOWBIT_OK) return st;
     const int64_t cols = t.n;
     const void* const wk = t.b;
+    t.partial = at<float>(workspace, q.partial);
     t.out = at<char>(workspace, q.d);
     t.ldo = q.piece;
     st = xent_product(p, q, kXentProb, t, stream);
-    t.partial = at<float>(workspace, q.partial);
     t.n = p->hidden;
     t.ldb = q.ld;
     t.lda = q.piece;
@@ -449,7 +445,6 @@ lowbit_status lowbit_linear_xent_backward(const void* x, const void* w, const in
       t.k = cols;
       t.out = dx;
       t.acc = q.pieces > 1 ? at<float>(workspace, q.acc) : nullptr;
-      t.ldacc = q.ld;
       t.first = k == 0;
       t.last = k == q.pieces - 1;
       st = xent_product(p, q, kXentDx, t, stream);

@@ -11,11 +11,12 @@ namespace lowbit {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_2 __attribute__((ext_vector_type(2), aligned(2)));
 #define LOWBIT_LDS __attribute__((address_space(3)))
 
-constexpr int kRowBytes = 128;             // of k, between two barriers
+constexpr int kRowBytes = kXentRowBytes;   // of k, between two barriers
 constexpr uint32_t kNowhere = 0x7FFFFFF0u; // beyond every buffer's records
 constexpr float kLog2e = 1.44269502f;      // log2(e) to binary32
 
@@ -24,94 +25,104 @@ constexpr float kLog2e = 1.44269502f;      // log2(e) to binary32
 // matrix's row, and LDS holds rows of k; else rows of the tile.  The pieces of
 // a row in LDS are permuted by the row's number, so that the reads of Frag
 // meet no bank twice; a load writes LDS in lane order, so each lane fetches
-// the piece that belongs in its place.  What lies behind the matrix's end reads as 0.
+// the piece that belongs in its place.  What lies behind the matrix's end reads
+// as 0.  (Rows of 64 bytes, which would let more steps be under way, load at
+// half the rate: 67 against 130 bytes/ns and CU.)
 template <int DT, int T, int W, bool OUTER>
 struct Feed {
   static constexpr int ES = elem_size<DT>(), K = kRowBytes / ES, LOADS = T / 8 / W;
   static constexpr int KR = 1024 / (T * ES);     // OUTER: rows of k in a wave's load
+  static constexpr int PIECE = DT == kF32 ? 128 : 32;   // OUTER: bytes
   const char* base;
-  int64_t left, jstep, kstep;                    // bytes
-  uint32_t voff, vcol;
+  int64_t left, kstep;                           // bytes
+  uint32_t voff[LOADS];
   int kin;                                       // the lane's first k within the step
 
-  // the pieces (32 bytes of bfloat16, 64 of binary32: 16 columns) of row k are xored with this
+  // OUTER: the pieces of row k are xored with this
   static __device__ __forceinline__ constexpr int mix(int k) {
-    return (DT == kF32 ? k >> 2 & 3 : (k & 3) | (k >> 1 & 4)) & (T / 16 - 1);
+    return (DT == kF32 ? k >> 2 & 1 : (k & 3) << 1 | (k >> 3 & 1)) & (T * ES / PIECE - 1);
   }
-  // rows: of the matrix in memory; k0: where to begin
-  __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t rows, int64_t row0,
-                                       int64_t k0, int wave, int lane) {
-    const char* at = static_cast<const char*>(p);
-    if constexpr (OUTER) {
-      constexpr int L = T * ES / 16, P = ES;     // lanes of a row, of a piece
-      const int k = wave * KR + lane / L, slot = lane % L;
-      base = at + (k0 * ld + row0) * ES;
-      left = ((rows - k0) * ld - row0) * ES;
-      jstep = (int64_t)W * KR * ld * ES;
-      kstep = K * ld * ES;
-      kin = 0;
-      voff = (uint32_t)(k * ld * ES);
-      vcol = ((slot / P ^ mix(k)) * P + slot % P) * 16;
-    } else {
-      const int r = wave * 8 + lane / 8, c = lane % 8 ^ (r >> 1 & 7);
-      base = at + (row0 * ld + k0) * ES;
-      left = ((rows - row0) * ld - k0) * ES;
-      jstep = (int64_t)W * 8 * ld * ES;
-      kstep = kRowBytes;
-      kin = c * (16 / ES);
-      voff = (uint32_t)(r * ld * ES);
-      vcol = c * 16;
-    }
-  }
-  __device__ __forceinline__ void issue(char* lds, int wave, int64_t kleft) {
+  __device__ __forceinline__ void init(int64_t ld, int wave, int lane) {
     static_assert(LOADS >= 1 && (!OUTER || K % (W * KR) == 0), "");
+    kstep = OUTER ? K * ld * ES : kRowBytes;
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
-      uint32_t v = voff + (OUTER ? vcol ^ mix(j * W * KR) * 16 * ES : vcol);
-      if (!OUTER && kin >= kleft) v = kNowhere;
-      const int64_t l = left - j * jstep;
-      const int records = (int)(l < 0 ? 0 : l > kNowhere ? kNowhere : l);
-      __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<char*>(base + j * jstep), 0, records, 0x00020000);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LOWBIT_LDS void*)(lds + (j * W + wave) * 1024),
-                                               16, v, 0, 0, 0);
+      if constexpr (OUTER) {
+        constexpr int L = T * ES / 16, P = PIECE / 16;   // lanes of a row, of a piece
+        const int k = (j * W + wave) * KR + lane / L, slot = lane % L;
+        kin = 0;
+        voff[j] = (uint32_t)(k * ld * ES) + ((slot / P ^ mix(k)) * P + slot % P) * 16;
+      } else {
+        const int r = (j * W + wave) * 8 + lane / 8, c = lane % 8 ^ (r >> 1 & 7);
+        kin = c * (16 / ES);                             // (r >> 1 & 7 is the same for every j)
+        voff[j] = (uint32_t)(r * ld * ES) + c * 16;
+      }
     }
+  }
+  // rows: of the matrix in memory; k0: where to begin
+  __device__ __forceinline__ void seek(const void* p, int64_t ld, int64_t rows, int64_t row0,
+                                       int64_t k0) {
+    const int64_t at = (OUTER ? k0 * ld + row0 : row0 * ld + k0) * ES;
+    base = static_cast<const char*>(p) + at;
+    left = rows * ld * ES - at;
+  }
+  // The matrix from here on, for the loads of one step (none if !any).
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t open(bool any) const {
+    const int records = (int)(left < 0 || !any ? 0 : left > kNowhere ? kNowhere : left);
+    const uint64_t at = (uint64_t)base;            // (uniform, but not for the compiler)
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)hi << 32 | lo), 0,
+                                             __builtin_amdgcn_readfirstlane(records), 0x00020000);
+  }
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, char* lds, int wave, int kleft,
+                                       int j) const {
+    const uint32_t v = !OUTER && kin >= kleft ? kNowhere : voff[j];
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LOWBIT_LDS void*)(lds + (j * W + wave) * 1024),
+                                             16, v, 0, 0, 0);
+  }
+  __device__ __forceinline__ void next() {
     base += kstep;
     left -= kstep;
   }
 };
 
-// A lane's part of 16 rows by 64 bytes of k: row lane mod 16, the (lane / 16)-th 16 bytes.
+// A lane's part of 32 rows by 32 bytes of k: row lane mod 32, the (lane / 32)-th 16 bytes.
 template <int DT, int T, bool OUTER>
 struct Frag {
   static constexpr int ES = elem_size<DT>(), PITCH = T * ES;
-  uint32_t at[2];
+  uint32_t at[4];
   int piece, f;                                  // OUTER
   __device__ __forceinline__ void init(int row0, int lane) {
-    const int g = lane / 16, i = lane % 16;
-    if constexpr (OUTER) {
-      f = Feed<DT, T, 1, true>::mix(DT == kF32 ? 4 * g : 8 * g + i / 4);
-      piece = row0 / 16;
-      at[0] = DT == kF32 ? 4 * g * PITCH + i * 4 : (8 * g + i / 4) * PITCH + i % 4 * 8;
+    const int h = lane / 32;
+    if constexpr (OUTER && DT == kF32) {
+      f = Feed<DT, T, 1, true>::mix(4 * h);
+      piece = row0 / 32;
+      at[0] = 4 * h * PITCH + lane % 32 * 4;
+    } else if constexpr (OUTER) {
+      const int k = 8 * h + lane % 16 / 4;
+      f = Feed<DT, T, 1, true>::mix(k);
+      piece = row0 / 16 + lane / 16 % 2;
+      at[0] = k * PITCH + lane % 4 * 8;
     } else {
-      const int r = row0 + i, s = r >> 1 & 7;
-      at[0] = r * kRowBytes + (g ^ s) * 16;
-      at[1] = r * kRowBytes + ((4 + g) ^ s) * 16;
+      const int r = row0 + lane % 32, s = r >> 1 & 7;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) at[kk] = r * kRowBytes + ((2 * kk + h) ^ s) * 16;
     }
   }
-  // 16-row piece i of the wave, half kk of the step
+  // 32-row piece i of the wave, quarter kk of the step
   __device__ __forceinline__ u32x4 load(const char* lds, int i, int kk) const {
     if constexpr (!OUTER) {
-      return *reinterpret_cast<const u32x4*>(lds + at[kk] + i * 16 * kRowBytes);
+      return *reinterpret_cast<const u32x4*>(lds + at[kk] + i * 32 * kRowBytes);
     } else if constexpr (DT == kF32) {
-      const char* p = lds + at[0] + ((piece + i) ^ f) * 64 + kk * 16 * PITCH;
+      const char* p = lds + at[0] + ((piece + i) ^ f) * 128 + kk * 8 * PITCH;
       u32x4 v;
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint32_t*>(p + j * PITCH);
       return v;
     } else {
       // 16 lanes read 16 columns of four rows of k and get a column each
-      const char* p = lds + at[0] + ((piece + i) ^ f) * 32 + kk * 32 * PITCH;
+      const char* p = lds + at[0] + ((piece + 2 * i) ^ f) * 32 + kk * 16 * PITCH;
       typedef LOWBIT_LDS s16x4* lp;
       const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(LOWBIT_LDS char*)p);
       const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(LOWBIT_LDS char*)(p + 4 * PITCH));
@@ -120,18 +131,18 @@ struct Frag {
   }
 };
 
-// The product of 16 rows of n with 16 rows of m over 64 bytes of k.  For
+// The product of 32 rows of n with 32 rows of m over 32 bytes of k.  For
 // binary32 four products take one element of each lane: k in another order, the
 // same for both.
 template <int DT>
-__device__ __forceinline__ f32x4 mma(const u32x4& b, const u32x4& a, f32x4 c) {
+__device__ __forceinline__ f32x16 mma(const u32x4& b, const u32x4& a, f32x16 c) {
   if constexpr (DT == kBF16) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b),
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b),
                                                    __builtin_bit_cast(bf16x8, a), c, 0, 0, 0);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(b[j]), __uint_as_float(a[j]), c, 0,
+      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(b[j]), __uint_as_float(a[j]), c, 0,
                                                0, 0);
     return c;
   }
@@ -150,42 +161,10 @@ __device__ __forceinline__ float exp_term(float x) {
   return x < -200.0f ? 0.0f : __builtin_fmaf(y, e * 0.693147182f, y);
 }
 
-// Which tiles of a product are cut along k.  The workgroups that the chip holds
-// at one time (SLOTS) take whole tiles as long as all of them have one; the
-// remaining tiles are cut into as many parts as there are slots for them, of
-// four steps of k at least, and the parts' sums are added by a second kernel.
-// Two rounds instead of one and a half would leave half of the chip idle in the second.
-struct XentCut {
-  uint32_t across, down, tiles, whole;           // whole: tiles that are not cut
-  uint32_t rest, parts;                          // tiles that are, each into `parts`
-  __host__ __device__ XentCut(int64_t m, int64_t n, uint32_t k_steps, uint32_t tm, uint32_t tn,
-                              uint32_t slots, bool may_cut) {
-    across = ((uint32_t)n + tn - 1) / tn;
-    down = ((uint32_t)m + tm - 1) / tm;
-    tiles = across * down;
-    rest = tiles % slots;
-    parts = rest && may_cut ? slots / rest : 1;
-    if (parts > k_steps / 4) parts = k_steps / 4;
-    if (parts <= 1) {
-      parts = 1;
-      rest = 0;
-    }
-    whole = tiles - rest;
-  }
-};
-
-// XCD x of 8 takes a contiguous run of the units; -1 for workgroups beyond them.
-__device__ __forceinline__ int xcd_run(uint32_t block, uint32_t units) {
-  const uint32_t x = block % kXcds, q = block / kXcds;
-  const uint32_t each = units / kXcds, more = units % kXcds;
-  if (q >= each + (x < more ? 1 : 0)) return -1;
-  return x * each + (x < more ? x : more) + q;
-}
-
 template <int DT_, int TM_, int TN_, int WM_, int WN_, int SLOTS_>
 struct Form {
   static constexpr int DT = DT_, TM = TM_, TN = TN_, WM = WM_, WN = WN_, SLOTS = SLOTS_;
-  static constexpr int W = WM * WN, I = TM / WM / 16, J = TN / WN / 16, THREADS = 64 * W;
+  static constexpr int W = WM * WN, I = TM / WM / 32, J = TN / WN / 32, THREADS = 64 * W;
 };
 
 template <class F, int KIND>
@@ -195,39 +174,37 @@ struct TilePlan {
   // count: rows that count (device), or the most there can be (host)
   __host__ __device__ TilePlan(const XentTileArgs& g, int64_t count)
       : cut(KIND == kXentDw ? g.m : count, g.n, steps(KIND == kXentDw ? count : g.k), F::TM, F::TN,
-            F::SLOTS, KIND == kXentDx || KIND == kXentDw),
+            F::SLOTS, xent_least(KIND)),
         m(KIND == kXentDw ? g.m : count), k(KIND == kXentDw ? count : g.k) {}
   static __host__ __device__ uint32_t steps(int64_t k) {
-    constexpr int K = kRowBytes / elem_size<F::DT>();
-    return (uint32_t)((k + K - 1) / K);
-  }
-  // tiles in bands of 8 rows of tiles: the 32 that an XCD's CUs hold at one time
-  // read 8 panels of a and 4 of b through its L2
-  __device__ __forceinline__ void place(uint32_t tile, uint32_t& tm, uint32_t& tn) const {
-    const uint32_t band = tile / (8 * cut.across), in = tile % (8 * cut.across);
-    const uint32_t high = cut.down - band * 8 < 8 ? cut.down - band * 8 : 8;
-    tm = band * 8 + in % high;
-    tn = in / high;
+    return xent_steps(k, elem_size<F::DT>());
   }
 };
 
-// Four consecutive columns n .. n + 3 of row `row` of dx or dw.
+__device__ __forceinline__ f32x4 quad(const f32x16& v, int q) {
+  return (f32x4){v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+}
+
+// Four consecutive columns n .. n + 3 of row `row` of d, dx or dw.
 template <int DT, int KIND>
 __device__ __forceinline__ void emit(const XentTileArgs& g, float scale, int64_t row, int64_t n,
                                      f32x4 v) {
-  if (n >= g.n) return;
-  int64_t to = row * g.ldo;
-  if constexpr (KIND == kXentDx) {
-    if (!(g.first && g.last)) {
-      f32x4* sum = reinterpret_cast<f32x4*>(g.acc + row * g.ldacc + n);
-      if (!g.first) v += *sum;
-      if (!g.last) {
-        *sum = v;
-        return;
-      }
+  if constexpr (KIND == kXentProb) {
+    const float4 info = g.info[row];
+    const int64_t target = (int64_t)__float_as_int(info.w) - g.col0 - n;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      v[r] = exp_term<DT>(v[r] - info.x) * (info.y / scale);
+      if (target == r) v[r] -= info.z / scale;
+      if (n + r >= g.n) v[r] = 0.0f;
     }
-    to = (int64_t)g.map[row] * g.ldo;
+    char* to = static_cast<char*>(g.out) + (row * g.ldo + n) * elem_size<DT>();
+    if constexpr (DT == kF32) *reinterpret_cast<f32x4*>(to) = v;
+    else *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    return;
   }
+  if (n >= g.n) return;
+  const int64_t to = (KIND == kXentDx ? (int64_t)g.map[row] : row) * g.ldo;
   v *= scale;
   if constexpr (DT == kF32) {
     float* p = static_cast<float*>(g.out) + to + n;
@@ -250,108 +227,84 @@ __device__ __forceinline__ void emit(const XentTileArgs& g, float scale, int64_t
   }
 }
 
-// W waves, each I x J products of 16 x 16.  Lane l holds of product (i, j) row
-// 16 i + l mod 16 of m and rows 16 j + 4 (l / 16) + r of n: four consecutive
-// columns of the output's row.  Two buffers in LDS: while the matrix units work
-// on one, the other is filled.
+__device__ __forceinline__ void barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+// All that the wave has loaded, stored or read in LDS is done.
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// Order for the compiler: R reads of LDS, spread over M products.
+template <int R, int M, int N = 0>
+__device__ __forceinline__ void spread_reads() {
+  if constexpr (N < R) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, M * (N + 1) / R - M * N / R, 0);
+    spread_reads<R, M, N + 1>();
+  }
+}
+// R reads and L loads to LDS, spread over M products of Q instructions.
+template <int R, int M, int Q, int L, int N = 0>
+__device__ __forceinline__ void spread_loads() {
+  if constexpr (N < M) {
+    __builtin_amdgcn_sched_group_barrier(0x008, Q, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, R * (N + 1) / M - R * N / M, 0);
+    __builtin_amdgcn_sched_group_barrier(0x020, L * (N + 1) / M - L * N / M, 0);
+    spread_loads<R, M, Q, L, N + 1>();
+  }
+}
+
+// A tile's sums as the lanes hold them, TM x TN values in a row.
+template <class F>
+__device__ __forceinline__ f32x4* lanes(float* base, int64_t tile) {
+  return reinterpret_cast<f32x4*>(base) + tile * (F::TM * F::TN / 4) + threadIdx.x;
+}
+template <class F>
+__device__ __forceinline__ void store_lanes(f32x4* to, const f32x16 (&acc)[F::I][F::J]) {
+#pragma unroll
+  for (int i = 0; i < F::I; ++i)
+#pragma unroll
+    for (int j = 0; j < F::J; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) to[((i * F::J + j) * 4 + q) * F::THREADS] = quad(acc[i][j], q);
+}
+
+// What becomes of a tile's sums.  halves: [WN][TM] in LDS.
 template <class F, int KIND>
-__global__ void __launch_bounds__(F::THREADS) xent_tile_kernel(XentTileArgs g) {
-  constexpr int DT = F::DT, TM = F::TM, TN = F::TN, W = F::W, I = F::I, J = F::J;
-  constexpr bool AO = KIND == kXentDw, BO = KIND == kXentDx || KIND == kXentDw;
-  constexpr int K = kRowBytes / elem_size<DT>();
-  __shared__ __attribute__((aligned(1024))) char la0[TM * kRowBytes];
-  __shared__ __attribute__((aligned(1024))) char lb0[TN * kRowBytes];
-  __shared__ __attribute__((aligned(1024))) char la1[TM * kRowBytes];
-  __shared__ __attribute__((aligned(1024))) char lb1[TN * kRowBytes];
-  const TilePlan<F, KIND> plan(g, *g.count);
-  const XentCut& cut = plan.cut;
-  const int64_t m = plan.m, k = plan.k;
-  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / F::WN, wn = wave % F::WN;
-
-  int tile, slot = -1, s0 = 0, s1 = (int)plan.steps(k);
-  if (blockIdx.x < cut.whole) {
-    tile = xcd_run(blockIdx.x, cut.whole);
-  } else {
-    slot = xcd_run(blockIdx.x - cut.whole, cut.rest * cut.parts);
-    if (slot < 0) return;
-    const uint32_t part = (uint32_t)slot / cut.rest, all = s1;
-    tile = cut.whole + (uint32_t)slot % cut.rest;
-    s0 = all / cut.parts * part + min(part, all % cut.parts);
-    s1 = s0 + all / cut.parts + (part < all % cut.parts ? 1 : 0);
-  }
-  uint32_t tm, tn;
-  plan.place(tile, tm, tn);
-  const int64_t m0 = (int64_t)tm * TM, n0 = (int64_t)tn * TN;
-
-  f32x4 acc[I][J];
-#pragma unroll
-  for (int i = 0; i < I; ++i)
-#pragma unroll
-    for (int j = 0; j < J; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-  Feed<DT, TM, W, AO> fa;
-  Feed<DT, TN, W, BO> fb;
-  fa.init(g.a, g.lda, AO ? k : g.m, m0, (int64_t)s0 * K, wave, lane);
-  fb.init(g.b, g.ldb, BO ? k : g.n, n0, (int64_t)s0 * K, wave, lane);
-  Frag<DT, TM, AO> ra;
-  Frag<DT, TN, BO> rb;
-  ra.init(wm * (TM / F::WM), lane);
-  rb.init(wn * (TN / F::WN), lane);
-
-  if (s0 < s1) {
-    fa.issue(la0, wave, k - (int64_t)s0 * K);
-    fb.issue(lb0, wave, k - (int64_t)s0 * K);
-  }
-  auto step = [&](const char* la, const char* lb, char* na, char* nb, int s) {
-    __syncthreads();               // the loads have arrived, and nobody reads na and nb any more
-    if (s + 1 < s1) {
-      fa.issue(na, wave, k - (int64_t)(s + 1) * K);
-      fb.issue(nb, wave, k - (int64_t)(s + 1) * K);
-    }
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      u32x4 a[I], b[J];
-#pragma unroll
-      for (int j = 0; j < J; ++j) b[j] = rb.load(lb, j, kk);
-#pragma unroll
-      for (int i = 0; i < I; ++i) a[i] = ra.load(la, i, kk);
-#pragma unroll
-      for (int i = 0; i < I; ++i)
-#pragma unroll
-        for (int j = 0; j < J; ++j) acc[i][j] = mma<DT>(b[j], a[i], acc[i][j]);
-    }
-  };
-  for (int s = s0; s < s1; s += 2) {
-    step(la0, lb0, la1, lb1, s);
-    if (s + 1 < s1) step(la1, lb1, la0, lb0, s + 1);
-  }
-
-  const int64_t ml = m0 + wm * (TM / F::WM) + lane % 16;          // + 16 i
-  const int64_t nl = n0 + wn * (TN / F::WN) + lane / 16 * 4;      // + 16 j + r
+__device__ __forceinline__ void finish(const XentTileArgs& g, f32x16 (&acc)[F::I][F::J], int64_t m,
+                                       int64_t m0, int64_t n0, uint32_t tn, int wm, int wn, int lane,
+                                       float2* halves) {
+  constexpr int DT = F::DT, TM = F::TM, TN = F::TN, I = F::I, J = F::J;
+  const int64_t ml = m0 + wm * (TM / F::WM) + lane % 32;          // + 32 i
+  const int64_t nl = n0 + wn * (TN / F::WN) + lane / 32 * 4;      // + 32 j + at(r)
   const bool inside = n0 + TN <= g.n;
+  auto at = [](int r) { return r / 4 * 8 + r % 4; };
   if constexpr (KIND == kXentStats) {
-    float2* halves = reinterpret_cast<float2*>(la0);              // [WN][TM]
-    __syncthreads();
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int64_t row = ml + 16 * i;
+      const int64_t row = ml + 32 * i;
       const int64_t target = row < m ? (int64_t)__float_as_int(g.info[row].w) - nl : -1;
-      if (__any(target >= 0 && target < 16 * J)) {
+      if (__any(target >= 0 && target < 32 * J)) {
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (target == 16 * j + r) g.hit[row] = acc[i][j][r];
+          for (int r = 0; r < 16; ++r)
+            if (target == 32 * j + at(r)) g.hit[row] = acc[i][j][r];
       }
       float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if (!inside && nl + 16 * j + r >= g.n) acc[i][j][r] = -INFINITY;
+        for (int r = 0; r < 16; ++r) {
+          if (!inside && nl + 32 * j + at(r) >= g.n) acc[i][j][r] = -INFINITY;
           top = fmaxf(top, acc[i][j][r]);
         }
-      top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       // bfloat16: 2^(l log2(e) - base) in two instructions; base is off by at most
       // |top| 2^-24, as lse itself
@@ -360,16 +313,17 @@ __global__ void __launch_bounds__(F::THREADS) xent_tile_kernel(XentTileArgs g) {
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < 16; ++r) {
           const float l = acc[i][j][r];
           if constexpr (DT == kF32) sum += exp_term<DT>(l - base);
           else sum += __builtin_amdgcn_exp2f(__builtin_fmaf(l, kLog2e, -base));
         }
-      sum += __shfl_xor(sum, 16);
       sum += __shfl_xor(sum, 32);
-      if (lane < 16) halves[wn * TM + wm * (TM / F::WM) + i * 16 + lane] = make_float2(top, sum);
+      __builtin_amdgcn_sched_barrier(0);
+      if (lane < 32) halves[wn * TM + wm * (TM / F::WM) + i * 32 + lane] = make_float2(top, sum);
     }
-    __syncthreads();
+    wait_lds();
+    barrier();
     const int r = threadIdx.x;
     if (r < TM && m0 + r < m) {
       float top = -INFINITY, sum = 0.0f;
@@ -386,53 +340,234 @@ __global__ void __launch_bounds__(F::THREADS) xent_tile_kernel(XentTileArgs g) {
     const float scale = DT == kF32 ? 1.0f : *g.scale;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int64_t row = ml + 16 * i;
-      const float4 info = row < m ? g.info[row] : make_float4(0, 0, 0, __int_as_float(-1));
+      const int64_t row = ml + 32 * i;
+      const float4 info = g.info[row];             // (rows beyond those that count have some, too)
       const float both = info.y / scale, own = info.z / scale;
       const int64_t target = (int64_t)__float_as_int(info.w) - g.col0 - nl;
       char* to = static_cast<char*>(g.out) + (row * g.ldo + nl) * elem_size<DT>();
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < 16; ++r) {
           acc[i][j][r] = exp_term<DT>(acc[i][j][r] - info.x) * both;
-          if (!inside && nl + 16 * j + r >= g.n) acc[i][j][r] = 0.0f;
+          if (!inside && nl + 32 * j + at(r) >= g.n) acc[i][j][r] = 0.0f;
         }
-      if (__any(target >= 0 && target < 16 * J)) {
+      if (__any(target >= 0 && target < 32 * J)) {
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (target == 16 * j + r && nl + target < g.n) acc[i][j][r] -= own;
+          for (int r = 0; r < 16; ++r)
+            if (target == 32 * j + at(r) && nl + target < g.n) acc[i][j][r] -= own;
       }
-      if (row < m) {
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const f32x4 d = acc[i][j];
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 d = quad(acc[i][j], q);
           if constexpr (DT == kF32)
-            *reinterpret_cast<f32x4*>(to + 64 * j) = d;
+            *reinterpret_cast<f32x4*>(to + 128 * j + 32 * q) = d;
           else
-            *reinterpret_cast<uint2*>(to + 32 * j) =
+            *reinterpret_cast<uint2*>(to + 64 * j + 16 * q) =
                 make_uint2(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]));
+        }
+    }
+  } else {
+    const float scale = DT == kF32 ? 1.0f : *g.scale;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int64_t row = ml + 32 * i;
+      if (row < m) {
+        if (inside) {
+          char* to = static_cast<char*>(g.out) +
+                     ((KIND == kXentDx ? (int64_t)g.map[row] : row) * g.ldo + nl) * elem_size<DT>();
+#pragma unroll
+          for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const f32x4 v = quad(acc[i][j], q) * scale;
+              if constexpr (DT == kF32)
+                *reinterpret_cast<u32x4_4*>(to + 128 * j + 32 * q) = __builtin_bit_cast(u32x4, v);
+              else
+                *reinterpret_cast<u32x2_2*>(to + 64 * j + 16 * q) =
+                    (u32x2_2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+            }
+        } else {
+#pragma unroll
+          for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              emit<DT, KIND>(g, scale, row, nl + 32 * j + 8 * q, quad(acc[i][j], q));
         }
       }
     }
-  } else {
-    if (slot >= 0) {               // a part's sums, as the lanes hold them
-      f32x4* to = reinterpret_cast<f32x4*>(g.partial) + (int64_t)slot * (TM * TN / 4) + threadIdx.x;
+  }
+}
+
+// W waves, each I x J products of 32 x 32.  Lane l holds of product (i, j) row
+// 32 i + l mod 32 of m and rows 32 j + 8 q + 4 (l / 32) + r of n: four times
+// four consecutive columns of the output's row.  Two buffers in LDS: while the
+// matrix units work on one, the other is filled.
+template <class F, int KIND>
+__global__ void __launch_bounds__(F::THREADS, F::SLOTS * F::W / 1024) xent_tile_kernel(XentTileArgs g) {
+  constexpr int DT = F::DT, TM = F::TM, TN = F::TN, W = F::W, I = F::I, J = F::J;
+  constexpr bool AO = KIND == kXentDw, BO = KIND == kXentDx || KIND == kXentDw;
+  constexpr int K = kRowBytes / elem_size<DT>();
+  __shared__ __attribute__((aligned(1024))) char la0[TM * kRowBytes];
+  __shared__ __attribute__((aligned(1024))) char lb0[TN * kRowBytes];
+  __shared__ __attribute__((aligned(1024))) char la1[TM * kRowBytes];
+  __shared__ __attribute__((aligned(1024))) char lb1[TN * kRowBytes];
+  __shared__ float2 halves[KIND == kXentStats ? F::WN * TM : 1];
+  const TilePlan<F, KIND> plan(g, __builtin_amdgcn_readfirstlane(*g.count));
+  const XentCut& cut = plan.cut;
+  const int64_t m = plan.m, k = plan.k;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / F::WN, wn = wave % F::WN;
+
+  const int64_t steps = plan.steps(k);
+  const uint32_t units = cut.units();
+  int slot, s0, s1;
+  uint32_t tile, tm, tn;
+  auto take = [&](uint32_t u) {
+    const XentUnit v = cut.unit(u, (uint32_t)steps);
+    tm = __builtin_amdgcn_readfirstlane(v.tm);     // (the compiler does not see that they are uniform)
+    tn = __builtin_amdgcn_readfirstlane(v.tn);
+    s0 = __builtin_amdgcn_readfirstlane(v.s0);
+    s1 = __builtin_amdgcn_readfirstlane(v.s1);
+    slot = __builtin_amdgcn_readfirstlane(v.slot);
+    tile = __builtin_amdgcn_readfirstlane(v.tile);
+  };
+
+  constexpr int NA = Feed<DT, TM, W, AO>::LOADS, NB = Feed<DT, TN, W, BO>::LOADS, N = NA + NB;
+  constexpr int Q = DT == kF32 ? 4 : 1;            // matrix instructions of a product
+  constexpr int RD = I * (AO ? Q > 1 ? 4 : 2 : 1) + J * (BO ? Q > 1 ? 4 : 2 : 1);
+  Feed<DT, TM, W, AO> fa;
+  Feed<DT, TN, W, BO> fb;
+  Frag<DT, TM, AO> ra;
+  Frag<DT, TN, BO> rb;
+  fa.init(g.lda, wave, lane);
+  fb.init(g.ldb, wave, lane);
+  ra.init(wm * (TM / F::WM), lane);
+  rb.init(wn * (TN / F::WN), lane);
+  u32x4 fra[2][I], frb[2][J];
+  f32x16 acc[I][J];
+
+  auto kleft = [&](int s) { return (int)min(k - (int64_t)s * K, (int64_t)K); };
+  auto issue = [&](char* la, char* lb, int s) {
+    const auto qa = fa.open(s < s1), qb = fb.open(s < s1);
+#pragma unroll
+    for (int j = 0; j < NA; ++j) fa.load(qa, la, wave, kleft(s), j);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) fb.load(qb, lb, wave, kleft(s), j);
+    fa.next();
+    fb.next();
+  };
+  auto begin = [&] {                               // the unit's first two steps
+    fa.seek(g.a, g.lda, AO ? k : g.m, (int64_t)tm * TM, (int64_t)s0 * K);
+    fb.seek(g.b, g.ldb, BO ? k : g.n, (int64_t)tn * TN, (int64_t)s0 * K);
+    issue(la0, lb0, s0);
+    issue(la1, lb1, s0 + 1);
+  };
+  auto read = [&](int to, const char* la, const char* lb, int kk) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) frb[to][j] = rb.load(lb, j, kk);
+#pragma unroll
+    for (int i = 0; i < I; ++i) fra[to][i] = ra.load(la, i, kk);
+  };
+  auto mul = [&](int f) {
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+      for (int j = 0; j < J; ++j) acc[i][j] = mma<DT>(frb[f][j], fra[f][i], acc[i][j]);
+    spread_reads<RD, I * J * Q>();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Step s, in la and lb, whose first quarter is in registers.  While a quarter is
+  // multiplied the next is read; before the last, everybody has read all of
+  // this step, the next one has arrived, and the loads of the one after it begin.
+  auto step = [&](char* la, char* lb, const char* na, const char* nb, int s) {
+    const auto qa = fa.open(s + 2 < s1), qb = fb.open(s + 2 < s1);
+    const int kl = kleft(s + 2);
+    read(1, la, lb, 1);
+    mul(0);
+    read(0, la, lb, 2);
+    mul(1);
+    read(1, la, lb, 3);
+    mul(0);
+    wait_loads();
+    barrier();
+    read(0, na, nb, 0);
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        acc[i][j] = mma<DT>(frb[1][j], fra[1][i], acc[i][j]);
+        const int p = i * J + j;
+#pragma unroll
+        for (int u = N * p / (I * J); u < N * (p + 1) / (I * J); ++u) {
+          if (u < NA) fa.load(qa, la, wave, kl, u);
+          else fb.load(qb, lb, wave, kl, u - NA);
+        }
+      }
+    fa.next();
+    fb.next();
+    spread_loads<RD, I * J, Q, N>();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  uint32_t unit = blockIdx.x;
+  if (unit >= units) return;
+  take(unit);
+  begin();
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+    if (KIND == kXentDx && !g.first && slot < 0) { // the earlier pieces' sums
+      const f32x4* from = lanes<F>(g.acc, tile);
 #pragma unroll
       for (int i = 0; i < I; ++i)
 #pragma unroll
-        for (int j = 0; j < J; ++j) to[(i * J + j) * F::THREADS] = acc[i][j];
-      return;
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x4 v = from[((i * J + j) * 4 + q) * F::THREADS];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[i][j][4 * q + r] = v[r];
+          }
     }
-    const float scale = DT == kF32 ? 1.0f : *g.scale;
-#pragma unroll
-    for (int i = 0; i < I; ++i)
-      if (ml + 16 * i < m) {
-#pragma unroll
-        for (int j = 0; j < J; ++j) emit<DT, KIND>(g, scale, ml + 16 * i, nl + 16 * j, acc[i][j]);
-      }
+    wait_loads();
+    barrier();
+    read(0, la0, lb0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    int s = s0;
+    for (; s + 1 < s1; s += 2) {
+      step(la0, lb0, la1, lb1, s);
+      step(la1, lb1, la0, lb0, s + 1);
+    }
+    if (s < s1) step(la0, lb0, la1, lb1, s);
+    wait_loads();
+    barrier();                                     // nobody reads la0 .. lb1 any more
+
+    const int64_t m0 = (int64_t)tm * TM, n0 = (int64_t)tn * TN;
+    const uint32_t tn_done = tn;
+    const int slot_done = slot;
+    const uint32_t tile_done = tile;
+    unit += gridDim.x;
+    const bool more = unit < units;
+    if (more) {                                    // the next unit's loads, meanwhile
+      take(unit);
+      begin();
+    }
+    if (KIND != kXentStats && slot_done >= 0)
+      store_lanes<F>(lanes<F>(g.partial, slot_done), acc);
+    else if (KIND == kXentDx && !g.last)
+      store_lanes<F>(lanes<F>(g.acc, tile_done), acc);
+    else
+      finish<F, KIND>(g, acc, m, m0, n0, tn_done, wm, wn, lane, halves);
+    if (!more) break;
   }
 }
 
@@ -443,22 +578,27 @@ __global__ void __launch_bounds__(F::THREADS) xent_add_kernel(XentTileArgs g) {
   const XentCut& cut = plan.cut;
   const float scale = F::DT == kF32 ? 1.0f : *g.scale;
   const int lane = lane_id(), wave = threadIdx.x >> 6;
-  constexpr int C = F::I * F::J;
+  constexpr int C = F::I * F::J * 4;
   for (uint32_t u = blockIdx.x; u < cut.rest * C; u += gridDim.x) {
     const uint32_t r = u / C;
-    const int i = (int)(u % C) / F::J, j = (int)(u % C) % F::J;
+    const int i = (int)(u % C) / (4 * F::J), j = (int)(u % C) / 4 % F::J, q = (int)(u % 4);
     uint32_t tm, tn;
-    plan.place(cut.whole + r, tm, tn);
-    const int64_t row = (int64_t)tm * F::TM + wave / F::WN * (F::TM / F::WM) + lane % 16 + 16 * i;
-    const int64_t n = (int64_t)tn * F::TN + wave % F::WN * (F::TN / F::WN) + lane / 16 * 4 + 16 * j;
-    if (row >= plan.m) continue;
-    const f32x4* from = reinterpret_cast<const f32x4*>(g.partial) + (int64_t)r * (F::TM * F::TN / 4) +
-                        (u % C) * F::THREADS + threadIdx.x;
-    f32x4 v = from[0];
+    cut.place(cut.whole + r, tm, tn);
+    const int64_t row = (int64_t)tm * F::TM + wave / F::WN * (F::TM / F::WM) + lane % 32 + 32 * i;
+    const int64_t n = (int64_t)tn * F::TN + wave % F::WN * (F::TN / F::WN) + lane / 32 * 4 + 32 * j + 8 * q;
+    const int64_t at = (u % C) * F::THREADS;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    f32x4* sum = nullptr;
+    if constexpr (KIND == kXentDx) {
+      if (!(g.first && g.last)) sum = lanes<F>(g.acc, cut.whole + r) + at;
+      if (!g.first) v = *sum;
+    }
+    const f32x4* from = lanes<F>(g.partial, r) + at;
 #pragma unroll 8
-    for (uint32_t p = 1; p < cut.parts; ++p)
+    for (uint32_t p = 0; p < cut.parts; ++p)
       v += from[(int64_t)(p * cut.rest) * (F::TM * F::TN / 4)];
-    emit<F::DT, KIND>(g, scale, row, n, v);
+    if (KIND == kXentDx && !g.last) *sum = v;
+    else if (row < plan.m) emit<F::DT, KIND>(g, scale, row, n, v);
   }
 }
 
@@ -466,14 +606,14 @@ __global__ void __launch_bounds__(F::THREADS) xent_add_kernel(XentTileArgs g) {
 template <class F, int KIND>
 lowbit_status launch_form_kind(const XentTileArgs& g, hipStream_t s) {
   const TilePlan<F, KIND> plan(g, KIND == kXentDw ? g.k : g.m);
-  // Where fewer rows count, fewer tiles may be whole, and more cut, into SLOTS
-  // parts at most (dx), or the tiles be cut into fewer parts (dw).
-  const uint32_t blocks = KIND == kXentDx   ? plan.cut.tiles + F::SLOTS
-                          : KIND == kXentDw ? plan.cut.whole + plan.cut.rest * plan.cut.parts
-                                            : plan.cut.tiles;
+  // one workgroup for each slot, each taking every SLOTS-th unit (fewer rows
+  // may leave fewer tiles whole and more cut: as many workgroups as tiles do not always do)
+  if (KIND != kXentStats && !g.partial) return LOWBIT_EINVAL;
+  const uint32_t blocks = plan.cut.tiles < F::SLOTS && KIND == kXentStats ? plan.cut.tiles : F::SLOTS;
   const lowbit_status st = launch(&xent_tile_kernel<F, KIND>, blocks, F::THREADS, s, g);
-  if constexpr (KIND == kXentDx || KIND == kXentDw) {
-    if (st == LOWBIT_OK && (KIND == kXentDx || plan.cut.rest))
+  if constexpr (KIND != kXentStats) {
+    // (dw: the same tiles whatever counts; rows cut them into fewer parts at most)
+    if (st == LOWBIT_OK && (KIND != kXentDw || plan.cut.rest))
       return launch(&xent_add_kernel<F, KIND>, 512, F::THREADS, s, g);
   }
   return st;
