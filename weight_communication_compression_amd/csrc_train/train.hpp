@@ -22,10 +22,13 @@ struct DropoutArgs {
 
 constexpr int kJoinMaxCols = 16384;
 struct JoinShape {
-  int threads;              // of a workgroup, which takes whole rows
-  int vecs;                 // vectors of 8 elements per thread: 1 or 2
-  int64_t blocks;
-  int64_t rows_per_block;   // consecutive
+  int threads;              // of a workgroup
+  int lanes;                // of a row: 8 to 64 (several rows a workgroup), or all threads
+  int vecs;                 // vectors of 8 elements per lane: 1 or 2
+  bool ragged;              // the lanes have more elements than a row
+  int64_t runs;             // runs of rows_per_run consecutive rows, each `lanes` lanes'
+  int64_t rows_per_run;
+  int64_t blocks;           // workgroups of threads / lanes runs
 };
 
 struct JoinArgs {
@@ -33,8 +36,8 @@ struct JoinArgs {
   const void *post_w, *post_b, *gate, *pre_w, *pre_b;
   void *x_out, *z;
   float* stats;
-  int64_t rows, rows_per_block, rows_per_gate;
-  int32_t cols;
+  int64_t rows, rows_per_run, rows_per_gate;
+  int32_t cols, lanes;
   float eps, scale;
   uint32_t key, cut;
   float factor;
@@ -44,10 +47,10 @@ struct JoinBackArgs {
   JoinArgs j;
   const void *dx_out, *dz;
   void *df, *dx;
-  // rows of `cols` partial sums, one for each workgroup (two for the gate: the
-  // group that its first row belongs to, the one its last row belongs to)
+  // rows of `cols` partial sums, one for each workgroup (for the gate two for each
+  // run: the group that its first row belongs to, the one its last row belongs to)
   float *part_post_w, *part_post_b, *part_pre_w, *part_pre_b, *part_gate;
-  float* dgate;             // groups that lie within one workgroup's rows
+  float* dgate;             // groups that lie within one run
 };
 
 struct JoinSumArgs {
@@ -55,7 +58,7 @@ struct JoinSumArgs {
   float* out[4];
   const float* part_gate;
   float* dgate;
-  int64_t rows, rows_per_block, rows_per_gate, blocks;
+  int64_t rows, rows_per_run, rows_per_gate, blocks;
   int32_t cols;
   int32_t params;           // how many of part[] there are
 };
@@ -132,8 +135,7 @@ struct XentTileArgs {
   float* partial;            // sums of tiles that are cut along k (dx, dw)
 };
 
-lowbit_status launch_xent_rows(const XentRows& a, hipStream_t s);
-lowbit_status launch_xent_gather(int dt, const XentGather& a, hipStream_t s);
+lowbit_status launch_xent_rows(int dt, const XentRows& r, const XentGather& g, hipStream_t s);
 lowbit_status launch_xent_pack(int dt, const XentPack& a, hipStream_t s);
 lowbit_status launch_xent_join(const XentJoin& a, hipStream_t s);
 lowbit_status launch_xent_tile_bf16(int form, int kind, const XentTileArgs& a, hipStream_t s);

@@ -76,7 +76,8 @@ lowbit_status check_join(const lowbit_join_params* p, bool gate) {
 JoinArgs join_args(const lowbit_join_params* p, const JoinShape& g) {
   JoinArgs a{};
   a.rows = p->rows;
-  a.rows_per_block = g.rows_per_block;
+  a.rows_per_run = g.rows_per_run;
+  a.lanes = g.lanes;
   a.rows_per_gate = p->rows_per_gate;
   a.cols = (int32_t)p->cols;
   a.eps = p->eps;
@@ -87,19 +88,17 @@ JoinArgs join_args(const lowbit_join_params* p, const JoinShape& g) {
   return a;
 }
 
-// partial sums: one row for each workgroup and parameter, two for the gate
-int64_t join_part_bytes(const JoinShape& g, int64_t cols, int rows_each) {
-  return (g.blocks * rows_each * cols * 4 + 255) / 256 * 256;
-}
+// partial sums: `rows` rows of a parameter or the gate
+int64_t join_part_bytes(int64_t rows, int64_t cols) { return (rows * cols * 4 + 255) / 256 * 256; }
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30, kMaxVocab = ((int64_t)1 << 31) - 1;
 constexpr int64_t kMaxHidden = (int64_t)1 << 20;
 // d of a piece of the vocabulary takes at most this much, so that the loss
 // needs far less than its logits; all of the vocabulary in one piece where it fits
 constexpr int64_t kXentPieceBytes = (int64_t)512 << 20;
-// copies of w's rows, where they are no multiples of 16 bytes; 64 Mi keep the
-// chip busy for several rounds of tiles in each piece
-constexpr int64_t kXentPackBytes = (int64_t)64 << 20;
+// copies of w's rows, where they are no multiples of 16 bytes: what the last
+// level of cache still holds when the products read it
+constexpr int64_t kXentPackBytes = (int64_t)128 << 20;
 constexpr int64_t kXentTiles = (int64_t)1 << 22;       // of a launch, at most
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -193,8 +192,6 @@ lowbit_status xent_rows(const XentPlan& w, const lowbit_xent_params* p, void* ws
   r.count = at<int32_t>(ws, w.count);
   r.scale = at<float>(ws, w.count + 4);
   r.padded = w.padded;
-  const lowbit_status st = launch_xent_rows(r, s);
-  if (st != LOWBIT_OK) return st;
   XentGather g{};
   g.x = x;
   g.xc = at<char>(ws, w.xc);
@@ -205,7 +202,7 @@ lowbit_status xent_rows(const XentPlan& w, const lowbit_xent_params* p, void* ws
   g.padded = w.padded;
   g.hidden = (int32_t)p->hidden;
   g.ld = (int32_t)w.ld;
-  return launch_xent_gather(p->type, g, s);
+  return launch_xent_rows(p->type, r, g, s);
 }
 
 lowbit_status xent_product(const lowbit_xent_params* p, const XentPlan& w, int kind,
@@ -302,7 +299,7 @@ int64_t lowbit_block_join_backward_workspace(const lowbit_join_params* p) {
   if (check_join(p, false) != LOWBIT_OK) return -1;
   if (p->rows == 0) return 0;
   const JoinShape g = join_shape(p->rows, (int)p->cols, true);
-  return 4 * join_part_bytes(g, p->cols, 1) + join_part_bytes(g, p->cols, 2);
+  return 4 * join_part_bytes(g.blocks, p->cols) + join_part_bytes(2 * g.runs, p->cols);
 }
 
 lowbit_status lowbit_block_join_backward(const void* dx_out, const void* dz, const void* f,
@@ -359,12 +356,12 @@ lowbit_status lowbit_block_join_backward(const void* dx_out, const void* dz, con
       sums.part[sums.params] = *part[k];
       sums.out[sums.params++] = out[k];
     }
-    at += join_part_bytes(g, p->cols, 1);
+    at += join_part_bytes(g.blocks, p->cols);
   }
   b.part_gate = reinterpret_cast<float*>(at);
   sums.part_gate = b.part_gate;
   sums.dgate = dgate;
-  sums.rows_per_block = g.rows_per_block;
+  sums.rows_per_run = g.rows_per_run;
   sums.blocks = g.blocks;
   const lowbit_status st = launch_join_back(p->block_type, p->stream_type, p->param_type,
                                             p->norm == LOWBIT_NORM_LAYER, g, b, stream);

@@ -110,23 +110,31 @@ __device__ __forceinline__ uint32_t draw_word(const HiMix& h, uint32_t q) {
 __device__ __forceinline__ bool keeps_lo(uint32_t word, uint32_t cut) { return (word & 0xFFFFu) >= cut; }
 __device__ __forceinline__ bool keeps_hi(uint32_t word, uint32_t cut) { return (word >> 16) >= cut; }
 
-// Sums of N values over a workgroup of `waves` waves, the waves' parts added in
-// order; every lane gets the result.  `slot` is LDS for N * 16 values; a
-// caller that alternates two slots needs no other barrier.
-template <int N>
-__device__ __forceinline__ void block_sum(float* v, float* slot, int waves) {
+// Sums of N values over the L lanes that share a row: 8, 16, 32 or 64 of a wave, or
+// whole waves of a workgroup, whose parts are added in order; every lane gets
+// the result.  `slot` is LDS for N * 16 values; a caller that alternates two
+// slots needs no other barrier.  (Loads and stores to memory may stay under way.)
+// SUB: L is less than 64.
+template <int N, bool SUB>
+__device__ __forceinline__ void row_sum(float* v, float* slot, int L) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = group_reduce<64, true>(v[i]);
-  if (waves == 1) return;
+  for (int i = 0; i < N; ++i) {
+    if constexpr (SUB)
+      v[i] = L == 8 ? group_reduce<8, true>(v[i]) : L == 16 ? group_reduce<16, true>(v[i])
+                                                            : group_reduce<32, true>(v[i]);
+    else
+      v[i] = group_reduce<64, true>(v[i]);
+  }
+  if (SUB || L == 64) return;
   const int wave = threadIdx.x >> 6;
   if (lane_id() == 0) {
 #pragma unroll
     for (int i = 0; i < N; ++i) slot[wave * N + i] = v[i];
   }
-  __syncthreads();
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = slot[i];
-  for (int w = 1; w < waves; ++w) {
+  for (int w = 1; w < L >> 6; ++w) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += slot[w * N + i];
   }

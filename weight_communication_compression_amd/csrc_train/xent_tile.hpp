@@ -262,8 +262,12 @@ __device__ __forceinline__ void spread_loads() {
 
 // A tile's sums as the lanes hold them, TM x TN values in a row.
 template <class F>
+__device__ __forceinline__ f32x4* tile_base(float* base, int64_t tile) {
+  return reinterpret_cast<f32x4*>(base) + tile * (F::TM * F::TN / 4);
+}
+template <class F>
 __device__ __forceinline__ f32x4* lanes(float* base, int64_t tile) {
-  return reinterpret_cast<f32x4*>(base) + tile * (F::TM * F::TN / 4) + threadIdx.x;
+  return tile_base<F>(base, tile) + threadIdx.x;
 }
 template <class F>
 __device__ __forceinline__ void store_lanes(f32x4* to, const f32x16 (&acc)[F::I][F::J]) {
@@ -571,34 +575,45 @@ __global__ void __launch_bounds__(F::THREADS, F::SLOTS * F::W / 1024) xent_tile_
   }
 }
 
-// The cut tiles: their parts' sums added in order.
+// The cut tiles: their parts' sums added, every fourth part by one of four waves,
+// and the waves' sums in order.  A unit is 64 lanes' four values.
 template <class F, int KIND>
-__global__ void __launch_bounds__(F::THREADS) xent_add_kernel(XentTileArgs g) {
-  const TilePlan<F, KIND> plan(g, *g.count);
+__global__ void __launch_bounds__(256) xent_add_kernel(XentTileArgs g) {
+  __shared__ f32x4 sums[4][64];
+  const TilePlan<F, KIND> plan(g, __builtin_amdgcn_readfirstlane(*g.count));
   const XentCut& cut = plan.cut;
   const float scale = F::DT == kF32 ? 1.0f : *g.scale;
-  const int lane = lane_id(), wave = threadIdx.x >> 6;
-  constexpr int C = F::I * F::J * 4;
+  const int lane = lane_id(), mine = threadIdx.x >> 6;
+  constexpr uint32_t C = F::I * F::J * 4 * F::W;
   for (uint32_t u = blockIdx.x; u < cut.rest * C; u += gridDim.x) {
-    const uint32_t r = u / C;
-    const int i = (int)(u % C) / (4 * F::J), j = (int)(u % C) / 4 % F::J, q = (int)(u % 4);
-    uint32_t tm, tn;
-    cut.place(cut.whole + r, tm, tn);
-    const int64_t row = (int64_t)tm * F::TM + wave / F::WN * (F::TM / F::WM) + lane % 32 + 32 * i;
-    const int64_t n = (int64_t)tn * F::TN + wave % F::WN * (F::TN / F::WN) + lane / 32 * 4 + 32 * j + 8 * q;
-    const int64_t at = (u % C) * F::THREADS;
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    const uint32_t r = u / C, in = u % C;
+    const int wave = in % F::W, q = in / F::W % 4;
+    const int i = in / F::W / 4 / F::J, j = in / F::W / 4 % F::J;
+    const int64_t at = (int64_t)(in / F::W) * F::THREADS + wave * 64 + lane;
     f32x4* sum = nullptr;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
     if constexpr (KIND == kXentDx) {
-      if (!(g.first && g.last)) sum = lanes<F>(g.acc, cut.whole + r) + at;
-      if (!g.first) v = *sum;
+      if (!(g.first && g.last)) sum = tile_base<F>(g.acc, cut.whole + r) + at;
+      if (!g.first && mine == 0) v = *sum;
     }
-    const f32x4* from = lanes<F>(g.partial, r) + at;
+    const f32x4* from = tile_base<F>(g.partial, r) + at;
+    const int64_t next = (int64_t)cut.rest * (F::TM * F::TN / 4);
 #pragma unroll 8
-    for (uint32_t p = 0; p < cut.parts; ++p)
-      v += from[(int64_t)(p * cut.rest) * (F::TM * F::TN / 4)];
-    if (KIND == kXentDx && !g.last) *sum = v;
-    else if (row < plan.m) emit<F::DT, KIND>(g, scale, row, n, v);
+    for (uint32_t p = mine; p < cut.parts; p += 4) v += from[p * next];
+    sums[mine][lane] = v;
+    __syncthreads();
+    if (mine == 0) {
+#pragma unroll
+      for (int w = 1; w < 4; ++w) v += sums[w][lane];
+      uint32_t tm, tn;
+      cut.place(cut.whole + r, tm, tn);
+      const int64_t row = (int64_t)tm * F::TM + wave / F::WN * (F::TM / F::WM) + lane % 32 + 32 * i;
+      const int64_t n = (int64_t)tn * F::TN + wave % F::WN * (F::TN / F::WN) + lane / 32 * 4 +
+                        32 * j + 8 * q;
+      if (KIND == kXentDx && !g.last) *sum = v;
+      else if (row < plan.m) emit<F::DT, KIND>(g, scale, row, n, v);
+    }
+    __syncthreads();
   }
 }
 
@@ -612,9 +627,11 @@ lowbit_status launch_form_kind(const XentTileArgs& g, hipStream_t s) {
   const uint32_t blocks = plan.cut.tiles < F::SLOTS && KIND == kXentStats ? plan.cut.tiles : F::SLOTS;
   const lowbit_status st = launch(&xent_tile_kernel<F, KIND>, blocks, F::THREADS, s, g);
   if constexpr (KIND != kXentStats) {
-    // (dw: the same tiles whatever counts; rows cut them into fewer parts at most)
-    if (st == LOWBIT_OK && (KIND != kXentDw || plan.cut.rest))
-      return launch(&xent_add_kernel<F, KIND>, 512, F::THREADS, s, g);
+    // Nothing is cut where k is too short; of dw the tiles are the same whatever
+    // counts, and fewer rows cut them into fewer parts at most.
+    const bool cuts = KIND == kXentDw ? plan.cut.rest != 0 : plan.steps(plan.k) >= xent_least(KIND);
+    if (st == LOWBIT_OK && cuts)
+      return launch(&xent_add_kernel<F, KIND>, 2048, 256, s, g);
   }
   return st;
 }

@@ -151,7 +151,14 @@ def _dev(t: torch.Tensor, what: str) -> int:
     return t.data_ptr()
 
 
+# The current stream's handle without the Stream object around it (0.15 instead of
+# 2 us a call); torch versions without it take the long way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(t: torch.Tensor) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
