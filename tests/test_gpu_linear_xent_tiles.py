@@ -23,6 +23,8 @@ CASES = [
     (40, 40000, 520, "bf16", 0.1),
     (1300, 2000, 1040, "f32", 0.2),      # cut along k, of logits too
     (90, 20000, 261, "f32", 0.1),        # rows of w copied
+    (19, 2644, 3672, "f32", 0.2),        # the loss cut along k
+    (300, 2000, 3001, "bf16", 0.2),      # and with rows of w copied
 ]
 
 

@@ -8,8 +8,9 @@ using namespace lowbit;
 extern "C" int check(int form, int kind, int64_t m, int64_t most_m, int64_t n, uint32_t k_steps,
                      uint32_t most_steps, unsigned char* seen, int64_t seen_size) {
   const XentForm& f = kXentForms[form];
-  const XentCut cut(m, n, k_steps, f.tm, f.tn, f.slots, xent_least(kind));
-  if ((int64_t)cut.rest * cut.parts * (cut.parts > 1) > xent_slots(f, most_m, n, most_steps)) return 1;
+  const XentCut cut(m, n, k_steps, f.tm, f.tn, f.slots,
+                    xent_may_cut(f, kind, most_m, n, most_steps));
+  if ((int64_t)cut.rest * cut.parts * (cut.parts > 1) > xent_slots(f, kind, most_m, n, most_steps)) return 1;
   if (cut.whole + cut.rest != cut.tiles || cut.tiles != cut.across * cut.down) return 2;
   if ((int64_t)cut.tiles * k_steps > seen_size) return 3;
   for (uint32_t u = 0; u < cut.units(); ++u) {

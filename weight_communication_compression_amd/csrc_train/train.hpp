@@ -132,7 +132,8 @@ struct XentTileArgs {
   int64_t ldo;
   float* acc;                // dx over several pieces: their sum so far, tile by tile
   int32_t first, last;       // piece of the vocabulary
-  float* partial;            // sums of tiles that are cut along k (dx, dw)
+  float* partial;            // sums of the parts of tiles that are cut along k
+  int32_t may_cut;           // whether there are any
 };
 
 lowbit_status launch_xent_rows(int dt, const XentRows& r, const XentGather& g, hipStream_t s);
@@ -142,6 +143,6 @@ lowbit_status launch_xent_tile_bf16(int form, int kind, const XentTileArgs& a, h
 lowbit_status launch_xent_tile_f32(int form, int kind, const XentTileArgs& a, hipStream_t s);
 
 constexpr int64_t kXentPad = 256;  // rows and pieces of the vocabulary: multiples of every tile's
-int xent_form(int dt, int kind, int64_t m, int64_t n);
+int xent_form(int dt, int kind, int64_t m, int64_t n, int64_t k);
 
 }  // namespace lowbit

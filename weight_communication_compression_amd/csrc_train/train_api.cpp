@@ -113,20 +113,23 @@ struct XentPlan {
   int64_t padded, ld, parts, piece, pieces;
   bool packs;                              // w's rows are copied to rows of ld
   int form[4];                             // of each kind of product, in every piece
+  bool cuts[4];                            // whether it may cut tiles along k
   int64_t pos, map, info, count, xc, wc, part, hit, d, acc, partial, bytes;
 };
 
-int64_t xent_partial_bytes(int64_t es, const XentForm& f, int64_t m, int64_t n, int64_t k) {
-  return xent_slots(f, m, n, xent_steps(k, (int)es)) * f.tm * f.tn * 4;
-}
-
 XentPlan xent_plan(const lowbit_xent_params* p, bool backward) {
   XentPlan w{};
-  const int64_t es = p->type == LOWBIT_F32 ? 4 : 2;
+  const int es = p->type == LOWBIT_F32 ? 4 : 2;
   auto take = [&](int64_t bytes) {
     const int64_t at = w.bytes;
     w.bytes += up(bytes, 256);
     return at;
+  };
+  // whether a product in its form cuts tiles, and the room for their parts' sums
+  auto room = [&](int kind, int64_t m, int64_t n, int64_t k) {
+    const XentForm& f = kXentForms[w.form[kind]];
+    w.cuts[kind] = xent_may_cut(f, kind, m, n, xent_steps(k, es));
+    return xent_slots(f, kind, m, n, xent_steps(k, es)) * f.tm * f.tn * 4;
   };
   w.padded = up(p->rows > 0 ? p->rows : 1, kXentPad);
   w.ld = up(p->hidden, 16 / es);
@@ -140,7 +143,7 @@ XentPlan xent_plan(const lowbit_xent_params* p, bool backward) {
   auto cut = [&](int64_t cols) {
     if (cols < most) most = cols > kXentPad ? cols / kXentPad * kXentPad : kXentPad;
   };
-  w.form[kXentStats] = xent_form(p->type, kXentStats, p->rows, p->vocab);
+  w.form[kXentStats] = xent_form(p->type, kXentStats, p->rows, p->vocab, p->hidden);
   const XentForm& f = kXentForms[w.form[kXentStats]];
   if (backward) cut(std::max(kXentPieceBytes / (w.padded * es), (int64_t)1024));
   if (w.packs) cut(std::max(kXentPackBytes / (w.ld * es), (int64_t)1024));
@@ -148,23 +151,23 @@ XentPlan xent_plan(const lowbit_xent_params* p, bool backward) {
   w.pieces = (p->vocab + most - 1) / most;
   w.piece = up((p->vocab + w.pieces - 1) / w.pieces, kXentPad);
   w.pieces = (p->vocab + w.piece - 1) / w.piece;
+  const int64_t cols = w.piece < p->vocab ? w.piece : p->vocab;
   if (w.packs) w.wc = take(w.piece * w.ld * es);
   if (backward) {
     w.d = take(w.padded * w.piece * es);
-    const int64_t cols = w.piece < p->vocab ? w.piece : p->vocab;
-    w.form[kXentProb] = xent_form(p->type, kXentProb, p->rows, cols);
-    w.form[kXentDx] = xent_form(p->type, kXentDx, p->rows, p->hidden);
-    w.form[kXentDw] = xent_form(p->type, kXentDw, cols, p->hidden);
+    w.form[kXentProb] = xent_form(p->type, kXentProb, p->rows, cols, p->hidden);
+    w.form[kXentDx] = xent_form(p->type, kXentDx, p->rows, p->hidden, cols);
+    w.form[kXentDw] = xent_form(p->type, kXentDw, cols, p->hidden, p->rows);
     const XentForm& fx = kXentForms[w.form[kXentDx]];
     if (w.pieces > 1) w.acc = take(up(p->rows, fx.tm) * up(p->hidden, fx.tn) * 4);
-    w.partial = take(std::max(
-        {xent_partial_bytes(es, kXentForms[w.form[kXentProb]], p->rows, cols, p->hidden),
-         xent_partial_bytes(es, fx, p->rows, p->hidden, cols),
-         xent_partial_bytes(es, kXentForms[w.form[kXentDw]], cols, p->hidden, p->rows)}));
+    w.partial = take(std::max({room(kXentProb, p->rows, cols, p->hidden),
+                               room(kXentDx, p->rows, p->hidden, cols),
+                               room(kXentDw, cols, p->hidden, p->rows)}));
   } else {
     w.parts = (p->vocab + f.tn - 1) / f.tn;
     w.part = take(p->rows * w.parts * 8);
     w.hit = take(w.padded * 4);
+    w.partial = take(room(kXentStats, p->rows, cols, p->hidden));
   }
   return w;
 }
@@ -206,7 +209,8 @@ lowbit_status xent_rows(const XentPlan& w, const lowbit_xent_params* p, void* ws
 }
 
 lowbit_status xent_product(const lowbit_xent_params* p, const XentPlan& w, int kind,
-                           const XentTileArgs& t, hipStream_t s) {
+                           XentTileArgs& t, hipStream_t s) {
+  t.may_cut = w.cuts[kind];
   return p->type == LOWBIT_F32 ? launch_xent_tile_f32(w.form[kind], kind, t, s)
                                : launch_xent_tile_bf16(w.form[kind], kind, t, s);
 }
@@ -240,14 +244,42 @@ lowbit_status xent_logits(const XentPlan& w, const lowbit_xent_params* p, void* 
 
 }  // namespace
 
-// The largest form that the rows fill, unless it leaves too few tiles.
-int xent_form(int dt, int kind, int64_t m, int64_t n) {
-  int f = m > 128 && dt == LOWBIT_BF16 ? 0 : m > 64 ? 1 : m > 32 ? 2 : 3;
-  const int64_t want = kind == kXentStats || kind == kXentProb ? 192 : 64;
-  while (f < 3 && ((m + kXentForms[f].tm - 1) / kXentForms[f].tm) *
-                          ((n + kXentForms[f].tn - 1) / kXentForms[f].tn) < want)
-    ++f;
-  return f;
+// The form that takes least time by what its steps and tiles were measured to take
+// (us): a step of k with all slots taken, a step at the least, and what a tile takes
+// besides (the parts of the softmax; d, dx and dw, which are written).  It picks
+// the fastest form, or one within 10 % of it, at sizes from 1 x 1690 x 640 to
+// 8192 x 1000 x 4096; beside the best the next form loses 5 to 60 %.
+int xent_form(int dt, int kind, int64_t m, int64_t n, int64_t k) {
+  static const double full[2][4] = {{0, 4.6, 3.36, 2.27}, {1.73, 1.19, 1.15, 1.25}};
+  static const double least[2][4] = {{0, 3.6, 2.1, 1.2}, {1.3, 0.5, 0.4, 0.25}};
+  static const double tile[2][4] = {{5.0, 3.0, 2.5, 3.0}, {13.0, 4.5, 3.8, 3.0}};
+  const bool bf16 = dt != LOWBIT_F32;
+  m = std::min(m, (int64_t)1 << 20);       // (beyond it the answer is the same, and the counts fit)
+  n = std::min(n, (int64_t)1 << 20);
+  const uint32_t steps = xent_steps(k, bf16 ? 2 : 4);
+  int best = 3;
+  double best_time = 0.0;
+  for (int i = 3; i >= (bf16 ? 0 : 1); --i) {
+    const XentForm& f = kXentForms[i];
+    const double own = tile[kind != kXentStats][i];
+    const XentCut cut(m > 0 ? m : 1, n, steps, f.tm, f.tn, f.slots,
+                      xent_may_cut(f, kind, m, n, steps));
+    auto round = [&](double count, double each) {
+      const double share = count / f.slots;
+      return each * std::max(least[bf16][i], full[bf16][i] * share) + own * std::max(0.5, share);
+    };
+    double time = cut.whole / f.slots * round(f.slots, steps);
+    if (cut.whole % f.slots) time += round(cut.whole % f.slots, steps);
+    if (cut.rest) {                        // and the kernel that adds the parts' sums, at 4 TB/s
+      const double units = (double)cut.rest * cut.parts;
+      time += round(units, (double)steps / cut.parts) + 5.0 + units * f.tm * f.tn * 8 / 4e6;
+    }
+    if (i == 3 || time < best_time) {
+      best = i;
+      best_time = time;
+    }
+  }
+  return best;
 }
 
 }  // namespace lowbit
@@ -390,6 +422,7 @@ lowbit_status lowbit_linear_xent(const void* x, const void* w, const int64_t* ta
     t.part = at<float2>(workspace, q.part);
     t.hit = at<float>(workspace, q.hit);
     t.parts = (int32_t)q.parts;
+    t.partial = at<float>(workspace, q.partial);
     t.part0 = (int32_t)(t.col0 / kXentForms[q.form[kXentStats]].tn);
     if (st == LOWBIT_OK) st = xent_product(p, q, kXentStats, t, stream);
   }

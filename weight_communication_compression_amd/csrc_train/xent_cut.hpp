@@ -32,10 +32,15 @@ inline LOWBIT_HD uint32_t xent_steps(int64_t k, int elem_size) {
   return (uint32_t)((k * elem_size + kXentRowBytes - 1) / kXentRowBytes);
 }
 
-// The steps of k below which a kind's tiles are not cut: the forward call's
-// never (its workspace would grow by what it saves least: one round of many).
-inline LOWBIT_HD uint32_t xent_least(int kind) {
-  return kind == kXentStats ? 0xFFFFFFFFu : kind == kXentProb ? 32u : 8u;
+// Whether a product of up to m rows (dw: k_steps) may cut tiles along k: not where
+// the second kernel would take longer than the steps it saves, and the loss only
+// where there are fewer tiles than slots: with more its workspace would grow by
+// 64 MiB for what saves least, half a round of many.
+inline bool xent_may_cut(const XentForm& f, int kind, int64_t m, int64_t n, uint32_t k_steps) {
+  const int64_t tiles = (m + f.tm - 1) / f.tm * ((n + f.tn - 1) / f.tn);
+  return kind == kXentStats  ? k_steps >= 24 && tiles < f.slots
+         : kind == kXentProb ? k_steps >= 32
+                             : k_steps >= 8;
 }
 
 // What one workgroup takes at a time: a tile, or a part of one (slot >= 0), and
@@ -54,12 +59,12 @@ struct XentCut {
   uint32_t across, down, tiles, whole;           // whole: tiles that are not cut
   uint32_t rest, parts;                          // tiles that are, each into `parts`
   LOWBIT_HD XentCut(int64_t m, int64_t n, uint32_t k_steps, uint32_t tm, uint32_t tn,
-                    uint32_t slots, uint32_t least) {
+                    uint32_t slots, bool may_cut) {
     across = ((uint32_t)n + tn - 1) / tn;
     down = ((uint32_t)m + tm - 1) / tm;
     tiles = across * down;
     rest = tiles % slots;
-    parts = rest && k_steps >= least ? slots / rest : 1;
+    parts = rest && may_cut ? slots / rest : 1;
     if (parts > k_steps / 4) parts = k_steps / 4;
     if (parts <= 1) {
       parts = 1;
@@ -103,9 +108,9 @@ struct XentCut {
 
 // How many parts' sums a product needs room for, of tm x tn values each, where
 // up to m rows count and k is at most k_steps.
-inline int64_t xent_slots(const XentForm& f, int64_t m, int64_t n, uint32_t k_steps) {
+inline int64_t xent_slots(const XentForm& f, int kind, int64_t m, int64_t n, uint32_t k_steps) {
+  if (!xent_may_cut(f, kind, m, n, k_steps)) return 0;
   const int64_t quarter = k_steps / 4;
-  if (quarter < 2) return 0;
   const int64_t tiles = (m + f.tm - 1) / f.tm * ((n + f.tn - 1) / f.tn);
   return tiles < f.slots && tiles * quarter < f.slots ? tiles * quarter : f.slots;
 }

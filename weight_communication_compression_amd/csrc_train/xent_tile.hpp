@@ -174,7 +174,7 @@ struct TilePlan {
   // count: rows that count (device), or the most there can be (host)
   __host__ __device__ TilePlan(const XentTileArgs& g, int64_t count)
       : cut(KIND == kXentDw ? g.m : count, g.n, steps(KIND == kXentDw ? count : g.k), F::TM, F::TN,
-            F::SLOTS, xent_least(KIND)),
+            F::SLOTS, g.may_cut != 0),
         m(KIND == kXentDw ? g.m : count), k(KIND == kXentDw ? count : g.k) {}
   static __host__ __device__ uint32_t steps(int64_t k) {
     return xent_steps(k, elem_size<F::DT>());
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(F::THREADS, F::SLOTS * F::W / 1024) xent_tile_
       take(unit);
       begin();
     }
-    if (KIND != kXentStats && slot_done >= 0)
+    if (slot_done >= 0)
       store_lanes<F>(lanes<F>(g.partial, slot_done), acc);
     else if (KIND == kXentDx && !g.last)
       store_lanes<F>(lanes<F>(g.acc, tile_done), acc);
@@ -617,23 +617,58 @@ __global__ void __launch_bounds__(256) xent_add_kernel(XentTileArgs g) {
   }
 }
 
+// The same for tiles of logits whose rows' maxima and sums are wanted: a workgroup
+// a tile, whole in registers again.
+template <class F>
+__global__ void __launch_bounds__(F::THREADS) xent_add_stats_kernel(XentTileArgs g) {
+  __shared__ float2 halves[F::WN * F::TM];
+  const TilePlan<F, kXentStats> plan(g, __builtin_amdgcn_readfirstlane(*g.count));
+  const XentCut& cut = plan.cut;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t r = blockIdx.x;
+  if (r >= cut.rest) return;
+  f32x16 acc[F::I][F::J];
+#pragma unroll
+  for (int i = 0; i < F::I; ++i)
+#pragma unroll
+    for (int j = 0; j < F::J; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+#pragma unroll 2
+  for (uint32_t p = 0; p < cut.parts; ++p) {
+    const f32x4* from = lanes<F>(g.partial, (int64_t)p * cut.rest + r);
+#pragma unroll
+    for (int i = 0; i < F::I; ++i)
+#pragma unroll
+      for (int j = 0; j < F::J; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 v = from[((i * F::J + j) * 4 + q) * F::THREADS];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
+        }
+  }
+  uint32_t tm, tn;
+  cut.place(cut.whole + r, tm, tn);
+  finish<F, kXentStats>(g, acc, plan.m, (int64_t)tm * F::TM, (int64_t)tn * F::TN, tn, wave / F::WN,
+                        wave % F::WN, lane, halves);
+}
+
 // g.m, and g.k for dw: the most rows that may count.
 template <class F, int KIND>
 lowbit_status launch_form_kind(const XentTileArgs& g, hipStream_t s) {
   const TilePlan<F, KIND> plan(g, KIND == kXentDw ? g.k : g.m);
+  if (g.may_cut && !g.partial) return LOWBIT_EINVAL;
   // one workgroup for each slot, each taking every SLOTS-th unit (fewer rows
   // may leave fewer tiles whole and more cut: as many workgroups as tiles do not always do)
-  if (KIND != kXentStats && !g.partial) return LOWBIT_EINVAL;
-  const uint32_t blocks = plan.cut.tiles < F::SLOTS && KIND == kXentStats ? plan.cut.tiles : F::SLOTS;
+  const uint32_t blocks = plan.cut.tiles < F::SLOTS && !g.may_cut ? plan.cut.tiles : F::SLOTS;
   const lowbit_status st = launch(&xent_tile_kernel<F, KIND>, blocks, F::THREADS, s, g);
-  if constexpr (KIND != kXentStats) {
-    // Nothing is cut where k is too short; of dw the tiles are the same whatever
-    // counts, and fewer rows cut them into fewer parts at most.
-    const bool cuts = KIND == kXentDw ? plan.cut.rest != 0 : plan.steps(plan.k) >= xent_least(KIND);
-    if (st == LOWBIT_OK && cuts)
-      return launch(&xent_add_kernel<F, KIND>, 2048, 256, s, g);
-  }
-  return st;
+  if (st != LOWBIT_OK || !g.may_cut) return st;
+  if (KIND == kXentDw && plan.cut.rest == 0) return st;    // (the same tiles whatever counts)
+  if constexpr (KIND == kXentStats)        // (fewer tiles than slots, all of them cut or none)
+    return launch(&xent_add_stats_kernel<F>, plan.cut.tiles, F::THREADS, s, g);
+  else
+    return launch(&xent_add_kernel<F, KIND>, 2048, 256, s, g);
 }
 
 template <class F>
