@@ -13,6 +13,7 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2_2 __attribute__((ext_vector_type(2), aligned(2)));
 #define LOWBIT_LDS __attribute__((address_space(3)))
 
@@ -279,17 +280,50 @@ __device__ __forceinline__ void store_lanes(f32x4* to, const f32x16 (&acc)[F::I]
       for (int q = 0; q < 4; ++q) to[((i * F::J + j) * 4 + q) * F::THREADS] = quad(acc[i][j], q);
 }
 
-// What becomes of a tile's sums.  halves: [WN][TM] in LDS.
+// LDS beside the two buffers: the row parts of the waves (stats), or 32 rows of 64
+// columns of each wave's outputs.
+template <class F, int KIND>
+struct Side {
+  static constexpr bool ROWS = KIND != kXentStats && F::DT == kBF16 && F::J == 2;
+  static constexpr int BYTES = KIND == kXentStats ? F::WN * F::TM * 8 : ROWS ? F::W * 4096 : 16;
+};
+
+// 32 rows by 64 columns of bfloat16 outputs, which the lanes hold as in the tile
+// kernel, through LDS (pieces of 16 bytes permuted by the row), so that each store
+// writes whole lines: to(row, column) is where eight columns go, or null.
+// Straight from the registers a store reaches 16 bytes of 32 rows each.
+template <typename To>
+__device__ __forceinline__ void store_rows(char* lds, int lane, const f32x16& a, const f32x16& b,
+                                           To to) {
+  const int r = lane % 32, h = lane / 32;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const f32x4 v = quad(q < 4 ? a : b, q % 4);
+    *reinterpret_cast<u32x2*>(lds + r * 128 + (q ^ (r & 7)) * 16 + h * 8) =
+        (u32x2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int row = k * 8 + lane / 8, c = lane % 8;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(lds + row * 128 + (c ^ (row & 7)) * 16);
+    uint16_t* p = to(row, c * 8);
+    if (p) *reinterpret_cast<u32x4_2*>(p) = v;
+  }
+}
+
+// What becomes of a tile's sums.
 template <class F, int KIND>
 __device__ __forceinline__ void finish(const XentTileArgs& g, f32x16 (&acc)[F::I][F::J], int64_t m,
                                        int64_t m0, int64_t n0, uint32_t tn, int wm, int wn, int lane,
-                                       float2* halves) {
+                                       char* side) {
   constexpr int DT = F::DT, TM = F::TM, TN = F::TN, I = F::I, J = F::J;
   const int64_t ml = m0 + wm * (TM / F::WM) + lane % 32;          // + 32 i
   const int64_t nl = n0 + wn * (TN / F::WN) + lane / 32 * 4;      // + 32 j + at(r)
   const bool inside = n0 + TN <= g.n;
   auto at = [](int r) { return r / 4 * 8 + r % 4; };
+  char* const mine = side + (wm * F::WN + wn) * 4096;             // (Side::ROWS)
   if constexpr (KIND == kXentStats) {
+    float2* const halves = reinterpret_cast<float2*>(side);       // [WN][TM]
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       const int64_t row = ml + 32 * i;
@@ -363,6 +397,13 @@ __device__ __forceinline__ void finish(const XentTileArgs& g, f32x16 (&acc)[F::I
           for (int r = 0; r < 16; ++r)
             if (target == 32 * j + at(r) && nl + target < g.n) acc[i][j][r] -= own;
       }
+      if constexpr (Side<F, KIND>::ROWS) {
+        uint16_t* const d0 = static_cast<uint16_t*>(g.out) +
+                             (m0 + wm * (TM / F::WM) + 32 * i) * g.ldo + n0 + wn * (TN / F::WN);
+        store_rows(mine, lane, acc[i][0], acc[i][1],
+                   [&](int r, int c) { return d0 + r * g.ldo + c; });
+        continue;
+      }
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -377,6 +418,21 @@ __device__ __forceinline__ void finish(const XentTileArgs& g, f32x16 (&acc)[F::I
     }
   } else {
     const float scale = DT == kF32 ? 1.0f : *g.scale;
+    if constexpr (Side<F, KIND>::ROWS) {
+      if (inside) {
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+          const int64_t first = m0 + wm * (TM / F::WM) + 32 * i;
+          uint16_t* const out = static_cast<uint16_t*>(g.out) + n0 + wn * (TN / F::WN);
+          store_rows(mine, lane, acc[i][0] * scale, acc[i][1] * scale, [&](int r, int c) {
+            const int64_t row = first + r;
+            return row < m ? out + (KIND == kXentDx ? (int64_t)g.map[row] : row) * g.ldo + c
+                           : nullptr;
+          });
+        }
+        return;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       const int64_t row = ml + 32 * i;
@@ -420,7 +476,7 @@ __global__ void __launch_bounds__(F::THREADS, F::SLOTS * F::W / 1024) xent_tile_
   __shared__ __attribute__((aligned(1024))) char lb0[TN * kRowBytes];
   __shared__ __attribute__((aligned(1024))) char la1[TM * kRowBytes];
   __shared__ __attribute__((aligned(1024))) char lb1[TN * kRowBytes];
-  __shared__ float2 halves[KIND == kXentStats ? F::WN * TM : 1];
+  __shared__ __attribute__((aligned(16))) char side[Side<F, KIND>::BYTES];
   const TilePlan<F, KIND> plan(g, __builtin_amdgcn_readfirstlane(*g.count));
   const XentCut& cut = plan.cut;
   const int64_t m = plan.m, k = plan.k;
@@ -570,7 +626,7 @@ __global__ void __launch_bounds__(F::THREADS, F::SLOTS * F::W / 1024) xent_tile_
     else if (KIND == kXentDx && !g.last)
       store_lanes<F>(lanes<F>(g.acc, tile_done), acc);
     else
-      finish<F, KIND>(g, acc, m, m0, n0, tn_done, wm, wn, lane, halves);
+      finish<F, KIND>(g, acc, m, m0, n0, tn_done, wm, wn, lane, side);
     if (!more) break;
   }
 }
@@ -621,7 +677,7 @@ __global__ void __launch_bounds__(256) xent_add_kernel(XentTileArgs g) {
 // a tile, whole in registers again.
 template <class F>
 __global__ void __launch_bounds__(F::THREADS) xent_add_stats_kernel(XentTileArgs g) {
-  __shared__ float2 halves[F::WN * F::TM];
+  __shared__ __attribute__((aligned(16))) char side[Side<F, kXentStats>::BYTES];
   const TilePlan<F, kXentStats> plan(g, __builtin_amdgcn_readfirstlane(*g.count));
   const XentCut& cut = plan.cut;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -651,7 +707,7 @@ __global__ void __launch_bounds__(F::THREADS) xent_add_stats_kernel(XentTileArgs
   uint32_t tm, tn;
   cut.place(cut.whole + r, tm, tn);
   finish<F, kXentStats>(g, acc, plan.m, (int64_t)tm * F::TM, (int64_t)tn * F::TN, tn, wave / F::WN,
-                        wave % F::WN, lane, halves);
+                        wave % F::WN, lane, side);
 }
 
 // g.m, and g.k for dw: the most rows that may count.
