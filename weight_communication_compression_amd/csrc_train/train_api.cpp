@@ -246,13 +246,14 @@ lowbit_status xent_logits(const XentPlan& w, const lowbit_xent_params* p, void* 
 
 // The form that takes least time by what its steps and tiles were measured to take
 // (us): a step of k with all slots taken, a step at the least, and what a tile takes
-// besides (the parts of the softmax; d, dx and dw, which are written).  It picks
-// the fastest form, or one within 10 % of it, at sizes from 1 x 1690 x 640 to
-// 8192 x 1000 x 4096; beside the best the next form loses 5 to 60 %.
+// besides (the parts of the softmax; d, dx and dw, which are written).  At 25 sizes
+// from 1 x 1690 x 640 to 8192 x 1000 x 4096 its choice takes 2 % longer than the
+// fastest form on average and 21 % (5 us) at worst; a form fixed by the rows alone
+// took up to 60 % longer.
 int xent_form(int dt, int kind, int64_t m, int64_t n, int64_t k) {
   static const double full[2][4] = {{0, 4.6, 3.36, 2.27}, {1.73, 1.19, 1.15, 1.25}};
   static const double least[2][4] = {{0, 3.6, 2.1, 1.2}, {1.3, 0.5, 0.4, 0.25}};
-  static const double tile[2][4] = {{5.0, 3.0, 2.5, 3.0}, {13.0, 4.5, 3.8, 3.0}};
+  static const double tile[2][4] = {{5.0, 3.0, 2.5, 3.0}, {8.0, 4.5, 3.8, 3.0}};
   const bool bf16 = dt != LOWBIT_F32;
   m = std::min(m, (int64_t)1 << 20);       // (beyond it the answer is the same, and the counts fit)
   n = std::min(n, (int64_t)1 << 20);

@@ -233,15 +233,27 @@ __global__ void __launch_bounds__(kBlockThreads) xent_join_kernel(XentJoin a) {
     float loss = 0.0f, lse = 0.0f;
     if (i >= 0) {
       const float2* part = a.part + i * a.parts;
-      float top = -INFINITY;
-      for (int p = lane; p < a.parts; p += 64) top = fmaxf(top, part[p].x);
-      for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-      float sum = 0.0f;
+      float top = -INFINITY, sum = 0.0f;
+      // eight parts a lane at a time, their loads under way together; the sum so far
+      // is kept relative to the maximum so far
       // (a part without finite logits has maximum -inf and a sum of 0 or NaN)
-      for (int p = lane; p < a.parts; p += 64) {
-        const float2 v = part[p];
-        sum += v.x == -INFINITY ? v.y : v.y * expf(v.x - top);
+      for (int p0 = lane; p0 < a.parts; p0 += 8 * 64) {
+        float2 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          v[u] = p0 + u * 64 < a.parts ? part[p0 + u * 64] : make_float2(-INFINITY, 0.0f);
+        float more = top;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) more = fmaxf(more, v[u].x);
+        if (top != -INFINITY) sum *= expf(top - more);
+        top = more;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) sum += v[u].x == -INFINITY ? v[u].y : v[u].y * expf(v[u].x - top);
       }
+      float all = top;
+      for (int d = 1; d < 64; d *= 2) all = fmaxf(all, __shfl_xor(all, d));
+      if (top != -INFINITY) sum *= expf(top - all);
+      top = all;
       for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
       lse = top + logf(sum);
       const int64_t t = a.targets[r];
