@@ -7,7 +7,9 @@ namespace lowbit {
 
 // y = r + D(x).  A lane takes 16 bytes of consecutive elements per trip and row
 // of the wave; the mask's word serves a pair, so that eight bfloat16 elements
-// cost four hashes.  Bound by memory: x (and r) read once, y written once.
+// cost four hashes.  Bound by memory: x (and r) read once, y written once (64 Mi
+// bfloat16 with a residual 67.5 us, 6.0 TB/s; 16 Mi binary32 19.7 us; the launch
+// alone 3.7 us).
 constexpr int kDropRows = 2;      // 16-byte pieces of a lane per trip
 
 template <int DT, bool RES>

@@ -20,6 +20,10 @@ namespace {
 // them and stores the same, and only the row's sums leave them out (`own`).  So no
 // load or store is ever cut, whatever the width and its alignment; only rows of
 // fewer than eight columns are taken element by element.
+//
+// Bound by memory where a row takes whole waves: 16 Ki x 4096 bfloat16 with a gate and
+// dropout 110 us, 4.9 TB/s (a copy: 5.1).  Short rows share a wave: with a
+// wave each, 10287 x 48 took 86 us for its gradient, now 20.
 struct Cols {
   int start;                        // column of element 0
   uint32_t own;                     // bit j: element j is this vector's
@@ -260,6 +264,10 @@ struct Acc {
 //     dx = a dy,  and per column  dgate += D(u) dy  (u = fh post_weight + post_bias),
 //     dpost_weight += du fh, dpost_bias += du, dpre_weight += dz yh, dpre_bias += dz
 // <.> the mean over the row, [.] only with LAYER.
+// 16 Ki x 4096 bfloat16 takes 182 us, 4.4 TB/s, and the sums of its partial rows 8:
+// two waves a SIMD (the sums take 40 registers for each vector), two exchanges over the
+// workgroup a row, vector ALU 46 % busy with 46 instructions an element.  At 128
+// registers, for twice the waves, 27 spill: 264 us.
 template <int FT, int ST, int PT, int NV, bool LAYER, int MAXT, bool RAGGED, bool SUB>
 __global__ void __launch_bounds__(MAXT) join_back_kernel(JoinBackArgs b) {
   __shared__ float slots[64];
