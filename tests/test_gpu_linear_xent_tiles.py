@@ -58,3 +58,69 @@ def test_minus_infinity_beside_a_row_that_ends_inside_a_step():
         assert torch.isfinite(clean.lse).all() and torch.isfinite(one.lse).all(), hidden
         # the same terms, summed in another order: 128 roundings each
         assert ((one.lse - want.lse).abs() <= 2 ** -24 * (256 + 4 * want.lse.abs())).all(), hidden
+
+
+def test_weights_beyond_32_bits():
+    """w and dw of 4.6 GB, a few rows: the far end of both, and dx summed over all of w."""
+    n, vocab, hidden, part = 5, 140000, 16384, 10000
+    say("xent far weights")
+    g = torch.Generator(device=X.DEV)
+    g.manual_seed(5)
+    x = torch.randn(n, hidden, generator=g, device=X.DEV).bfloat16()
+    w = torch.empty(vocab, hidden, dtype=torch.bfloat16, device=X.DEV)
+    for a in range(0, vocab, part):
+        w[a:a + part] = torch.randn(part, hidden, generator=g, device=X.DEV) * 1.5 / hidden ** 0.5
+    t = torch.tensor([0, vocab - 1, 131072, 77, -100], device=X.DEV)
+    dloss = torch.full((n,), 0.25, device=X.DEV)
+    out = L.linear_xent(x, w, t)
+    got = L.linear_xent_backward(x, w, t, out.lse, dloss)
+    torch.cuda.synchronize()
+    say("  ran")
+    x64, counts = x.double(), (t != -100)
+    logits = torch.cat([x64 @ w[a:a + part].double().t() for a in range(0, vocab, part)], 1)
+    off = (hidden + 1) * X.U * torch.cat([x64.abs() @ w[a:a + part].double().abs().t()
+                                          for a in range(0, vocab, part)], 1)
+    lse = torch.where(counts, torch.logsumexp(logits, 1), 0.0)
+    X.check(out.lse, lse, off.max(1).values + 128 * X.U + 2 * X.U * lse.abs(), "lse")
+    d = (logits - out.lse.double()[:, None]).exp() * 0.25
+    soft = d.clone()
+    rows = torch.arange(4, device=X.DEV)
+    d[rows, t[:4]] -= 0.25
+    d[4], soft[4] = 0, 0
+    half = torch.finfo(torch.bfloat16).eps / 2
+    err = soft * (off.exp() - 1 + X.U * (8 + (logits - out.lse.double()[:, None]).abs())) \
+        + 4 * X.U * (soft + 0.25 * (d != soft))
+    err = err + half * (d.abs() + err)
+    for a in (0, 60000, vocab - part):
+        want = d[:, a:a + part].t() @ x64
+        bound = err[:, a:a + part].t() @ x64.abs() + (n + 4) * X.U * (d[:, a:a + part].t().abs() @ x64.abs())
+        X.check(got.dw[a:a + part], want, bound + half * want.abs() + X.TINY * (x64.abs().sum(0) + n + 1),
+                "dw")
+    want = sum(d[:, a:a + part] @ w[a:a + part].double() for a in range(0, vocab, part))
+    bound = sum(err[:, a:a + part] @ w[a:a + part].double().abs()
+                + (vocab + 4) * X.U * (d[:, a:a + part].abs() @ w[a:a + part].double().abs())
+                for a in range(0, vocab, part))
+    X.check(got.dx, want, bound * (1 + 1e-6) + half * want.abs() + X.TINY * vocab, "dx")
+
+
+def test_tokens_beyond_32_bits():
+    """x, its compact copy and dx of 4.8 GB: the far rows equal the same rows alone."""
+    n, vocab, hidden = 73000, 300, 32768
+    say("xent far tokens")
+    g = torch.Generator(device=X.DEV)
+    g.manual_seed(6)
+    x = torch.empty(n, hidden, dtype=torch.bfloat16, device=X.DEV)
+    for a in range(0, n, 1000):
+        x[a:a + 1000] = torch.randn(min(1000, n - a), hidden, generator=g, device=X.DEV)
+    w = (torch.randn(vocab, hidden, generator=g, device=X.DEV) * 1.5 / hidden ** 0.5).bfloat16()
+    t = torch.arange(n, device=X.DEV) % vocab
+    t[::3] = -100
+    dloss = torch.full((n,), 1e-4, device=X.DEV)
+    out = L.linear_xent(x, w, t)
+    got = L.linear_xent_backward(x, w, t, out.lse, dloss, need_dw=False)
+    torch.cuda.synchronize()
+    say("  ran")
+    far = slice(n - 500, n)
+    X.check_forward(x[far], w, t[far], L.LinearXent(out.loss[far], out.lse[far]))
+    X.check_backward(x[far], w, t[far], out.lse[far], dloss[far], None,
+                     L.LinearXentGrads(got.dx[far], None))

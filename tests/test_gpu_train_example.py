@@ -45,9 +45,10 @@ def plain(p, tokens, targets, layers, drop, seed):
 
 
 def test_gradients(example):
-    """Against binary32.  A tensor passes about ten roundings to bfloat16 of 2^-9 of
-    its size on its way (each step's output): their root sum of squares is under 2^-7,
-    and the whole gradient's relative distance stays within four times that."""
+    """Against binary32.  A tensor passes about ten roundings to bfloat16 on its way
+    (each step's output), each off by at most 2^-8 of a value and by 2^-9 in the root
+    mean square: ten of them by less than 2^-7, and the whole gradient's relative
+    distance stays within four times that."""
     say("train example")
     layers, drop, seed = 2, 0.1, 17
     p = example.make_params(layers, 256, 600, 3, DEV)
