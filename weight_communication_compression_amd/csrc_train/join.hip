@@ -22,7 +22,7 @@ namespace {
 // fewer than eight columns are taken element by element.
 //
 // Bound by memory where a row takes whole waves: 16 Ki x 4096 bfloat16 with a gate and
-// dropout 110 us, 4.9 TB/s (a copy: 5.1).  Short rows share a wave: with a
+// dropout 104 us, 5.2 TB/s (a copy: 5.1).  Short rows share a wave: with a
 // wave each, 10287 x 48 took 86 us for its gradient, now 20.
 struct Cols {
   int start;                        // column of element 0
@@ -559,9 +559,13 @@ JoinShape join_shape(int64_t rows, int cols, bool backward) {
   if (backward && g.vecs == 2 && g.lanes < 512) g.lanes = 512;
   g.ragged = cols != 8 * g.lanes * g.vecs;
   g.threads = g.lanes <= 64 ? 256 : g.lanes;
-  // runs: rounds of what the chip holds; for the gradient one round, as every
-  // run leaves partial sums behind
-  const int64_t most = (int64_t)256 * (backward ? 1024 : 2048) / (g.lanes < 64 ? 64 : g.lanes);
+  // runs: forward for several rounds of what the chip holds, which then ends evenly
+  // (16 Ki x 4096 bfloat16 in runs for 1024, 2048 and 4096 lanes a CU: 115.6, 110 and
+  // 104 us), but not a row each, which loads the parameters for every row (weights
+  // and biases in binary32: 128 against 103 us; one bfloat16 weight: 97 against 103);
+  // for the gradient one round, as every run leaves partial sums behind (2048
+  // lanes a CU: 191 against 186 us)
+  const int64_t most = (int64_t)256 * (backward ? 1024 : 4096) / (g.lanes < 64 ? 64 : g.lanes);
   g.rows_per_run = rows > most ? (rows + most - 1) / most : 1;
   if (backward) {
     // and four rows a run where that leaves one for each CU: partial sums of every
