@@ -327,7 +327,9 @@ __device__ __forceinline__ void finish(const XentTileArgs& g, f32x16 (&acc)[F::I
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       const int64_t row = ml + 32 * i;
-      const int64_t target = row < m ? (int64_t)__float_as_int(g.info[row].w) - nl : -1;
+      // (nl counts from the piece's first column; a piece that ends inside a tile is the last
+      // one, so that no target lies among the columns behind it)
+      const int64_t target = row < m ? (int64_t)__float_as_int(g.info[row].w) - g.col0 - nl : -1;
       if (__any(target >= 0 && target < 32 * J)) {
 #pragma unroll
         for (int j = 0; j < J; ++j)
