@@ -568,6 +568,7 @@ def _join_params(f, x, named, rows_per_gate, norm, residual_scale, eps, p, seed)
     rows = f.numel() // cols if cols else 0
     if norm not in _NORMS:
         raise LowbitError(EINVAL, "norm must be 'rms' or 'layer'")
+    rows_per_gate = int(rows_per_gate)
     pt = None
     for name, t in named:
         if t is None:
@@ -585,7 +586,8 @@ def _join_params(f, x, named, rows_per_gate, norm, residual_scale, eps, p, seed)
     if x.device != f.device:
         raise LowbitError(EINVAL, "f and x must be on one device")
     ft = _dtype_code(f)
-    return JoinParams(rows, cols, int(rows_per_gate), _NORMS[norm], ft, _dtype_code(x),
+    # (more rows a gate than there are: one gate; as a larger number 64 bits may not hold it)
+    return JoinParams(rows, cols, min(rows_per_gate, max(rows, 1)), _NORMS[norm], ft, _dtype_code(x),
                       ft if pt is None else (F32 if pt == torch.float32 else
                                              BF16 if pt == torch.bfloat16 else -1),
                       eps, residual_scale, p, int(seed) & _U64)
