@@ -65,7 +65,8 @@ typedef struct {
     int64_t rows;
     int64_t cols;             /* 1 .. 16384                                    */
     int64_t rows_per_gate;    /* consecutive rows that share a row of the gate;
-                                 used only where a gate is given               */
+                                 used only where a gate is given; any number
+                                 from `rows` on: one row for all               */
     int32_t norm;             /* LOWBIT_NORM_*                                 */
     int32_t block_type;       /* lowbit_dtype of f, z and their gradients      */
     int32_t stream_type;      /* of x, x_out and their gradients: block_type

@@ -78,7 +78,7 @@ JoinArgs join_args(const lowbit_join_params* p, const JoinShape& g) {
   a.rows = p->rows;
   a.rows_per_run = g.rows_per_run;
   a.lanes = g.lanes;
-  a.rows_per_gate = p->rows_per_gate;
+  a.rows_per_gate = std::min(p->rows_per_gate, p->rows);   // (so that sums with it fit)
   a.cols = (int32_t)p->cols;
   a.eps = p->eps;
   a.scale = p->residual_scale;
@@ -354,7 +354,6 @@ lowbit_status lowbit_block_join_backward(const void* dx_out, const void* dz, con
   if (!good_or_null(dgate)) return LOWBIT_EINVAL;
   JoinSumArgs sums{};
   sums.rows = p->rows;
-  sums.rows_per_gate = p->rows_per_gate;
   sums.cols = (int32_t)p->cols;
   if (p->rows == 0) {                     // sums of nothing
     for (float* o : out)
@@ -394,6 +393,7 @@ lowbit_status lowbit_block_join_backward(const void* dx_out, const void* dz, con
   b.part_gate = reinterpret_cast<float*>(at);
   sums.part_gate = b.part_gate;
   sums.dgate = dgate;
+  sums.rows_per_gate = b.j.rows_per_gate;
   sums.rows_per_run = g.rows_per_run;
   sums.blocks = g.blocks;
   const lowbit_status st = launch_join_back(p->block_type, p->stream_type, p->param_type,
