@@ -92,7 +92,7 @@ struct XentGather {
   const void* x;
   void* xc;                  // compact rows, zeros beyond the count
   void* dx;                  // backward: rows that are left out are set to 0; may be null
-  const int32_t *pos, *map, *count;
+  const int32_t *pos, *map;
   int64_t n, padded;
   int32_t hidden, ld;        // of x and dx; of xc
 };

@@ -96,14 +96,7 @@ __device__ __forceinline__ void store8(void* row, int c, int cols, const Raw8<DT
   }
 }
 
-// The dropout mask as the kernels take it.
-struct Drop {
-  uint32_t key;       // K(seed)
-  uint32_t cut;       // draws below it are dropped
-  float factor;       // of the kept ones
-};
-
-// the word of pair q: two draws
+// the word of the mask's pair q: two draws, of which those below `cut` are dropped
 __device__ __forceinline__ uint32_t draw_word(const HiMix& h, uint32_t q) {
   return fmix32(h.x0(q));
 }
