@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 from typing import NamedTuple, Optional, Sequence
 
 import torch
@@ -482,6 +483,7 @@ def stream_probe(op: int, dst: torch.Tensor, src: Optional[torch.Tensor] = None,
 
 
 # ------------------------------------------------ training-step operators --
+# Plain calls outside torch's autograd, each with its gradient as a call of its own.
 _U64 = 2 ** 64 - 1
 _NORMS = {"rms": 0, "layer": 1}
 
@@ -496,6 +498,15 @@ def _out_like(t: torch.Tensor, out: Optional[torch.Tensor], what: str) -> torch.
     if out.dtype != t.dtype or out.numel() != t.numel() or out.device != t.device:
         raise LowbitError(EINVAL, f"{what} must match the input in dtype, size and device")
     return out
+
+
+def _outside_autograd(name: str) -> None:
+    """For inputs that require a gradient: where torch would record a call, says that this one
+    is not."""
+    if torch.is_grad_enabled():
+        warnings.warn(f"{name} is not recorded for torch's backward pass: no gradient reaches its "
+                      f"inputs through its outputs.  Take it from {name}_backward (and call under "
+                      "torch.no_grad(), which also silences this)", stacklevel=3)
 
 
 def _scratch(nbytes: int, like: torch.Tensor, workspace: Optional[torch.Tensor], what: str):
@@ -518,6 +529,8 @@ def dropout(x: torch.Tensor, p: float, seed: int, residual: Optional[torch.Tenso
 
     index_offset (a multiple of 8): the mask's index of element 0, for a tensor
     that is a piece of a larger one.  `out` may be x or residual."""
+    if x.requires_grad or (residual is not None and residual.requires_grad):
+        _outside_autograd("dropout")
     if residual is not None and (residual.dtype != x.dtype or residual.numel() != x.numel()
                                  or residual.device != x.device):
         raise LowbitError(EINVAL, "residual must match x in dtype, size and device")
@@ -569,11 +582,12 @@ def _join_params(f, x, named, rows_per_gate, norm, residual_scale, eps, p, seed)
     if norm not in _NORMS:
         raise LowbitError(EINVAL, "norm must be 'rms' or 'layer'")
     rows_per_gate = int(rows_per_gate)
+    device = f.device
     pt = None
     for name, t in named:
         if t is None:
             continue
-        if t.device != f.device or (pt is not None and t.dtype != pt):
+        if t.device != device or (pt is not None and t.dtype != pt):
             raise LowbitError(EINVAL, "weights, biases and gate must have one dtype and f's device")
         pt = t.dtype
         want = cols
@@ -583,7 +597,7 @@ def _join_params(f, x, named, rows_per_gate, norm, residual_scale, eps, p, seed)
             want = -(-rows // rows_per_gate) * cols
         if t.numel() != want:
             raise LowbitError(EINVAL, f"{name} must have {want} elements")
-    if x.device != f.device:
+    if x.device != device:
         raise LowbitError(EINVAL, "f and x must be on one device")
     ft = _dtype_code(f)
     # (more rows a gate than there are: one gate; as a larger number 64 bits may not hold it)
@@ -612,6 +626,10 @@ def block_join(f: torch.Tensor, x: torch.Tensor, post_weight: Optional[torch.Ten
     `x_out` may be x, `z` may be f.  stats feeds block_join_backward."""
     named = (("post_weight", post_weight), ("post_bias", post_bias), ("gate", gate),
              ("pre_weight", pre_weight), ("pre_bias", pre_bias))
+    for t in (f, x, post_weight, post_bias, gate, pre_weight, pre_bias):
+        if t is not None and t.requires_grad:
+            _outside_autograd("block_join")
+            break
     q = _join_params(f, x, named, rows_per_gate, norm, residual_scale, eps, p, seed)
     x_out = _out_like(x, x_out, "x_out")
     z = _out_like(f, z, "z")
@@ -693,6 +711,8 @@ def linear_xent(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, ignore_
 
     x (..., hidden), w (vocab, hidden): float32 or bfloat16; targets: int64.
     Mean loss: loss.sum() / (targets != ignore_index).sum()."""
+    if x.requires_grad or w.requires_grad:
+        _outside_autograd("linear_xent")
     q = _xent_params(x, w, targets, ignore_index)
     L = lib()
     ws = _scratch(L.lowbit_linear_xent_workspace(q, 0), x, workspace, "linear_xent")
