@@ -18,6 +18,11 @@
  * for odd i.  With t = p * 65536 rounded to nearest (ties to even), D keeps the
  * elements whose draw is at least t, multiplied by 65536 / (65536 - t) (by 0 if
  * t = 65536), and gives +0 elsewhere, whatever stood there.
+ * Masks of two seeds are not independent of each other: below 2^33 elements pair
+ * q's word is fmix32(q ^ c) with c = fmix32(K(seed)), so that another seed's mask
+ * has the word of pair q at pair q ^ c ^ c'.  Two buffers of 2^25 pairs hold the same
+ * words in another order for one pair of seeds in 128 (of 2^m pairs: one in
+ * 2^(32 - m)), smaller or larger parts of them for others.
  *
  * Conventions of lowbit.h hold: device pointers, element buffers (x, y, f,
  * w, gradients, parameters, gate, lse, ...) aligned to 16 bytes, targets to 8;
@@ -26,9 +31,11 @@
  * Matrices are dense and row-major.  The library allocates nothing: calls with
  * scratch take `workspace`, aligned to 16 bytes, of at least the bytes that the
  * matching *_workspace function gives.  It holds nothing between calls, and two
- * calls that may run at the same time need one each.  All arithmetic is binary32
- * with each output rounded once; sums run in a fixed order, so that equal
- * calls give equal bits.  Every call can be captured into a HIP graph.
+ * calls that may run at the same time need one each.  Arithmetic, sums and
+ * statistics are binary32 and each output is rounded once; one value in between is
+ * held in fewer bits, d of linear xent's gradient (below).  Sums run in a fixed
+ * order, so that equal calls give equal bits.  Every call can be captured into a
+ * HIP graph.
  */
 #ifndef LOWBIT_TRAIN_H
 #define LOWBIT_TRAIN_H
@@ -105,7 +112,9 @@ int64_t lowbit_block_join_backward_workspace(const lowbit_join_params* p);
 
 /*
  * Gradient of the block join, from the gradients of x_out and z, the forward
- * call's f, x_out and stats and its parameters (p and seed redraw the mask).
+ * call's f, x_out and stats and its parameters (p and seed redraw the mask).  The
+ * second norm's gradient is taken at x_out as it was written, rounded to
+ * stream_type, with the statistics of the row before it was rounded.
  *   df, dx : rows x cols (written); df may be dz, dx may be dx_out
  *   dpost_weight, dpost_bias, dpre_weight, dpre_bias : cols binary32 each;
  *   dgate  : ceil(rows / rows_per_gate) x cols binary32 (only with a gate).
@@ -138,7 +147,8 @@ int64_t lowbit_linear_xent_workspace(const lowbit_xent_params* p, int32_t backwa
  * Softmax cross entropy of the logits l = x w^T:
  *     lse[r] = log sum_v exp(l[r, v]),   loss[r] = lse[r] - l[r, targets[r]]
  * and 0 for both in rows that are left out.  A target outside [0, vocab) that
- * is not ignore_index gives NaN for both.
+ * is not ignore_index gives NaN for both, and so does a logit of +infinity or NaN;
+ * logits of -infinity add nothing.
  *   x : rows x hidden;  w : vocab x hidden;  targets : rows int64
  *   loss, lse : rows binary32 (written)
  * Logits are binary32 sums of exact products.
@@ -155,7 +165,8 @@ lowbit_status lowbit_linear_xent(const void* x, const void* w, const int64_t* ta
  *     d[r, v] = exp(l[r, v] - lse[r]) (dloss[r] + dlse[r]) - dloss[r] [v = targets[r]]
  * it gives  dx = d w  and  dw = d^T x; d is formed in pieces of the vocabulary in
  * the workspace.  For LOWBIT_BF16 d is kept there in bfloat16, scaled so that
- * the largest |dloss| counts as 1.  Rows that are left out give dx = 0 and add
+ * the largest |dloss| counts as 1: each of its elements is off by up to 2^-8 more,
+ * relative, and so is an element of dx or dw that one of them makes up.  Rows that are left out give dx = 0 and add
  * nothing to dw; a target out of range gives NaN.
  *   dx : rows x hidden, dw : vocab x hidden, of type p->type; either may be NULL
  *        and is then not computed.  rows == 0 still writes dw (zeros).

@@ -257,7 +257,9 @@ struct Acc {
   }
 };
 
-// With yh = (x_out - mean2) rstd2 and fh = (f - mean1) rstd1:
+// With yh = (x_out - mean2) rstd2 and fh = (f - mean1) rstd1 (x_out as it was written: a
+// bfloat16 stream's yh is off by its half step, 2^-8 relative; the row before it was
+// rounded is kept nowhere):
 //     dy = dx_out + rstd2 (q - yh <q yh> - [<q>]),      q = dz pre_weight
 //     du = D(gate dy)                       (the mask redrawn)
 //     df = rstd1 (s - fh <s fh> - [<s>]),               s = du post_weight

@@ -312,6 +312,14 @@ __device__ __forceinline__ void store_rows(char* lds, int lane, const f32x16& a,
 }
 
 // What becomes of a tile's sums.
+//
+// d of bfloat16 inputs leaves in bfloat16: dx and dw are then products of bfloat16
+// matrices, at 1.25 PFLOP/s, where binary32 ones reach 0.13 (a library's), so that
+// two thirds of the gradient's operations would take ten times as long, and d is written
+// and read twice in half the bytes.  It costs half a step of each of its elements: the
+// gradient's root mean square error against 64 bits is 0.0024 of the gradient's own
+// where the outputs' rounding alone makes 0.0017 (2011 x 131072 x 2048; where many
+// terms add up alike, as over 8 Ki tokens, both 0.0017).
 template <class F, int KIND>
 __device__ __forceinline__ void finish(const XentTileArgs& g, f32x16 (&acc)[F::I][F::J], int64_t m,
                                        int64_t m0, int64_t n0, uint32_t tn, int wm, int wn, int lane,
