@@ -266,8 +266,8 @@ struct Acc {
 //     dx = a dy,  and per column  dgate += D(u) dy  (u = fh post_weight + post_bias),
 //     dpost_weight += du fh, dpost_bias += du, dpre_weight += dz yh, dpre_bias += dz
 // <.> the mean over the row, [.] only with LAYER.
-// 16 Ki x 4096 bfloat16 takes 182 us, 4.4 TB/s, and the sums of its partial rows 8:
-// two waves a SIMD (the sums take 40 registers for each vector), two exchanges over the
+// 16 Ki x 4096 bfloat16 takes 182 to 190 us a call, 4.2 to 4.4 TB/s, 8 of them for the
+// sums of its partial rows: two waves a SIMD (the sums take 40 registers for each vector), two exchanges over the
 // workgroup a row, vector ALU 46 % busy with 46 instructions an element.  At 128
 // registers, for twice the waves, 27 spill: 264 us.
 template <int FT, int ST, int PT, int NV, bool LAYER, int MAXT, bool RAGGED, bool SUB>

@@ -473,9 +473,10 @@ __device__ __forceinline__ void finish(const XentTileArgs& g, f32x16 (&acc)[F::I
   }
 }
 
-// Bound by the matrix units at the clock that power leaves them (1.9 GHz in the
-// largest form): 8192 x 50257 x 4096 bfloat16 2.6 ms, 1.28 PFLOP/s, dx of
-// 6144 x 25344 x 4096 1.02 ms, 1.25, dw 1.23, d 1.18; a large library product 1.31.
+// Bound by the matrix units at the clock that power leaves them (about 1.9 GHz in the
+// largest form; machines differ): 8192 x 50257 x 4096 bfloat16 2.55 to 2.74 ms, 1.32 to
+// 1.23 PFLOP/s, dx of 6144 x 25344 x 4096 1.02 ms, 1.25, dw 1.23, d 1.18; a large
+// library product 1.31.
 // Without the loads the loop reaches 1.55 on random data and 2.09 on zeros; with
 // four waves of 128 x 128, which read a third less from LDS, it is no faster and spills.
 // Few rows are bound by reading w: 13 x 50257 x 1024 17.5 us, 5.9 TB/s.
