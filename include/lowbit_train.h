@@ -10,6 +10,12 @@
  *                  and its gradient
  *   linear xent  : softmax cross entropy of x w^T over a large vocabulary
  *                  without keeping the logits, and its gradient
+ *   rotary       : rotary positions of queries and keys, and their gradient
+ *   attention    : softmax attention over packed documents (causal, sliding
+ *                  window, prefix, capped scores, distance bias, shared key-value
+ *                  heads), and its gradient
+ *   orthogonalize: Newton-Schulz products that bring a matrix's singular values
+ *                  towards 1, for updates that are orthogonalised
  *
  * The mask.  Element i of a buffer (for a matrix of `cols` columns, row r's
  * column c counts as i = r * (cols + cols mod 2) + c) belongs to pair i / 2,
@@ -176,6 +182,185 @@ lowbit_status lowbit_linear_xent_backward(const void* x, const void* w, const in
                                           const lowbit_xent_params* p, void* dx, void* dw,
                                           void* workspace, int64_t workspace_bytes,
                                           hipStream_t stream);
+
+/* ------------------------------------------------------------------ rotary -- */
+#define LOWBIT_ROTARY_HALF 0         /* pairs (i, i + rot_dim / 2)              */
+#define LOWBIT_ROTARY_INTERLEAVED 1  /* pairs (2 i, 2 i + 1)                    */
+
+#define LOWBIT_ROTARY_PLAIN 0        /* f_i = base^(-2 i / rot_dim)             */
+#define LOWBIT_ROTARY_LINEAR 1       /* f_i / factor                            */
+#define LOWBIT_ROTARY_BASE 2         /* base * factor^(rot_dim / (rot_dim - 2)):
+                                        the slowest pair is divided by factor,
+                                        the fastest kept (rot_dim 2: kept)      */
+#define LOWBIT_ROTARY_PARTS 3        /* f_i / factor for pairs of at most
+                                        slow_turns over original_length
+                                        positions, f_i for those of at least
+                                        fast_turns, in between a mean whose weight
+                                        is linear in the turns; rotated values are
+                                        to be scaled by 0.1 ln(factor) + 1      */
+
+/*
+ * The rot_dim / 2 frequencies of a context that is scaled by `factor`, in
+ * radians a position, and the scale that goes with them.  Host arithmetic only.
+ *   freqs : host, rot_dim / 2 binary64 (written);  scale : host (written)
+ * EINVAL: NULL pointer, rot_dim not an even number in 2 .. 65536, unknown scaling,
+ * base or factor not above 0 or not finite, factor below 1 for LOWBIT_ROTARY_PARTS,
+ * and there original_length < 1 or not 0 <= slow_turns < fast_turns.
+ */
+lowbit_status lowbit_rotary_frequencies(int32_t rot_dim, double base, int32_t scaling,
+                                        double factor, int64_t original_length, double slow_turns,
+                                        double fast_turns, double* freqs, float* scale);
+
+/* Where the rows and heads of a matrix rows x heads x head_dim lie, in elements;
+ * the elements of a head are dense. */
+typedef struct {
+    int64_t row, head;
+} lowbit_strides;
+
+typedef struct {
+    int64_t rows;               /* tokens, up to 2^31 - 1                       */
+    int64_t rows_per_sequence;  /* without `positions`: row r's is
+                                   r mod rows_per_sequence (>= 1)               */
+    lowbit_strides x, y;
+    int32_t heads;              /* up to 65536                                  */
+    int32_t head_dim;           /* up to 65536                                  */
+    int32_t rot_dim;            /* even, 2 .. head_dim: the first elements of a
+                                   head; the others are copied                  */
+    int32_t layout;             /* LOWBIT_ROTARY_HALF or _INTERLEAVED           */
+    int32_t type;               /* lowbit_dtype of x and y                      */
+    float   scale;              /* of the rotated values                        */
+} lowbit_rotary_params;
+
+/*
+ * Rotary positions: every pair (u, v) of a head of row r, of frequency f, gives
+ *     scale * (u cos a - v sin a),  scale * (u sin a + v cos a),   a = position[r] f.
+ *   x, y      : rows x heads x head_dim; y may be x, with equal strides, and then
+ *               only the rotated part is read and written.  They need no alignment
+ *               beyond the type's.
+ *   freqs     : rot_dim / 2 binary64, device
+ *   positions : rows int64, device, of any sign; NULL: counted
+ * Angles are taken in binary64 and reduced before sine and cosine: exact to
+ * 2^-22 of a turn up to positions of 2^30 and frequencies up to 1.
+ * EINVAL: p == NULL, a size, type or option outside its range, a negative stride, strides
+ * of y with which two of its elements share a place, y == x with unequal strides, NULL
+ * or misaligned pointer with rows > 0.
+ */
+lowbit_status lowbit_rotary(const void* x, const double* freqs, const int64_t* positions,
+                            const lowbit_rotary_params* p, void* y, hipStream_t stream);
+
+/* Its gradient: dx from dy, the pairs turned back.  The strides x are dy's, y
+ * are dx's; dx may be dy. */
+lowbit_status lowbit_rotary_backward(const void* dy, const double* freqs,
+                                     const int64_t* positions, const lowbit_rotary_params* p,
+                                     void* dx, hipStream_t stream);
+
+/* --------------------------------------------------------------- attention -- */
+typedef struct {
+    int64_t q_rows, k_rows;     /* of the buffers, up to 2^29                   */
+    int64_t window;             /* 0: none                                      */
+    int32_t sequences;          /* 0 .. 2^24                                    */
+    int32_t q_heads, kv_heads;  /* up to 4096; kv_heads divides q_heads, and query
+                                   head h reads key-value head
+                                   h / (q_heads / kv_heads)                     */
+    int32_t head_dim;           /* a multiple of 8, up to 128                   */
+    int32_t type;               /* lowbit_dtype of everything but lse and slopes */
+    int32_t causal;             /* 0 or 1                                       */
+    float   scale;              /* of the products, finite                      */
+    float   softcap;            /* 0: none; finite, >= 0                        */
+    lowbit_strides q, k, v, out;
+    lowbit_strides dout, dq, dk, dv;   /* the gradient's                        */
+} lowbit_attention_params;
+
+/*
+ * Attention.  Sequence s has the queries q_begin[s] .. q_begin[s + 1] - 1 and the
+ * keys k_begin[s] .. k_begin[s + 1] - 1, Lq and Lk of them.  Its query i stands at
+ * position i + Lk - Lq (the last query at the last key) and sees key j if
+ *     j < prefix[s], or
+ *     (not causal or j <= position) and (no window or |position - j| < window).
+ * Of those it sees
+ *     y_j = softcap * tanh(scale q.k_j / softcap) - slopes[head] |position - j|
+ *     lse = log sum_j exp(y_j),    out = sum_j exp(y_j - lse) v_j;
+ * a query that sees none has out = 0 and lse = -infinity.
+ *   q, out : q_rows x q_heads x head_dim;  k, v : k_rows x kv_heads x head_dim
+ *   lse    : q_heads x q_rows binary32, dense
+ *   q_begin, k_begin : sequences + 1 int32, device, not decreasing, from 0 up to at
+ *            most q_rows (k_rows); values beyond are cut to that.  Rows before the
+ *            first and behind the last sequence are neither read nor written.  Both
+ *            NULL: sequences of q_rows / sequences queries and k_rows / sequences keys
+ *            each (they have to divide); k_begin NULL: the same as q_begin (then
+ *            k_rows == q_rows); q_begin NULL alone: queries in equal sequences.
+ *            Offsets that decrease give unspecified results within the buffers.
+ *   prefix : sequences int32, device, or NULL: 0 for all
+ *   slopes : q_heads binary32, device, or NULL: 0 for all
+ * Rows' strides are multiples of 8 elements from head_dim up to 2^22, heads' strides
+ * multiples of 8; two elements of an output share no place.
+ * Scores, statistics and sums are binary32.  For LOWBIT_BF16 the weights exp(y - m)
+ * (m the largest so far) enter the product with v rounded to bfloat16, off by up to
+ * 2^-8 each, relative.  NaN and infinities of a key or value that a query does not
+ * see reach it only within its own sequence.
+ * EINVAL: p == NULL, a size, type, option or stride outside its range, NULL or
+ * misaligned pointer with rows and sequences > 0.  EUNSUPPORTED: head_dim above 128.
+ */
+lowbit_status lowbit_attention(const void* q, const void* k, const void* v,
+                               const int32_t* q_begin, const int32_t* k_begin,
+                               const int32_t* prefix, const float* slopes,
+                               const lowbit_attention_params* p, void* out, float* lse,
+                               hipStream_t stream);
+
+/* Bytes of workspace that lowbit_attention_backward needs, or -1 for invalid
+ * params. */
+int64_t lowbit_attention_backward_workspace(const lowbit_attention_params* p);
+
+/*
+ * Its gradient, from the gradient of out and the forward call's out and lse:
+ *     D = sum_d dout out,   g_j = exp(y_j - lse) (dout.v_j - D) (1 - tanh^2),
+ *     dq = scale sum_j g_j k_j,  dk_j = scale sum_i g_ij q_i,  dv_j = sum_i exp(y_ij - lse_i) dout_i,
+ * the last two over every query head that reads j's head.  lse and the slopes have no
+ * gradient here.  A key that no query sees has dk = dv = 0; rows outside all sequences are left as they
+ * were.  For LOWBIT_BF16 the weights and g enter their products rounded to
+ * bfloat16, as in the forward call.
+ */
+lowbit_status lowbit_attention_backward(const void* dout, const void* q, const void* k,
+                                        const void* v, const void* out, const float* lse,
+                                        const int32_t* q_begin, const int32_t* k_begin,
+                                        const int32_t* prefix, const float* slopes,
+                                        const lowbit_attention_params* p, void* dq, void* dk,
+                                        void* dv, void* workspace, int64_t workspace_bytes,
+                                        hipStream_t stream);
+
+/* ----------------------------------------------------------- orthogonalize -- */
+typedef struct {
+    int64_t batch;              /* matrices, up to 2^20                         */
+    int64_t rows, cols;         /* of each, 1 .. 65536; up to 2^40 elements in all */
+    int32_t type;               /* lowbit_dtype of g                            */
+    int32_t steps;              /* 0 .. 64                                      */
+    float   a, b, c;            /* coefficients, finite                         */
+    float   eps;                /* >= 0                                         */
+    float   scale;              /* of the result, finite                        */
+} lowbit_orthogonalize_params;
+
+/* Bytes of workspace that lowbit_orthogonalize needs, or -1 for invalid params. */
+int64_t lowbit_orthogonalize_workspace(const lowbit_orthogonalize_params* p);
+
+/*
+ * Newton-Schulz.  Of each matrix
+ *     X = g / (sqrt(sum g^2) + eps);   `steps` times  A = X X^T, X = a X + (b A + c A A) X;
+ *     out = scale X                    (for rows > cols: of g's transpose, turned back)
+ * With a = 3.4445, b = -4.7750, c = 2.0315 five steps bring all but the smallest
+ * singular values to between 0.7 and 1.2.
+ *   g   : batch x rows x cols, of p->type
+ *   out : batch x rows x cols bfloat16 (written); may be g where that is bfloat16
+ * X is held in binary32 throughout.  The products' operands (X, A, b A + c A A) are rounded
+ * to binary16, scaled by powers of two against its range, off by up to 2^-11 each,
+ * relative, and summed in binary32: three bits more than
+ * bfloat16 operands, whose errors the iteration raises to several hundredths.  They hold singular
+ * values up to 4; coefficients that let X grow beyond give infinities or NaN.  A matrix of zeros gives
+ * zeros if eps > 0, one with an infinity or NaN gives NaN.
+ * EINVAL: p == NULL, a size, type or option outside its range, NULL or misaligned
+ * pointer with batch > 0, workspace too small.
+ */
+lowbit_status lowbit_orthogonalize(const void* g, const lowbit_orthogonalize_params* p, void* out,
+                                   void* workspace, int64_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -25,7 +25,11 @@ SOURCES = ["api.cpp", "quantize_plain.hip", "quantize_ef.hip", "quantize_wdiff.h
            "dequant.hip", "measure.hip",
            "../csrc_train/train_api.cpp", "../csrc_train/dropout.hip", "../csrc_train/join.hip",
            "../csrc_train/xent_rows.hip", "../csrc_train/xent_tile_bf16.hip",
-           "../csrc_train/xent_tile_f32.hip"]
+           "../csrc_train/xent_tile_f32.hip",
+           "../csrc_train/block_api.cpp", "../csrc_train/rotary.hip",
+           "../csrc_train/attn_fwd_bf16.hip", "../csrc_train/attn_fwd_f32.hip",
+           "../csrc_train/attn_back_bf16.hip", "../csrc_train/attn_back_f32.hip",
+           "../csrc_train/attn_delta.hip", "../csrc_train/ortho.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 

@@ -1,0 +1,293 @@
+// attn.hpp -- what the attention kernels share: the tiles' way through LDS into
+// the operands of the matrix instructions, which sequence a tile belongs to, and what
+// its queries see.
+#pragma once
+
+#include "block.hpp"
+#include "train_device.hpp"
+#include "../csrc/launch.hpp"
+
+namespace lowbit {
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+#define LOWBIT_LDS __attribute__((address_space(3)))
+
+constexpr uint32_t kNowhere = 0x7FFFFFF0u;   // beyond every buffer's records
+constexpr float kLog2e = 1.44269502f;        // log2(e) to binary32
+constexpr float kLn2 = 0.693147182f;
+
+constexpr int kWaves = 4, kAttnThreads = 64 * kWaves;
+constexpr int kRowsPerTile = 32 * kWaves;    // of a workgroup: 32 of each wave
+
+// Scores are kept in units of which exp takes the fewest instructions: of log2 for
+// bfloat16 (2^t), natural ones for binary32, where the rounding error of x log2(e)
+// is made good so that results keep binary32's accuracy.
+template <int DT>
+__host__ __device__ constexpr float unit_of() { return DT == kF32 ? 1.0f : kLog2e; }
+template <int DT>
+__device__ __forceinline__ float exp_unit(float x) {
+  if constexpr (DT == kBF16) return __builtin_amdgcn_exp2f(x);
+  const float t = x * kLog2e;
+  const float y = __builtin_amdgcn_exp2f(t);
+  const float e = __builtin_fmaf(x, kLog2e, -t) + x * 1.92596303e-8f;
+  return x < -200.0f ? 0.0f : __builtin_fmaf(y, e * kLn2, y);
+}
+
+// v of the lane and of the one 32 further on, or back.
+__device__ __forceinline__ float other_half_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float both_halves_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ void barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+// All that the wave has loaded, stored or read in LDS is done.
+__device__ __forceinline__ void wait_all() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// d[row of first][column of second] += sum over 32 bytes of k.  Lane l gives row (column)
+// l mod 32 and the (l / 32)-th 16 bytes, and holds of the result column l mod 32
+// and rows 8 (r / 4) + 4 (l / 32) + r mod 4.  For binary32 four instructions take
+// one element of each lane: k in another order, the same for both.
+template <int DT>
+__device__ __forceinline__ f32x16 mma(const u32x4& first, const u32x4& second, f32x16 c) {
+  if constexpr (DT == kBF16) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, first),
+                                                   __builtin_bit_cast(bf16x8, second), c, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(first[j]),
+                                               __uint_as_float(second[j]), c, 0, 0, 0);
+    return c;
+  }
+}
+
+// Of 32 results in rows, those that make one operand along the rows: chunk c's.  The order of
+// k that this gives is that of Tile::column.
+template <int DT>
+__device__ __forceinline__ u32x4 pack_chunk(const f32x16& v, int c) {
+  u32x4 w;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (DT == kBF16) w[j] = pack_bf16(v[8 * c + 2 * j], v[8 * c + 2 * j + 1]);
+    else w[j] = __float_as_uint(v[4 * c + j]);
+  }
+  return w;
+}
+template <int DT>
+__host__ __device__ constexpr int chunks() { return DT == kF32 ? 4 : 2; }   // of 32 rows
+
+// The memory from p on, `records` bytes of it; what lies behind reads as 0.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t open(const void* p, int records) {
+  const uint64_t at = (uint64_t)p;                 // (uniform, but not for the compiler)
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)hi << 32 | lo), 0,
+                                           __builtin_amdgcn_readfirstlane(records), 0x00020000);
+}
+
+// 16 bytes a lane to LDS, in lane order.  (A function of its own: called within a member of
+// a nested class template, this builtin makes the compiler drop host stubs of the kernels.)
+__device__ __forceinline__ void load_pieces(__amdgpu_buffer_rsrc_t q, char* lds, uint32_t at) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(q, (LOWBIT_LDS void*)lds, 16, at, 0, 0, 0);
+}
+// 64 consecutive words to LDS.
+__device__ __forceinline__ void load_floats(__amdgpu_buffer_rsrc_t q, char* lds, int lane) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(q, (LOWBIT_LDS void*)lds, 4, lane * 4, 0, 0, 0);
+}
+
+// A tile of ROWS rows of D elements in LDS.  The 16-byte pieces of a row are
+// permuted by its number so that neither the operands that run along a row (32
+// rows, one piece each) nor those that run down the columns (four rows, 32 bytes
+// each) meet a bank of LDS more often than they must.
+template <int DT, int D, int ROWS>
+struct Tile {
+  static constexpr int ES = elem_size<DT>(), PITCH = D * ES, NP = PITCH / 16;
+  static constexpr int BYTES = ROWS * PITCH;
+  static constexpr int STEPS = PITCH / 32;         // operands along a row
+  static constexpr int BLOCKS = D / 32;            // blocks of 32 columns
+  static constexpr int LOADS = BYTES / 1024 / kWaves, PER_LOAD = 1024 / PITCH;
+
+  static __device__ __forceinline__ constexpr int mix(int r) {
+    if constexpr (DT == kF32) return (r & 3) | (r >> 2 & 1) << 3 | (r >> 3 & 1) << 2;
+    else if constexpr (NP == 16) return (r & 3) << 2 | (r >> 2 & 3);
+    else return (r >> 1 & 1) << 2 | (r >> 2 & 3);
+  }
+
+  // The way in: 16 bytes a lane straight from memory, the waves taking turns.
+  struct Loader {
+    uint32_t voff[LOADS];
+    __device__ __forceinline__ void init(int64_t row_bytes, int width_bytes, int wave, int lane) {
+#pragma unroll
+      for (int j = 0; j < LOADS; ++j) {
+        const int r = (j * kWaves + wave) * PER_LOAD + lane / NP;
+        const int piece = lane % NP ^ mix(r);
+        voff[j] = piece * 16 < width_bytes ? (uint32_t)(r * (int)row_bytes) + piece * 16 : kNowhere;
+      }
+    }
+    // rows: how many there are from `p` on; those behind read as 0
+    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const char* p, int row_bytes,
+                                                                     int width_bytes, int rows) {
+      const int n = rows < ROWS ? rows : ROWS;
+      return open(p, n > 0 ? (n - 1) * row_bytes + width_bytes : 0);
+    }
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t q, char* lds, int wave, int j) const {
+      load_pieces(q, lds + (j * kWaves + wave) * 1024, voff[j]);
+    }
+  };
+
+  // Operands along a row: row b * 32 + lane mod 32, step kk.
+  struct Along {
+    uint32_t at;
+    __device__ __forceinline__ void init(int lane) {
+      const int r = lane % 32;
+      at = r * PITCH + ((lane / 32) ^ mix(r)) * 16;
+    }
+    __device__ __forceinline__ u32x4 load(const char* lds, int b, int kk) const {
+      return *reinterpret_cast<const u32x4*>(lds + (at ^ (kk * 32)) + b * 32 * PITCH);
+    }
+  };
+
+  // Operands down a column: column i * 32 + lane mod 32, rows of chunk c.
+  struct Down {
+    uint32_t at;
+    __device__ __forceinline__ void init(int lane) {
+      const int h = lane / 32;
+      if constexpr (DT == kF32) {
+        at = 4 * h * PITCH + ((lane % 32 / 4) ^ mix(4 * h)) * 16 + lane % 4 * 4;
+      } else {
+        const int r = 4 * h + lane % 16 / 4;
+        at = r * PITCH + ((lane / 16 % 2 * 2 + lane % 4 / 2) ^ mix(r)) * 16 + lane % 2 * 8;
+      }
+    }
+    __device__ __forceinline__ u32x4 load(const char* lds, int i, int c) const {
+      if constexpr (DT == kF32) {
+        u32x4 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const char* p = lds + (at ^ ((i * 8 ^ mix(8 * c + j)) * 16)) + (8 * c + j) * PITCH;
+          v[j] = *reinterpret_cast<const uint32_t*>(p);
+        }
+        return v;
+      } else {
+        // 16 lanes read 16 columns of four rows and get a column each
+        const uint32_t a = at ^ (i * 64);
+        typedef LOWBIT_LDS s16x4* lp;
+        const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lp)(LOWBIT_LDS char*)(lds + a + 16 * c * PITCH));
+        const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lp)(LOWBIT_LDS char*)(lds + (a ^ 32) + (16 * c + 8) * PITCH));
+        return __builtin_bit_cast(u32x4, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+      }
+    }
+  };
+};
+
+// One sequence: its queries and keys in the buffers.
+struct Sequence {
+  int q0, lq, k0, lk, prefix;
+};
+
+__device__ __forceinline__ int offset_at(const int32_t* begin, int s, int sequences, int rows) {
+  if (!begin) return (int)((int64_t)rows / sequences * s);
+  const int v = begin[s];
+  return v < 0 ? 0 : v > rows ? rows : v;
+}
+
+__device__ __forceinline__ Sequence sequence_at(const AttnArgs& g, int s) {
+  const int32_t* kb = g.k_begin;
+  Sequence q;
+  q.q0 = offset_at(g.q_begin, s, g.sequences, g.q_rows);
+  q.lq = offset_at(g.q_begin, s + 1, g.sequences, g.q_rows) - q.q0;
+  q.k0 = offset_at(kb, s, g.sequences, g.k_rows);
+  q.lk = offset_at(kb, s + 1, g.sequences, g.k_rows) - q.k0;
+  q.lq = q.lq < 0 ? 0 : q.lq;
+  q.lk = q.lk < 0 ? 0 : q.lk;
+  q.prefix = g.prefix ? g.prefix[s] : 0;
+  q.prefix = q.prefix < 0 ? 0 : q.prefix > q.lk ? q.lk : q.prefix;
+  return q;
+}
+
+// Sequence s has the tiles from begin[s] / T + s on, whose count, ceil(length / T), never
+// reaches the next sequence's first: a tile's sequence is found without a table of
+// tiles, 64 sequences at a time.
+__device__ __forceinline__ int find_sequence(const int32_t* begin, int sequences, int rows, int T,
+                                             int tile) {
+  int first = 0, count = sequences;                // the answer is one of these
+  while (count > 1) {
+    const int step = (count + 63) / 64;
+    const int off = lane_id() * step;
+    const bool at_or_before =
+        off < count && offset_at(begin, first + off, sequences, rows) / T + first + off <= tile;
+    const int n = __popcll(__ballot(at_or_before));
+    const int skip = (n > 0 ? n - 1 : 0) * step;
+    first += skip;
+    count = count - skip < step ? count - skip : step;
+  }
+  return __builtin_amdgcn_readfirstlane(first);
+}
+__device__ __forceinline__ int first_tile(const int32_t* begin, int s, int sequences, int rows, int T) {
+  return offset_at(begin, s, sequences, rows) / T + s;
+}
+
+// What query `pos` sees: keys below `prefix` and those from low to high.
+struct Sight {
+  int low, high, prefix;
+};
+__device__ __forceinline__ Sight sight(const AttnArgs& g, const Sequence& q, int pos) {
+  Sight v;
+  v.low = g.window ? pos - g.window + 1 : 0;
+  v.high = q.lk - 1;
+  if (g.causal) v.high = min(v.high, pos);
+  else if (g.window) v.high = min(v.high, pos + g.window - 1);
+  v.prefix = q.prefix;
+  return v;
+}
+
+// Which work item a workgroup takes.  Workgroup b runs on XCD b mod 8; the
+// tiles of a key-value head go to as few XCDs as keep all eight busy, whose L2 then
+// holds its keys and values, and the longest tiles come first.
+struct Items {
+  int per_head, parts, spread, group;
+  int64_t total;
+  __host__ __device__ Items(int tiles, int heads, int group_) {
+    group = group_;
+    spread = heads % 8 == 0 ? 8 : heads % 4 == 0 ? 4 : heads % 2 == 0 ? 2 : 1;
+    parts = 8 / spread;                            // XCDs of a head
+    per_head = (tiles + parts - 1) / parts;
+    total = (int64_t)per_head * (heads / spread) * group * 8;
+  }
+  // tile: may be beyond the last
+  __device__ __forceinline__ void take(int64_t item, int heads, int& tile, int& head, int& in) const {
+    const int xcd = (int)(item % 8);
+    const int64_t u = item / 8;
+    const int each = heads / spread;
+    in = (int)(u % group);
+    const int64_t v = u / group;
+    head = xcd / parts + (int)(v % each) * spread;
+    tile = (int)(v / each) * parts + xcd % parts;
+  }
+};
+
+constexpr int64_t kMaxBlocks = 1 << 20;            // (a multiple of 8)
+
+}  // namespace
+
+}  // namespace lowbit

@@ -26,6 +26,9 @@ __all__ = [
     "dropout", "dropout_backward", "block_join", "block_join_backward", "BlockJoin",
     "BlockJoinGrads", "JoinParams", "linear_xent", "linear_xent_backward", "LinearXent",
     "LinearXentGrads", "XentParams",
+    "rotary_frequencies", "rotary", "rotary_backward", "RotaryParams", "attention",
+    "attention_backward", "Attention", "AttentionGrads", "AttentionParams", "orthogonalize",
+    "OrthogonalizeParams",
     "stream_probe", "PROBE_READ", "PROBE_WRITE", "PROBE_COPY",
     "OK", "EINVAL", "EUNSUPPORTED", "EDEVICE", "F32", "BF16", "HINT_INPUT_REUSED",
 ]
@@ -70,6 +73,37 @@ class XentParams(ctypes.Structure):
                 ("ignore_index", ctypes.c_int64), ("type", ctypes.c_int32)]
 
 
+class Strides(ctypes.Structure):
+    """lowbit_strides"""
+    _fields_ = [("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class RotaryParams(ctypes.Structure):
+    """lowbit_rotary_params"""
+    _fields_ = [("rows", ctypes.c_int64), ("rows_per_sequence", ctypes.c_int64), ("x", Strides),
+                ("y", Strides), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class AttentionParams(ctypes.Structure):
+    """lowbit_attention_params"""
+    _fields_ = [("q_rows", ctypes.c_int64), ("k_rows", ctypes.c_int64), ("window", ctypes.c_int64),
+                ("sequences", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("type", ctypes.c_int32), ("causal", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("softcap", ctypes.c_float)] + [
+                    (name, Strides) for name in ("q", "k", "v", "out", "dout", "dq", "dk", "dv")]
+
+
+class OrthogonalizeParams(ctypes.Structure):
+    """lowbit_orthogonalize_params"""
+    _fields_ = [("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("type", ctypes.c_int32), ("steps", ctypes.c_int32), ("a", ctypes.c_float),
+                ("b", ctypes.c_float), ("c", ctypes.c_float), ("eps", ctypes.c_float),
+                ("scale", ctypes.c_float)]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -84,6 +118,8 @@ def lib() -> ctypes.CDLL:
         f64, u64 = ctypes.c_double, ctypes.c_uint64
         QP, JP = ctypes.POINTER(QParams), ctypes.POINTER(JoinParams)
         XP = ctypes.POINTER(XentParams)
+        RP, AP = ctypes.POINTER(RotaryParams), ctypes.POINTER(AttentionParams)
+        OP = ctypes.POINTER(OrthogonalizeParams)
         sigs = {
             "lowbit_num_words": (i64, [i64, i32]),
             "lowbit_num_blocks": (i64, [i64, i32]),
@@ -111,6 +147,14 @@ def lib() -> ctypes.CDLL:
             "lowbit_linear_xent_workspace": (i64, [XP, i32]),
             "lowbit_linear_xent": (ctypes.c_int, [P, P, P, XP, P, P, P, i64, P]),
             "lowbit_linear_xent_backward": (ctypes.c_int, [P] * 6 + [XP] + [P] * 3 + [i64, P]),
+            "lowbit_rotary_frequencies": (ctypes.c_int, [i32, f64, i32, f64, i64, f64, f64, P, P]),
+            "lowbit_rotary": (ctypes.c_int, [P, P, P, RP, P, P]),
+            "lowbit_rotary_backward": (ctypes.c_int, [P, P, P, RP, P, P]),
+            "lowbit_attention": (ctypes.c_int, [P] * 7 + [AP] + [P] * 3),
+            "lowbit_attention_backward_workspace": (i64, [AP]),
+            "lowbit_attention_backward": (ctypes.c_int, [P] * 10 + [AP] + [P] * 4 + [i64, P]),
+            "lowbit_orthogonalize_workspace": (i64, [OP]),
+            "lowbit_orthogonalize": (ctypes.c_int, [P, OP, P, P, i64, P]),
             "lowbit_stream_probe_u32": (ctypes.c_int, [i32, P, P, i64, ctypes.c_uint32, i32, i32, P]),
         }
         for name, (res, args) in sigs.items():
@@ -746,3 +790,259 @@ def linear_xent_backward(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
         _dev(dloss, "dloss"), _opt(dlse, "dlse"), q, _opt(dx, "dx"), _opt(dw, "dw"),
         _dev(ws, "workspace"), ws.numel(), _stream(x)), "lowbit_linear_xent_backward")
     return LinearXentGrads(dx, dw)
+
+
+_SCALINGS = {None: 0, "linear": 1, "base": 2, "parts": 3}
+_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None,
+                       factor: float = 1.0, original_length: int = 0, slow_turns: float = 1.0,
+                       fast_turns: float = 32.0):
+    """The rot_dim / 2 frequencies of rotary positions in radians a position (a float64 CPU
+    tensor; `rotary` takes it on the GPU), and the scale that goes with them.
+
+    scaling: how a context `factor` times as long is reached: None; "linear": every frequency
+    divided by factor; "base": a larger base, which divides the slowest by it and keeps the
+    fastest; "parts": pairs that turn at most slow_turns times over original_length positions
+    divided, those of at least fast_turns kept, and scale = 0.1 ln(factor) + 1."""
+    if scaling not in _SCALINGS:
+        raise LowbitError(EINVAL, "scaling must be None, 'linear', 'base' or 'parts'")
+    if not 2 <= rot_dim <= 65536:
+        raise LowbitError(EINVAL, "rot_dim must be even, 2 to 65536")
+    freqs = torch.empty(rot_dim // 2, dtype=torch.float64)
+    scale = ctypes.c_float()
+    _check(lib().lowbit_rotary_frequencies(int(rot_dim), base, _SCALINGS[scaling], factor,
+                                           int(original_length), slow_turns, fast_turns,
+                                           freqs.data_ptr(), ctypes.byref(scale)),
+           "lowbit_rotary_frequencies")
+    return freqs, scale.value
+
+
+def _gpu(t: torch.Tensor, what: str) -> int:
+    if not t.is_cuda:
+        raise LowbitError(EINVAL, f"{what} must be a GPU tensor")
+    return t.data_ptr()
+
+
+def _heads(t: torch.Tensor, what: str):
+    """Rows and strides of (..., heads, head_dim): one step for all leading dimensions, dense
+    heads.  (A step of a dimension of one element is of no account.)"""
+    if t.dim() < 2:
+        raise LowbitError(EINVAL, f"{what} must be (..., heads, head_dim)")
+    size, step = t.shape, t.stride()
+    if size[-1] > 1 and step[-1] != 1:
+        raise LowbitError(EINVAL, f"{what}: the elements of a head must be dense")
+    rows, row = 1, None
+    for n, s in zip(size[-3::-1], step[-3::-1]):
+        if n != 1:
+            if row is None:
+                row = s
+            elif s != row * rows and t.numel():
+                raise LowbitError(EINVAL, f"{what}: the leading dimensions must have one step")
+            rows *= n
+    head = step[-2] if size[-2] > 1 else size[-1]
+    return rows, Strides(row if row is not None and rows > 1 else size[-2] * size[-1], head)
+
+
+def _rotary(call, x, freqs, positions, rows_per_sequence, layout, scale, out, what):
+    if layout not in _LAYOUTS:
+        raise LowbitError(EINVAL, "layout must be 'half' or 'interleaved'")
+    rows, xs = _heads(x, what)
+    if freqs.dtype != torch.float64 or freqs.device != x.device:
+        raise LowbitError(EINVAL, "freqs must be float64 on the device of the tensor to turn")
+    if positions is not None and (positions.dtype != torch.int64 or positions.numel() != rows
+                                  or positions.device != x.device):
+        raise LowbitError(EINVAL, "positions must be int64, one for each row")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
+        raise LowbitError(EINVAL, "out must match the input in shape, dtype and device")
+    _, ys = _heads(out, "out")
+    p = RotaryParams(rows, int(rows_per_sequence) or max(rows, 1), xs, ys, x.shape[-2],
+                     x.shape[-1], 2 * freqs.numel(), _LAYOUTS[layout], _dtype_code(x), scale)
+    _check(getattr(lib(), call)(_gpu(x, what), _dev(freqs, "freqs"), _opt(positions, "positions"),
+                                p, _gpu(out, "out"), _stream(x)), call)
+    return out
+
+
+def rotary(x: torch.Tensor, freqs: torch.Tensor, positions: Optional[torch.Tensor] = None,
+           rows_per_sequence: int = 0, layout: str = "half", scale: float = 1.0,
+           out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rotary positions of x (..., heads, head_dim), float32 or bfloat16: the first 2 len(freqs)
+    elements of a head in pairs, (i, i + len(freqs)) for layout "half", (2 i, 2 i + 1) for
+    "interleaved", turned by position * freqs[i] and multiplied by scale; the others copied.
+
+    x may be a view, as of the heads of a packed projection, whose leading dimensions have one
+    step.  freqs, scale: of `rotary_frequencies`, freqs on x's device.  positions: int64, one
+    for each row; without them rows are counted from 0, anew after every rows_per_sequence
+    (0: never).  `out` may be x."""
+    if x.requires_grad:
+        _outside_autograd("rotary")
+    return _rotary("lowbit_rotary", x, freqs, positions, rows_per_sequence, layout, scale, out, "x")
+
+
+def rotary_backward(dy: torch.Tensor, freqs: torch.Tensor,
+                    positions: Optional[torch.Tensor] = None, rows_per_sequence: int = 0,
+                    layout: str = "half", scale: float = 1.0,
+                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of `rotary` by x, with its options.  `out` may be dy."""
+    return _rotary("lowbit_rotary_backward", dy, freqs, positions, rows_per_sequence, layout,
+                   scale, out, "dy")
+
+
+class Attention(NamedTuple):
+    """What attention returns; lse is float32 (query heads, query rows)."""
+    out: torch.Tensor
+    lse: torch.Tensor
+
+
+class AttentionGrads(NamedTuple):
+    """What attention_backward returns."""
+    dq: torch.Tensor
+    dk: torch.Tensor
+    dv: torch.Tensor
+
+
+def _attention_params(q, k, v, q_begin, k_begin, scale, causal, window, prefix, softcap, slopes):
+    """Checks of the tensors' types and sizes, which the C ABI cannot see."""
+    for t, what in ((q, "q"), (k, "k"), (v, "v")):
+        if t.dtype != q.dtype or t.device != q.device:
+            raise LowbitError(EINVAL, "q, k and v must match in dtype and device")
+    if q.dim() not in (3, 4) or k.dim() != q.dim() or k.shape != v.shape:
+        raise LowbitError(EINVAL, "q, k and v must be (rows, heads, head_dim), or (batch, length, "
+                                  "heads, head_dim) for sequences of equal lengths")
+    if q.shape[-1] != k.shape[-1]:
+        raise LowbitError(EINVAL, "q, k and v must have one head_dim")
+    if q.shape[-2] < 1 or k.shape[-2] < 1 or q.shape[-2] % k.shape[-2]:
+        raise LowbitError(EINVAL, "k's heads must divide q's")
+    sequences = 1
+    if q.dim() == 4:
+        if q_begin is not None or k_begin is not None:
+            raise LowbitError(EINVAL, "offsets go with (rows, heads, head_dim)")
+        if k.shape[0] != q.shape[0]:
+            raise LowbitError(EINVAL, "q and k must have one batch")
+        sequences = q.shape[0]
+    for t, what in ((q_begin, "q_begin"), (k_begin, "k_begin")):
+        if t is None:
+            continue
+        if t.dtype != torch.int32 or t.dim() != 1 or t.numel() < 1 or t.device != q.device:
+            raise LowbitError(EINVAL, f"{what} must be int32 offsets, one more than sequences")
+        if what == "k_begin" and q_begin is not None and t.numel() != q_begin.numel():
+            raise LowbitError(EINVAL, "q_begin and k_begin must have the same length")
+        sequences = t.numel() - 1
+    if prefix is not None and (prefix.dtype != torch.int32 or prefix.numel() != sequences
+                               or prefix.device != q.device):
+        raise LowbitError(EINVAL, "prefix must be int32, one for each sequence")
+    if slopes is not None and (slopes.dtype != torch.float32 or slopes.numel() != q.shape[-2]
+                               or slopes.device != q.device):
+        raise LowbitError(EINVAL, "slopes must be float32, one for each head of q")
+    (q_rows, qs), (k_rows, ks), (_, vs) = _heads(q, "q"), _heads(k, "k"), _heads(v, "v")
+    d = q.shape[-1]
+    # (a window beyond 64 bits hides nothing either)
+    p = AttentionParams(q_rows, k_rows, max(-1, min(int(window), 1 << 40)), sequences, q.shape[-2],
+                        k.shape[-2], d, _dtype_code(q), int(bool(causal)),
+                        d ** -0.5 if scale is None else scale, softcap, qs, ks, vs)
+    return p
+
+
+def _attention_out(t, like, what):
+    if t is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
+        raise LowbitError(EINVAL, f"{what} must match in shape, dtype and device")
+    return t
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+              q_begin: Optional[torch.Tensor] = None, k_begin: Optional[torch.Tensor] = None,
+              scale: Optional[float] = None, causal: bool = True, window: int = 0,
+              prefix: Optional[torch.Tensor] = None, softcap: float = 0.0,
+              slopes: Optional[torch.Tensor] = None,
+              out: Optional[torch.Tensor] = None) -> Attention:
+    """Softmax attention within each sequence of packed rows.
+
+    q (rows, heads, head_dim), k and v (key rows, key-value heads, head_dim), float32 or
+    bfloat16, head_dim a multiple of 8 up to 128; key-value heads divide q's and are shared by
+    consecutive ones.  They may be views with dense heads, as of a packed projection.  q_begin,
+    k_begin: int32 offsets of the sequences (one more than there are); k_begin None: the same.
+    Without offsets: one sequence, or for 4-dimensional tensors one for each of the batch.
+
+    With Lq queries and Lk keys query i of a sequence stands at position i + Lk - Lq and sees
+    key j if  j < prefix[s]  or  (not causal or j <= position) and (window == 0 or
+    |position - j| < window).  Scores are softcap * tanh(scale q.k / softcap) (softcap 0: scale
+    q.k; scale None: head_dim ** -0.5) minus slopes[head] * |position - j|.  A query that sees
+    nothing gives 0 and lse -infinity.  Rows outside all sequences are left as they were."""
+    if q.requires_grad or k.requires_grad or v.requires_grad:
+        _outside_autograd("attention")
+    p = _attention_params(q, k, v, q_begin, k_begin, scale, causal, window, prefix, softcap, slopes)
+    out = _attention_out(out, q, "out")
+    p.out = _heads(out, "out")[1]
+    lse = torch.empty(p.q_heads, p.q_rows, dtype=torch.float32, device=q.device)
+    _check(lib().lowbit_attention(_gpu(q, "q"), _gpu(k, "k"), _gpu(v, "v"),
+                                  _opt(q_begin, "q_begin"), _opt(k_begin, "k_begin"),
+                                  _opt(prefix, "prefix"), _opt(slopes, "slopes"), p,
+                                  _gpu(out, "out"), lse.data_ptr(), _stream(q)), "lowbit_attention")
+    return Attention(out, lse)
+
+
+def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                       out: torch.Tensor, lse: torch.Tensor,
+                       q_begin: Optional[torch.Tensor] = None,
+                       k_begin: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                       causal: bool = True, window: int = 0,
+                       prefix: Optional[torch.Tensor] = None, softcap: float = 0.0,
+                       slopes: Optional[torch.Tensor] = None, dq: Optional[torch.Tensor] = None,
+                       dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None) -> AttentionGrads:
+    """Gradients of `attention` by q, k and v from that of out, with the forward call's out, lse
+    and options.  dq, dk, dv may be views, as of a packed projection's gradient."""
+    p = _attention_params(q, k, v, q_begin, k_begin, scale, causal, window, prefix, softcap, slopes)
+    for t, what in ((dout, "dout"), (out, "out")):
+        _attention_out(t, q, what)
+    if lse.dtype != torch.float32 or lse.numel() != p.q_heads * p.q_rows or lse.device != q.device:
+        raise LowbitError(EINVAL, "lse must be the forward call's")
+    dq, dk, dv = (_attention_out(dq, q, "dq"), _attention_out(dk, k, "dk"),
+                  _attention_out(dv, v, "dv"))
+    for name, t in (("out", out), ("dout", dout), ("dq", dq), ("dk", dk), ("dv", dv)):
+        setattr(p, name, _heads(t, name)[1])
+    L = lib()
+    nbytes = L.lowbit_attention_backward_workspace(p)
+    if nbytes < 0 and p.head_dim % 8 == 0 and p.head_dim > 128:
+        raise LowbitError(EUNSUPPORTED, "attention_backward: head_dim above 128")
+    ws = _scratch(nbytes, q, workspace, "attention_backward")
+    _check(L.lowbit_attention_backward(
+        _gpu(dout, "dout"), _gpu(q, "q"), _gpu(k, "k"), _gpu(v, "v"), _gpu(out, "out"),
+        _dev(lse, "lse"), _opt(q_begin, "q_begin"), _opt(k_begin, "k_begin"),
+        _opt(prefix, "prefix"), _opt(slopes, "slopes"), p, _gpu(dq, "dq"), _gpu(dk, "dk"),
+        _gpu(dv, "dv"), _dev(ws, "workspace"), ws.numel(), _stream(q)), "lowbit_attention_backward")
+    return AttentionGrads(dq, dk, dv)
+
+
+def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
+                  eps: float = 1e-7, scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Newton-Schulz iteration on the matrices g (..., rows, columns), float32 or bfloat16:
+
+        X = g / (||g||_F + eps);  steps times  A = X X^T,  X = a X + (b A + c A A) X
+
+    (of the transpose where there are more rows than columns); scale X as bfloat16.  With the
+    default coefficients five steps bring all but the smallest singular values to between 0.7
+    and 1.2.  `out` may be a bfloat16 g."""
+    if g.requires_grad:
+        _outside_autograd("orthogonalize")
+    if g.dim() < 2:
+        raise LowbitError(EINVAL, "g must be (..., rows, columns)")
+    a, b, c = coefficients
+    rows, cols = g.shape[-2:]
+    p = OrthogonalizeParams(g.numel() // (rows * cols) if rows and cols else 0, max(rows, 1),
+                            max(cols, 1), _dtype_code(g), int(steps), a, b, c, eps, scale)
+    if out is None:
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+    elif out.dtype != torch.bfloat16 or out.shape != g.shape or out.device != g.device:
+        raise LowbitError(EINVAL, "out must be bfloat16, of g's shape and device")
+    L = lib()
+    ws = _scratch(L.lowbit_orthogonalize_workspace(p), g, workspace, "orthogonalize")
+    _check(L.lowbit_orthogonalize(_dev(g, "g"), p, _dev(out, "out"), _dev(ws, "workspace"),
+                                  ws.numel(), _stream(g)), "lowbit_orthogonalize")
+    return out
