@@ -23,7 +23,8 @@ constexpr float kLog2e = 1.44269502f;        // log2(e) to binary32
 constexpr float kLn2 = 0.693147182f;
 
 constexpr int kWaves = 4, kAttnThreads = 64 * kWaves;
-constexpr int kRowsPerTile = 32 * kWaves;    // of a workgroup: 32 of each wave
+constexpr int kRowsPerTile = kAttnRows;      // of a workgroup: 32 of each wave
+static_assert(kRowsPerTile == 32 * kWaves, "");
 
 // Scores are kept in units of which exp takes the fewest instructions: of log2 for
 // bfloat16 (2^t), natural ones for binary32, where the rounding error of x log2(e)
@@ -59,6 +60,21 @@ __device__ __forceinline__ void barrier() {
 __device__ __forceinline__ void wait_all() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
+}
+
+// Order for the compiler: N times M matrix instructions, whose operands take R reads of
+// LDS; the reads run AHEAD times ahead.  (Left alone it takes all reads first, for
+// which the registers do not suffice.)
+template <int N, int R, int M, int AHEAD, int I = 0>
+__device__ __forceinline__ void reads_ahead() {
+  if constexpr (I == 0) __builtin_amdgcn_sched_group_barrier(0x100, R * (AHEAD < N ? AHEAD : N), 0);
+  if constexpr (I < N) {
+    __builtin_amdgcn_sched_group_barrier(0x008, M, 0);
+    if constexpr (I + AHEAD < N) __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+    reads_ahead<N, R, M, AHEAD, I + 1>();
+  } else {
+    __builtin_amdgcn_sched_barrier(0);
+  }
 }
 
 // d[row of first][column of second] += sum over 32 bytes of k.  Lane l gives row (column)
@@ -113,15 +129,15 @@ __device__ __forceinline__ void load_floats(__amdgpu_buffer_rsrc_t q, char* lds,
   __builtin_amdgcn_raw_ptr_buffer_load_lds(q, (LOWBIT_LDS void*)lds, 4, lane * 4, 0, 0, 0);
 }
 
-// A tile of ROWS rows of D elements in LDS.  The 16-byte pieces of a row are
-// permuted by its number so that neither the operands that run along a row (32
+// A tile of ROWS rows of D elements in LDS (rows of 96 take the room of 128).  The 16-byte
+// pieces of a row are permuted by its number so that neither the operands that run along a row (32
 // rows, one piece each) nor those that run down the columns (four rows, 32 bytes
 // each) meet a bank of LDS more often than they must.
 template <int DT, int D, int ROWS>
 struct Tile {
-  static constexpr int ES = elem_size<DT>(), PITCH = D * ES, NP = PITCH / 16;
+  static constexpr int ES = elem_size<DT>(), PITCH = (D <= 64 ? 64 : 128) * ES, NP = PITCH / 16;
   static constexpr int BYTES = ROWS * PITCH;
-  static constexpr int STEPS = PITCH / 32;         // operands along a row
+  static constexpr int STEPS = D * ES / 32;        // operands along a row
   static constexpr int BLOCKS = D / 32;            // blocks of 32 columns
   static constexpr int LOADS = BYTES / 1024 / kWaves, PER_LOAD = 1024 / PITCH;
 
@@ -163,6 +179,9 @@ struct Tile {
     __device__ __forceinline__ u32x4 load(const char* lds, int b, int kk) const {
       return *reinterpret_cast<const u32x4*>(lds + (at ^ (kk * 32)) + b * 32 * PITCH);
     }
+    __device__ __forceinline__ void store(char* lds, int kk, u32x4 v) const {
+      *reinterpret_cast<u32x4*>(lds + (at ^ (kk * 32))) = v;
+    }
   };
 
   // Operands down a column: column i * 32 + lane mod 32, rows of chunk c.
@@ -199,6 +218,70 @@ struct Tile {
     }
   };
 };
+
+// Which scores a kernel is built for: plain ones, ones with a distance bias, or capped
+// ones (with a bias, which may be 0).
+enum ScoreMode : int { kPlainScore = 0, kBiasScore = 1, kCapScore = 2 };
+inline int score_mode(const AttnArgs& a) {
+  return a.softcap > 0.0f ? kCapScore : a.slopes ? kBiasScore : kPlainScore;
+}
+
+// What a score is from the products' sum.  Plain ones stay unscaled until their exp, whose
+// argument then is one fused product and sum; a negative scale is turned into the sign of
+// the operand that is held in registers.
+template <int DT, int MODE>
+struct Score {
+  float factor, cap, slope;
+  __device__ __forceinline__ explicit Score(const AttnArgs& g) {
+    const float unit = unit_of<DT>(), scale = fabsf(g.scale);
+    cap = g.softcap * unit;
+    // (a scale of 0 as 2^-100: -infinity times it has to stay what it is)
+    factor = MODE != kCapScore ? fmaxf(scale * unit, 0x1p-100f)
+             : DT == kF32      ? scale / g.softcap
+                               : scale / g.softcap * (2.0f * kLog2e);
+    slope = 0.0f;
+  }
+  __device__ __forceinline__ void head(const AttnArgs& g, int h) {
+    if (MODE != kPlainScore && g.slopes) slope = g.slopes[h] * unit_of<DT>();
+  }
+  // x: a sum of products; distance: |distance - c| to the key.  bend: what the gradient is
+  // multiplied by, 1 - tanh^2
+  __device__ __forceinline__ float at(float x, float distance, int c, float& bend) const {
+    bend = 1.0f;
+    if constexpr (MODE == kPlainScore) return x;
+    float y;
+    if constexpr (MODE == kCapScore) {
+      if constexpr (DT == kF32) {
+        const float t = tanhf(x * factor);
+        bend = __builtin_fmaf(-t, t, 1.0f);
+        y = cap * t;
+      } else {
+        // t = 1 - 2 / (exp(2 x) + 1), off by 2^-23, well below what the weights are rounded to
+        const float r = __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * factor) + 1.0f);
+        const float t = __builtin_fmaf(-2.0f, r, 1.0f);
+        bend = __builtin_fmaf(-t, t, 1.0f);
+        y = cap * t;
+      }
+    } else {
+      y = x * factor;
+    }
+    return __builtin_fmaf(-slope, fabsf(distance - (float)c), y);
+  }
+  // of a largest score, in units
+  __device__ __forceinline__ float scaled(float y) const {
+    return MODE == kPlainScore ? y * factor : y;
+  }
+  // exp(y - base)
+  __device__ __forceinline__ float weight(float y, float base) const {
+    return exp_unit<DT>(MODE == kPlainScore ? __builtin_fmaf(y, factor, -base) : y - base);
+  }
+};
+
+// The signs of an operand's elements turned.
+template <int DT>
+__device__ __forceinline__ u32x4 negated(u32x4 v) {
+  return v ^ (DT == kF32 ? 0x80000000u : 0x80008000u);
+}
 
 // One sequence: its queries and keys in the buffers.
 struct Sequence {

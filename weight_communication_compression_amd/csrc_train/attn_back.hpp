@@ -7,32 +7,6 @@ namespace lowbit {
 
 namespace {
 
-// What a score is from the products' sum: y in units, and for capped scores what its
-// slope is multiplied by (1 - tanh^2).
-template <int DT, bool SHAPED>
-struct Score {
-  float factor, cap, slope;
-  __device__ __forceinline__ Score(const AttnArgs& g, int head) {
-    const float unit = unit_of<DT>();
-    cap = SHAPED && g.softcap > 0.0f ? g.softcap * unit : 0.0f;
-    factor = cap > 0.0f ? g.scale / g.softcap : g.scale * unit;
-    slope = SHAPED && g.slopes ? g.slopes[head] * unit : 0.0f;
-  }
-  __device__ __forceinline__ float at(float x, int distance, float& bend) const {
-    float y = x * factor;
-    bend = 1.0f;
-    if constexpr (SHAPED) {
-      if (cap > 0.0f) {
-        const float t = tanhf(y);
-        bend = __builtin_fmaf(-t, t, 1.0f);
-        y = cap * t;
-      }
-      y -= slope * fabsf((float)distance);
-    }
-    return y;
-  }
-};
-
 // Rows of a result that lies as columns d by rows of lanes: 32 x D.
 template <int DT, int BLOCKS>
 __device__ __forceinline__ void store_columns(char* to, const f32x16 (&acc)[BLOCKS], float scale,
@@ -69,8 +43,8 @@ __device__ __forceinline__ void load_rows(u32x4 (&f)[STEPS], const void* base, i
 // dq: four waves, each 32 queries, as in the forward pass; the scores and dout.v
 // are taken again, transposed, and their gradient is, as it lies, the operand
 // of the product with the keys.
-template <int DT, int D, bool SHAPED>
-__global__ void __launch_bounds__(kAttnThreads, 2) attn_dq_kernel(AttnArgs g, int tiles) {
+template <int DT, int D, int MODE>
+__global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) attn_dq_kernel(AttnArgs g, int tiles) {
   constexpr int KT = DT == kF32 ? 32 : 64, NB = KT / 32, ES = elem_size<DT>();
   using T = Tile<DT, D, KT>;
   __shared__ __attribute__((aligned(1024))) char lk0[T::BYTES];
@@ -103,10 +77,15 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_dq_kernel(AttnArgs g, in
     const int shift = q.lk - q.lq;
     const bool mine = i < q.lq;
     const int64_t row = (int64_t)q.q0 + i;
-    const Score<DT, SHAPED> score(g, head);
+    Score<DT, MODE> score(g);
+    score.head(g, head);
 
     u32x4 fq[T::STEPS], fdo[T::STEPS];
     load_rows(fq, g.q.p, row * g.q.row + head * g.q.head, half, width, mine);
+    if (g.scale < 0.0f) {
+#pragma unroll
+      for (int kk = 0; kk < T::STEPS; ++kk) fq[kk] = negated<DT>(fq[kk]);
+    }
     load_rows(fdo, g.dout.p, row * g.dout.row + head * g.dout.head, half, width, mine);
     float lse = 0.0f, delta = 0.0f;
     if (mine) {
@@ -146,6 +125,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_dq_kernel(AttnArgs g, in
     auto compute = [&](const char* lk, const char* lv, int t) {
       const int j0 = t * KT;
       const bool whole = (j0 + KT <= see.prefix) || (j0 >= wh.low && j0 + KT - 1 <= wl.high);
+      const float distance = (float)(i + shift - j0 - 4 * half);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         f32x16 x, dp;
@@ -162,8 +142,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_dq_kernel(AttnArgs g, in
         for (int r = 0; r < 16; ++r) {
           const int j = r / 4 * 8 + r % 4;
           float bend;
-          const float y = score.at(x[r], i + shift - base - j, bend);
-          float p = exp_unit<DT>(y - lse) * (dp[r] - delta) * bend;
+          const float y = score.at(x[r], distance, 32 * b + j, bend);
+          float p = score.weight(y, lse) * (dp[r] - delta) * bend;
           if (!whole && !(j < pre || (j >= low && j <= high))) p = 0.0f;
           x[r] = p;
         }
@@ -177,23 +157,22 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_dq_kernel(AttnArgs g, in
       }
     };
 
-    int now = after(0);
-    if (now < end) issue(now, lk0, lv0);
-    while (now < end) {
+    // one tile, in lk and lv, while the next one's loads run
+    int now = after(0), next = after(now + 1);
+    auto step = [&](char* lk, char* lv, char* nk, char* nv) {
       wait_all();
       barrier();
-      int next = after(now + 1);
-      if (next < end) issue(next, lk1, lv1);
-      compute(lk0, lv0, now);
+      if (next < end) issue(next, nk, nv);
+      compute(lk, lv, now);
       now = next;
-      if (now >= end) break;
-      wait_all();
-      barrier();
       next = after(now + 1);
-      if (next < end) issue(next, lk0, lv0);
-      compute(lk1, lv1, now);
-      now = next;
+    };
+    if (now < end) issue(now, lk0, lv0);
+    while (next < end) {
+      step(lk0, lv0, lk1, lv1);
+      step(lk1, lv1, lk0, lv0);
     }
+    if (now < end) step(lk0, lv0, lk1, lv1);
     wait_all();
     barrier();
     if (mine)
@@ -202,13 +181,45 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_dq_kernel(AttnArgs g, in
   }
 }
 
+// Room for the parts' sums of dk and dv, as the lanes hold them.
+template <int BLOCKS>
+__device__ __forceinline__ f32x4* part_at(float* parts, int64_t unit) {
+  return reinterpret_cast<f32x4*>(parts) + unit * (2 * BLOCKS * 4 * kAttnThreads) + threadIdx.x;
+}
+
+// Where a workgroup's keys are.
+struct Keys {
+  Sequence q;
+  int j0, kv, part;
+  bool any;
+  int64_t unit;                                    // tile and head, for the parts
+  __device__ __forceinline__ Keys(const AttnArgs& g, const Items& items, int64_t item, int tiles) {
+    int t;
+    items.take(item, g.kv_heads, t, kv, part);
+    any = t < tiles;                               // causal: the first keys are seen by most
+    unit = (int64_t)kv * tiles + t;
+    if (!any) return;
+    const int s = find_sequence(g.k_begin, g.sequences, g.k_rows, kRowsPerTile, t);
+    q = sequence_at(g, s);
+    j0 = (t - first_tile(g.k_begin, s, g.sequences, g.k_rows, kRowsPerTile)) * kRowsPerTile;
+    any = j0 < q.lk;
+  }
+};
+
 // dk and dv: four waves, each 32 keys; the queries of every head that reads them
 // pass by in tiles.  A key a lane and queries down the registers, so that the weights
-// and the scores' gradient are operands as they lie here too.
-template <int DT, int D, bool SHAPED>
-__global__ void __launch_bounds__(kAttnThreads, 2) attn_dkv_kernel(AttnArgs g, int tiles) {
-  constexpr int QT = DT == kF32 ? 32 : 64, NB = QT / 32, ES = elem_size<DT>();
+// and the scores' gradient are operands as they lie here too.  Where there are too few
+// tiles of keys for the chip, the queries of all heads are shared out in g.parts
+// even parts, whose sums a second kernel adds in order.
+template <int DT, int D, int MODE>
+__global__ void __launch_bounds__(kAttnThreads, DT == kF32 ? 1 : 2) attn_dkv_kernel(AttnArgs g, int tiles) {
+  // the wide form's values stay in LDS, since a lane's 256 registers do not hold them too
+  constexpr bool KEEP = D <= (DT == kF32 ? 96 : 64);
+  constexpr int QT = DT == kF32 || !KEEP ? 32 : 64, NB = QT / 32, ES = elem_size<DT>();
   using T = Tile<DT, D, QT>;
+  constexpr int INSTR = DT == kF32 ? 4 : 1;        // matrix instructions of a product
+  using V = Tile<DT, D, 32>;                       // a wave's values
+  __shared__ __attribute__((aligned(1024))) char lvalues[KEEP ? 16 : kWaves * V::BYTES];
   __shared__ __attribute__((aligned(1024))) char lq0[T::BYTES];
   __shared__ __attribute__((aligned(1024))) char ld0[T::BYTES];
   __shared__ __attribute__((aligned(1024))) char lq1[T::BYTES];
@@ -225,17 +236,14 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_dkv_kernel(AttnArgs g, i
   load_d.init(g.dout.row, width, wave, lane);
   along.init(lane);
   down.init(lane);
-  const int32_t* const kb = g.k_begin;
+  Score<DT, MODE> score(g);
 
-  const Items items(tiles, g.kv_heads, 1);
+  const Items items(tiles, g.kv_heads, g.parts);
   for (int64_t item = blockIdx.x; item < items.total; item += gridDim.x) {
-    int t, kv, in;
-    items.take(item, g.kv_heads, t, kv, in);
-    if (t >= tiles) continue;                      // causal: the first keys are seen by most
-    const int s = find_sequence(kb, g.sequences, g.k_rows, kRowsPerTile, t);
-    const Sequence q = sequence_at(g, s);
-    const int j0 = (t - first_tile(kb, s, g.sequences, g.k_rows, kRowsPerTile)) * kRowsPerTile;
-    if (j0 >= q.lk) continue;
+    const Keys w(g, items, item, tiles);
+    if (!w.any) continue;
+    const Sequence& q = w.q;
+    const int kv = w.kv, j0 = w.j0;
     const int j = j0 + wave * 32 + col;            // the lane's key
     const int shift = q.lk - q.lq;
     const bool mine = j < q.lk;
@@ -243,7 +251,16 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_dkv_kernel(AttnArgs g, i
 
     u32x4 fk[T::STEPS], fv[T::STEPS];
     load_rows(fk, g.k.p, row * g.k.row + kv * g.k.head, half, width, mine);
+    if (g.scale < 0.0f) {
+#pragma unroll
+      for (int kk = 0; kk < T::STEPS; ++kk) fk[kk] = negated<DT>(fk[kk]);
+    }
     load_rows(fv, g.v.p, row * g.v.row + kv * g.v.head, half, width, mine);
+    char* const lv = lvalues + wave * V::BYTES;
+    if constexpr (!KEEP) {
+#pragma unroll
+      for (int kk = 0; kk < T::STEPS; ++kk) along.store(lv, kk, fv[kk]);
+    }
 
     // queries low .. high see key j
     auto low_of = [&](int j) {
@@ -256,10 +273,15 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_dkv_kernel(AttnArgs g, i
     const int last = min(j0 + kRowsPerTile, q.lk) - 1;
     const int from = low_of(j0) / QT;
     const int top = j0 < q.prefix ? q.lq - 1 : high_of(last);
-    const int end = top < 0 ? 0 : top / QT + 1;
+    const int across = max(0, (top < 0 ? 0 : top / QT + 1) - from);   // tiles of a head's queries
     // what all 32 keys of the wave are seen by
     const int w0 = j0 + wave * 32, w1 = min(w0 + 31, last);
     const int wlow = low_of(w1), whigh = high_of(max(w0, min(q.prefix, w1)));
+    // this part's tiles of all heads' queries
+    const int64_t all = (int64_t)across * g.group;
+    int left = (int)(all * (w.part + 1) / g.parts - all * w.part / g.parts);
+    const int first = (int)(all * w.part / g.parts);
+    int in = across ? first / across : 0, t = from + (across ? first % across : 0);
 
     f32x16 dk[T::BLOCKS], dv[T::BLOCKS];
 #pragma unroll
@@ -267,86 +289,103 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_dkv_kernel(AttnArgs g, i
 #pragma unroll
       for (int r = 0; r < 16; ++r) dk[n][r] = dv[n][r] = 0.0f;
 
-    for (int in_group = 0; in_group < g.group; ++in_group) {
-      const int head = kv * g.group + in_group;
-      const Score<DT, SHAPED> score(g, head);
-      const char* qp = static_cast<const char*>(g.q.p) + q.q0 * g.q.row + head * g.q.head;
-      const char* dp_ = static_cast<const char*>(g.dout.p) + q.q0 * g.dout.row + head * g.dout.head;
-      const float* info = g.rows_info + (int64_t)head * g.q_rows + q.q0;
-      auto issue = [&](int t, char* lq, char* ld, char* li) {
-        const int rows = q.lq - t * QT;
-        const auto rq = load_q.rows_at(qp + (int64_t)t * QT * g.q.row, (int)g.q.row, width, rows);
-        const auto rd = load_d.rows_at(dp_ + (int64_t)t * QT * g.dout.row, (int)g.dout.row, width, rows);
+    auto issue = [&](char* lq, char* ld, char* li) {
+      const int head = kv * g.group + in;
+      const int rows = q.lq - t * QT;
+      const int64_t at = (int64_t)q.q0 + t * QT;
+      const auto rq = load_q.rows_at(static_cast<const char*>(g.q.p) + at * g.q.row + head * g.q.head,
+                                     (int)g.q.row, width, rows);
+      const auto rd = load_d.rows_at(static_cast<const char*>(g.dout.p) + at * g.dout.row +
+                                         head * g.dout.head, (int)g.dout.row, width, rows);
 #pragma unroll
-        for (int j = 0; j < T::LOADS; ++j) load_q.load(rq, lq, wave, j);
+      for (int j = 0; j < T::LOADS; ++j) load_q.load(rq, lq, wave, j);
 #pragma unroll
-        for (int j = 0; j < T::LOADS; ++j) load_d.load(rd, ld, wave, j);
-        if (wave < 2) {                            // lse, or D
-          const float* p = info + (wave ? (int64_t)g.q_heads * g.q_rows : 0) + t * QT;
-          const auto r = open(p, max(0, min(rows, 64)) * 4);
-          load_floats(r, li + wave * 256, lane);
-        }
-      };
-      auto compute = [&](const char* lq, const char* ld, const char* li, int t) {
-        const int i0 = t * QT;
-        const bool whole = i0 >= wlow && i0 + QT - 1 <= whigh;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          f32x16 x, dp;
-#pragma unroll
-          for (int r = 0; r < 16; ++r) x[r] = dp[r] = 0.0f;
-#pragma unroll
-          for (int kk = 0; kk < T::STEPS; ++kk) {
-            x = mma<DT>(along.load(lq, b, kk), fk[kk], x);
-            dp = mma<DT>(along.load(ld, b, kk), fv[kk], dp);
-          }
-          const int base = i0 + 32 * b + 4 * half;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const f32x4 lse = *reinterpret_cast<const f32x4*>(li + (32 * b + 8 * c + 4 * half) * 4);
-            const f32x4 delta =
-                *reinterpret_cast<const f32x4*>(li + 256 + (32 * b + 8 * c + 4 * half) * 4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int r = 4 * c + e, i = base + 8 * c + e;
-              float bend;
-              const float y = score.at(x[r], i + shift - j, bend);
-              float p = exp_unit<DT>(y - lse[e]);
-              float d = p * (dp[r] - delta[e]) * bend;
-              if (!whole && !(i >= low && i <= high)) p = d = 0.0f;
-              x[r] = p;
-              dp[r] = d;
-            }
-          }
-#pragma unroll
-          for (int c = 0; c < chunks<DT>(); ++c) {
-            const u32x4 p = pack_chunk<DT>(x, c), d = pack_chunk<DT>(dp, c);
-#pragma unroll
-            for (int n = 0; n < T::BLOCKS; ++n) {
-              dv[n] = mma<DT>(down.load(ld, n, b * chunks<DT>() + c), p, dv[n]);
-              dk[n] = mma<DT>(down.load(lq, n, b * chunks<DT>() + c), d, dk[n]);
-            }
-          }
-        }
-      };
-      int now = from;
-      if (now < end) issue(now, lq0, ld0, li0);
-      while (now < end) {
-        wait_all();
-        barrier();
-        if (now + 1 < end) issue(now + 1, lq1, ld1, li1);
-        compute(lq0, ld0, li0, now);
-        if (++now >= end) break;
-        wait_all();
-        barrier();
-        if (now + 1 < end) issue(now + 1, lq0, ld0, li0);
-        compute(lq1, ld1, li1, now);
-        ++now;
+      for (int j = 0; j < T::LOADS; ++j) load_d.load(rd, ld, wave, j);
+      if (wave < 2) {                              // lse, or D
+        const auto r = open(g.rows_info + ((int64_t)wave * g.q_heads + head) * g.q_rows + at,
+                            max(0, min(rows, 64)) * 4);
+        load_floats(r, li + wave * 256, lane);
       }
+    };
+    auto compute = [&](const char* lq, const char* ld, const char* li, int t) {
+      const int i0 = t * QT;
+      const bool whole = i0 >= wlow && i0 + QT - 1 <= whigh;
+      const float distance = (float)(i0 + 4 * half + shift - j);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        f32x16 x, dp;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[r] = dp[r] = 0.0f;
+#pragma unroll
+        for (int kk = 0; kk < T::STEPS; ++kk) {
+          x = mma<DT>(along.load(lq, b, kk), fk[kk], x);
+          dp = mma<DT>(along.load(ld, b, kk), KEEP ? fv[kk] : along.load(lv, 0, kk), dp);
+        }
+        reads_ahead<T::STEPS, KEEP ? 2 : 3, 2 * INSTR, 2>();
+        const int base = i0 + 32 * b + 4 * half;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const f32x4 lse = *reinterpret_cast<const f32x4*>(li + (32 * b + 8 * c + 4 * half) * 4);
+          const f32x4 delta =
+              *reinterpret_cast<const f32x4*>(li + 256 + (32 * b + 8 * c + 4 * half) * 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = 4 * c + e, i = base + 8 * c + e;
+            float bend;
+            const float y = score.at(x[r], distance, -(32 * b + 8 * c + e), bend);
+            float p = score.weight(y, lse[e]);
+            float d = p * (dp[r] - delta[e]) * bend;
+            if (!whole && !(i >= low && i <= high)) p = d = 0.0f;
+            x[r] = p;
+            dp[r] = d;
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int c = 0; c < chunks<DT>(); ++c) {
+          const u32x4 p = pack_chunk<DT>(x, c), d = pack_chunk<DT>(dp, c);
+#pragma unroll
+          for (int n = 0; n < T::BLOCKS; ++n) {
+            dv[n] = mma<DT>(down.load(ld, n, b * chunks<DT>() + c), p, dv[n]);
+            dk[n] = mma<DT>(down.load(lq, n, b * chunks<DT>() + c), d, dk[n]);
+          }
+        }
+        reads_ahead<chunks<DT>() * T::BLOCKS, DT == kF32 ? 8 : 4, 2 * INSTR, 2>();
+      }
+    };
+    // one step: the tile in lq .. li, while the next one's loads run
+    auto step = [&](char* lq, char* ld, char* li, char* nq, char* nd, char* ni, bool more) {
       wait_all();
-      barrier();                                   // (the next head writes the buffers)
+      barrier();
+      const int now = t;
+      score.head(g, kv * g.group + in);
+      if (++t == from + across) {
+        t = from;
+        ++in;
+      }
+      if (more) issue(nq, nd, ni);
+      compute(lq, ld, li, now);
+    };
+    if (left > 0) issue(lq0, ld0, li0);
+    for (; left > 1; left -= 2) {
+      step(lq0, ld0, li0, lq1, ld1, li1, true);
+      step(lq1, ld1, li1, lq0, ld0, li0, left > 2);
     }
-    if (mine) {
+    if (left > 0) step(lq0, ld0, li0, lq1, ld1, li1, false);
+    wait_all();
+    barrier();                                     // (the next item writes the buffers)
+    if (g.parts > 1) {
+      f32x4* to = part_at<T::BLOCKS>(g.part_sums, w.unit * g.parts + w.part);
+#pragma unroll
+      for (int n = 0; n < T::BLOCKS; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          to[(n * 4 + c) * kAttnThreads] =
+              (f32x4){dk[n][4 * c], dk[n][4 * c + 1], dk[n][4 * c + 2], dk[n][4 * c + 3]};
+          to[((T::BLOCKS + n) * 4 + c) * kAttnThreads] =
+              (f32x4){dv[n][4 * c], dv[n][4 * c + 1], dv[n][4 * c + 2], dv[n][4 * c + 3]};
+        }
+    } else if (mine) {
       store_columns<DT>(static_cast<char*>(const_cast<void*>(g.dk.p)) + row * g.dk.row +
                             kv * g.dk.head, dk, g.scale, half, g.head_dim);
       store_columns<DT>(static_cast<char*>(const_cast<void*>(g.dv.p)) + row * g.dv.row +
@@ -355,24 +394,69 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_dkv_kernel(AttnArgs g, i
   }
 }
 
-template <int DT, int D, bool SHAPED>
-lowbit_status launch_back_shaped(const AttnArgs& a, hipStream_t s) {
-  const int qt = a.q_rows / kRowsPerTile + a.sequences, kt = a.k_rows / kRowsPerTile + a.sequences;
-  const Items iq(qt, a.kv_heads, a.group), ik(kt, a.kv_heads, 1);
-  const lowbit_status st = launch(&attn_dkv_kernel<DT, D, SHAPED>,
-                                  ik.total < kMaxBlocks ? ik.total : kMaxBlocks, kAttnThreads, s, a, kt);
-  if (st != LOWBIT_OK) return st;
-  return launch(&attn_dq_kernel<DT, D, SHAPED>, iq.total < kMaxBlocks ? iq.total : kMaxBlocks,
-                kAttnThreads, s, a, qt);
+// The parts' sums, added in order; a workgroup a tile of keys and head, dk or dv.
+template <int DT, int D>
+__global__ void __launch_bounds__(kAttnThreads) attn_dkv_sum_kernel(AttnArgs g, int tiles) {
+  constexpr int BLOCKS = D / 32;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Items items(tiles, g.kv_heads, 2);
+  for (int64_t item = blockIdx.x; item < items.total; item += gridDim.x) {
+    const Keys w(g, items, item, tiles);
+    if (!w.any) continue;
+    f32x16 sum[BLOCKS];
+#pragma unroll
+    for (int n = 0; n < BLOCKS; ++n)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) sum[n][r] = 0.0f;
+    for (int p = 0; p < g.parts; ++p) {
+      const f32x4* from = part_at<BLOCKS>(g.part_sums, w.unit * g.parts + p) +
+                          w.part * (BLOCKS * 4 * kAttnThreads);
+#pragma unroll
+      for (int n = 0; n < BLOCKS; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const f32x4 v = from[(n * 4 + c) * kAttnThreads];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sum[n][4 * c + r] += v[r];
+        }
+    }
+    const int j = w.j0 + wave * 32 + lane % 32;
+    const AttnMatrix& to = w.part ? g.dv : g.dk;
+    if (j < w.q.lk)
+      store_columns<DT>(static_cast<char*>(const_cast<void*>(to.p)) +
+                            ((int64_t)w.q.k0 + j) * to.row + w.kv * to.head, sum,
+                        w.part ? 1.0f : g.scale, lane / 32, g.head_dim);
+  }
+}
+
+inline int64_t capped(int64_t blocks) { return blocks < kMaxBlocks ? blocks : kMaxBlocks; }
+
+template <int DT, int D, int MODE>
+lowbit_status launch_back_width(const AttnArgs& a, hipStream_t s) {
+  const int qt = attn_tiles(a.q_rows, a.sequences), kt = attn_tiles(a.k_rows, a.sequences);
+  const int64_t nk = capped(Items(kt, a.kv_heads, a.parts).total);
+  const int64_t nq = capped(Items(qt, a.kv_heads, a.group).total);
+  lowbit_status st = launch(&attn_dkv_kernel<DT, D, MODE>, nk, kAttnThreads, s, a, kt);
+  if (st == LOWBIT_OK && a.parts > 1)
+    st = launch(&attn_dkv_sum_kernel<DT, D>, capped(Items(kt, a.kv_heads, 2).total), kAttnThreads, s,
+                a, kt);
+  return st == LOWBIT_OK ? launch(&attn_dq_kernel<DT, D, MODE>, nq, kAttnThreads, s, a, qt) : st;
+}
+
+template <int DT, int MODE>
+lowbit_status launch_back_mode(const AttnArgs& a, hipStream_t s) {
+  return a.head_dim <= 64   ? launch_back_width<DT, 64, MODE>(a, s)
+         : a.head_dim <= 96 ? launch_back_width<DT, 96, MODE>(a, s)
+                            : launch_back_width<DT, 128, MODE>(a, s);
 }
 
 template <int DT>
 lowbit_status launch_attn_back(const AttnArgs& a, hipStream_t s) {
-  if (a.softcap > 0.0f || a.slopes)
-    return a.head_dim <= 64 ? launch_back_shaped<DT, 64, true>(a, s)
-                            : launch_back_shaped<DT, 128, true>(a, s);
-  return a.head_dim <= 64 ? launch_back_shaped<DT, 64, false>(a, s)
-                          : launch_back_shaped<DT, 128, false>(a, s);
+  switch (score_mode(a)) {
+    case kPlainScore: return launch_back_mode<DT, kPlainScore>(a, s);
+    case kBiasScore: return launch_back_mode<DT, kBiasScore>(a, s);
+    default: return launch_back_mode<DT, kCapScore>(a, s);
+  }
 }
 
 }  // namespace

@@ -11,16 +11,17 @@ namespace {
 // The scores are taken transposed, keys down the registers and a query a lane,
 // so that the maximum and the sum of a row stay in the lane (and its other half) and
 // the weights are, as they lie, the operand of the product with the values.
-template <int DT, int D, bool SHAPED>
+template <int DT, int D, int MODE>
 struct Forward {
   static constexpr int ES = elem_size<DT>(), KT = DT == kF32 ? 32 : 64, NB = KT / 32;
   using T = Tile<DT, D, KT>;
-  static constexpr float UNIT = unit_of<DT>();
 };
 
-template <int DT, int D, bool SHAPED>
-__global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(AttnArgs g, int tiles) {
-  using F = Forward<DT, D, SHAPED>;
+constexpr float kSlack = 5.5f;                     // e^5.5 < 2^8; in units of log2 2^5.5
+
+template <int DT, int D, int MODE>
+__global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) attn_kernel(AttnArgs g, int tiles) {
+  using F = Forward<DT, D, MODE>;
   using T = typename F::T;
   constexpr int KT = F::KT, NB = F::NB, ES = F::ES;
   __shared__ __attribute__((aligned(1024))) char lk0[T::BYTES];
@@ -37,8 +38,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(AttnArgs g, int t
   load_v.init(g.v.row, width, wave, lane);
   along.init(lane);
   down.init(lane);
-  const float unit = F::UNIT;
-  const float factor = SHAPED && g.softcap > 0.0f ? g.scale / g.softcap : g.scale * unit;
+  Score<DT, MODE> score(g);
 
   const Items items(tiles, g.kv_heads, g.group);
   for (int64_t item = blockIdx.x; item < items.total; item += gridDim.x) {
@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(AttnArgs g, int t
         const int at = kk * 32 + half * 16;
         fq[kk] = (u32x4){0, 0, 0, 0};
         if (mine && at < width) fq[kk] = *reinterpret_cast<const u32x4*>(p + at);
+        if (g.scale < 0.0f) fq[kk] = negated<DT>(fq[kk]);
       }
     }
     const Sight see = sight(g, q, i + shift);
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(AttnArgs g, int t
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[n][r] = 0.0f;
     float top = -INFINITY, sum = 0.0f;             // sum: of this half's keys
-    const float slope = SHAPED && g.slopes ? g.slopes[head] * unit : 0.0f;
+    score.head(g, head);
 
     auto compute = [&](const char* lk, const char* lv, int t) {
       f32x16 x[NB];
@@ -110,18 +111,14 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(AttnArgs g, int t
       }
       const int j0 = t * KT;
       const bool whole = (j0 + KT <= see.prefix) || (j0 >= wh.low && j0 + KT - 1 <= wl.high);
+      const float distance = (float)(i + shift - j0 - 4 * half);
       float most = -INFINITY;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          float y = x[b][r] * factor;
-          if constexpr (SHAPED) {
-            if (g.softcap > 0.0f) y = g.softcap * unit * tanhf(y);
-            const int j = j0 + 32 * b + 4 * half + r / 4 * 8 + r % 4;
-            y -= slope * fabsf((float)(i + shift - j));
-          }
-          x[b][r] = y;
+          float bend;
+          x[b][r] = score.at(x[b][r], distance, 32 * b + r / 4 * 8 + r % 4, bend);
         }
         if (!whole) {
           const int base = j0 + 32 * b + 4 * half;
@@ -135,8 +132,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(AttnArgs g, int t
 #pragma unroll
         for (int r = 0; r < 16; ++r) most = fmaxf(most, x[b][r]);
       }
-      most = other_half_max(most);
-      if (__any(most > top)) {
+      most = score.scaled(other_half_max(most));
+      // the sums stand relative to `top`, which follows the largest score only when it is
+      // passed by more than kSlack: weights then are up to 2^8, which loses nothing, and
+      // later tiles hardly ever rescale what has been summed
+      if (__any(most > top + kSlack)) {
         const float next = fmaxf(top, most);
         const float shrink = next == -INFINITY ? 1.0f : exp_unit<DT>(top - next);
         top = next;
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(AttnArgs g, int t
       for (int b = 0; b < NB; ++b) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          x[b][r] = exp_unit<DT>(x[b][r] - base);
+          x[b][r] = score.weight(x[b][r], base);
           sum += x[b][r];
         }
 #pragma unroll
@@ -162,23 +162,22 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(AttnArgs g, int t
       }
     };
 
-    int now = after(0);
-    if (now < end) issue(now, lk0, lv0);
-    while (now < end) {
+    // one tile, in lk and lv, while the next one's loads run
+    int now = after(0), next = after(now + 1);
+    auto step = [&](char* lk, char* lv, char* nk, char* nv) {
       wait_all();
       barrier();
-      int next = after(now + 1);
-      if (next < end) issue(next, lk1, lv1);
-      compute(lk0, lv0, now);
+      if (next < end) issue(next, nk, nv);
+      compute(lk, lv, now);
       now = next;
-      if (now >= end) break;
-      wait_all();
-      barrier();
       next = after(now + 1);
-      if (next < end) issue(next, lk0, lv0);
-      compute(lk1, lv1, now);
-      now = next;
+    };
+    if (now < end) issue(now, lk0, lv0);
+    while (next < end) {
+      step(lk0, lv0, lk1, lv1);
+      step(lk1, lv1, lk0, lv0);
     }
+    if (now < end) step(lk0, lv0, lk1, lv1);
     wait_all();
     barrier();                                     // (the next item writes the buffers)
 
@@ -207,21 +206,26 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(AttnArgs g, int t
   }
 }
 
-inline int attn_tiles(int rows, int sequences, int T) { return rows / T + sequences; }
-
 template <int DT, int D>
 lowbit_status launch_attn_width(const AttnArgs& a, hipStream_t s) {
-  const int tiles = attn_tiles(a.q_rows, a.sequences, kRowsPerTile);
+  const int tiles = attn_tiles(a.q_rows, a.sequences);
   const Items items(tiles, a.kv_heads, a.group);
   const int64_t blocks = items.total < kMaxBlocks ? items.total : kMaxBlocks;
-  return a.softcap > 0.0f || a.slopes
-             ? launch(&attn_kernel<DT, D, true>, blocks, kAttnThreads, s, a, tiles)
-             : launch(&attn_kernel<DT, D, false>, blocks, kAttnThreads, s, a, tiles);
+  switch (score_mode(a)) {
+    case kPlainScore:
+      return launch(&attn_kernel<DT, D, kPlainScore>, blocks, kAttnThreads, s, a, tiles);
+    case kBiasScore:
+      return launch(&attn_kernel<DT, D, kBiasScore>, blocks, kAttnThreads, s, a, tiles);
+    default:
+      return launch(&attn_kernel<DT, D, kCapScore>, blocks, kAttnThreads, s, a, tiles);
+  }
 }
 
 template <int DT>
 lowbit_status launch_attn(const AttnArgs& a, hipStream_t s) {
-  return a.head_dim <= 64 ? launch_attn_width<DT, 64>(a, s) : launch_attn_width<DT, 128>(a, s);
+  return a.head_dim <= 64   ? launch_attn_width<DT, 64>(a, s)
+         : a.head_dim <= 96 ? launch_attn_width<DT, 96>(a, s)
+                            : launch_attn_width<DT, 128>(a, s);
 }
 
 }  // namespace

@@ -31,12 +31,19 @@ struct AttnMatrix {
   int64_t row, head;         // bytes
 };
 
+constexpr int kAttnRows = 128;   // of a workgroup's tile of queries, or of keys
+
+// As many tiles as sequences of any lengths may have.
+inline int attn_tiles(int64_t rows, int sequences) { return (int)(rows / kAttnRows) + sequences; }
+
 struct AttnArgs {
   AttnMatrix q, k, v, o, dout, dq, dk, dv;
   const int32_t *q_begin, *k_begin, *prefix;   // may be null
   const float* slopes;       // may be null
   float* lse;                // q_heads x q_rows
   float* rows_info;          // gradient: q_heads x q_rows of lse, then of D
+  float* part_sums;          // gradient: dk's and dv's, where there are several parts
+  int32_t parts;
   int32_t q_rows, k_rows, sequences;
   int32_t q_heads, kv_heads, group;
   int32_t head_dim;

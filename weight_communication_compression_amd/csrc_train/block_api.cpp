@@ -129,6 +129,28 @@ AttnArgs attention_args(const void* q, const void* k, const void* v, const void*
   return a;
 }
 
+// The gradient's workspace: lse and D of each query row, the parts' sums of dk and dv.
+struct AttnPlan {
+  int parts;
+  int64_t sums, bytes;
+};
+
+// The chip holds 512 workgroups of the gradient by k and v at one time.  A causal
+// sequence's take from nothing to twice the mean, so two rounds of them, the long ones
+// first, are wanted; fewer are cut into parts of at least 256 queries of all heads.
+AttnPlan attn_plan(const lowbit_attention_params* p) {
+  AttnPlan w{};
+  const int64_t tiles = attn_tiles(p->k_rows, p->sequences) * (int64_t)p->kv_heads;
+  const int64_t group = p->q_heads / p->kv_heads;
+  int64_t parts = tiles ? (1024 + tiles - 1) / tiles : 1;
+  parts = std::min(parts, p->sequences ? p->q_rows * group / p->sequences / 256 : 1);
+  w.parts = (int)std::max<int64_t>(1, std::min<int64_t>(parts, 16));
+  w.sums = up(p->q_rows * p->q_heads * 8, 256);
+  const int width = p->head_dim <= 64 ? 64 : p->head_dim <= 96 ? 96 : 128;
+  w.bytes = w.sums + (w.parts > 1 ? tiles * w.parts * 2 * kAttnRows * width * 4 : 0);
+  return w;
+}
+
 bool check_ortho(const lowbit_orthogonalize_params* p) {
   if (!p || !within(p->batch, 0, 1 << 20) || !within(p->rows, 1, 65536) ||
       !within(p->cols, 1, 65536) || !valid_dtype(p->type) || !within(p->steps, 0, 64) ||
@@ -230,7 +252,7 @@ lowbit_status lowbit_attention(const void* q, const void* k, const void* v,
 }
 
 int64_t lowbit_attention_backward_workspace(const lowbit_attention_params* p) {
-  return check_attention(p) == LOWBIT_OK ? up(p->q_rows * p->q_heads * 8, 256) : -1;
+  return check_attention(p) == LOWBIT_OK ? attn_plan(p).bytes : -1;
 }
 
 lowbit_status lowbit_attention_backward(const void* dout, const void* q, const void* k,
@@ -253,9 +275,8 @@ lowbit_status lowbit_attention_backward(const void* dout, const void* q, const v
   if (p->q_rows > 0 && (!good(q) || !good(dout) || !good(out) || !good(lse) || !good(dq)))
     return LOWBIT_EINVAL;
   if (p->k_rows > 0 && (!good(k) || !good(v) || !good(dk) || !good(dv))) return LOWBIT_EINVAL;
-  if (p->q_rows > 0 &&
-      (!good(workspace) || workspace_bytes < lowbit_attention_backward_workspace(p)))
-    return LOWBIT_EINVAL;
+  const AttnPlan plan = attn_plan(p);
+  if (plan.bytes > 0 && (!good(workspace) || workspace_bytes < plan.bytes)) return LOWBIT_EINVAL;
   AttnArgs a = attention_args(q, k, v, out, const_cast<float*>(lse), q_begin, k_begin, prefix,
                               slopes, p);
   const int es = elem(p->type);
@@ -264,6 +285,8 @@ lowbit_status lowbit_attention_backward(const void* dout, const void* q, const v
   a.dk = matrix(dk, p->dk, es);
   a.dv = matrix(dv, p->dv, es);
   a.rows_info = static_cast<float*>(workspace);
+  a.parts = plan.parts;
+  a.part_sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.sums);
   if (p->q_rows > 0) {
     const lowbit_status sd = launch_attn_delta(p->type, a, stream);
     if (sd != LOWBIT_OK) return sd;
