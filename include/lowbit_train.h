@@ -271,6 +271,10 @@ typedef struct {
     lowbit_strides dout, dq, dk, dv;   /* the gradient's                        */
 } lowbit_attention_params;
 
+/* Bytes of workspace that the forward (backward = 0) or the backward call
+ * (backward = 1) needs, or -1 for invalid params; 0 where it takes none. */
+int64_t lowbit_attention_workspace(const lowbit_attention_params* p, int32_t backward);
+
 /*
  * Attention.  Sequence s has the queries q_begin[s] .. q_begin[s + 1] - 1 and the
  * keys k_begin[s] .. k_begin[s + 1] - 1, Lq and Lk of them.  Its query i stands at
@@ -299,17 +303,13 @@ typedef struct {
  * 2^-8 each, relative.  NaN and infinities of a key or value that a query does not
  * see reach it only within its own sequence.
  * EINVAL: p == NULL, a size, type, option or stride outside its range, NULL or
- * misaligned pointer with rows and sequences > 0.  EUNSUPPORTED: head_dim above 128.
+ * misaligned pointer with rows and sequences > 0, workspace too small.  EUNSUPPORTED: head_dim above 128.
  */
 lowbit_status lowbit_attention(const void* q, const void* k, const void* v,
                                const int32_t* q_begin, const int32_t* k_begin,
                                const int32_t* prefix, const float* slopes,
                                const lowbit_attention_params* p, void* out, float* lse,
-                               hipStream_t stream);
-
-/* Bytes of workspace that lowbit_attention_backward needs, or -1 for invalid
- * params. */
-int64_t lowbit_attention_backward_workspace(const lowbit_attention_params* p);
+                               void* workspace, int64_t workspace_bytes, hipStream_t stream);
 
 /*
  * Its gradient, from the gradient of out and the forward call's out and lse:

@@ -113,7 +113,7 @@ def _params(**change):
 def _both(p, q=OK16, k=OK16, v=OK16, qb=OK16, kb=None, pre=None, sl=None, out=OK16, lse=OK16,
           ws=OK16, bytes=1 << 40, dq=OK16, dk=OK16, dv=OK16, dout=OK16):
     lib = L.lib()
-    return (lib.lowbit_attention(q, k, v, qb, kb, pre, sl, p, out, lse, None),
+    return (lib.lowbit_attention(q, k, v, qb, kb, pre, sl, p, out, lse, ws, bytes, None),
             lib.lowbit_attention_backward(dout, q, k, v, out, lse, qb, kb, pre, sl, p, dq, dk, dv,
                                           ws, bytes, None))
 
@@ -154,9 +154,18 @@ def test_attention_refusals():
 
 
 def test_attention_workspace():
-    ws = L.lib().lowbit_attention_backward_workspace
-    assert ws(_params()) >= 100 * 4 * 8 and ws(_params(q_rows=0)) == 0
-    assert ws(_params(type=3)) == -1 and ws(_params(head_dim=136)) == -1 and ws(None) == -1
+    ws = L.lib().lowbit_attention_workspace
+    assert ws(_params(), 1) >= 100 * 4 * 8 and ws(_params(q_rows=0, k_rows=0), 1) == 0
+    assert ws(_params(), 0) == 0 and ws(_params(q_rows=0, k_rows=0), 0) == 0
+    # few queries against many keys, and the other way round: parts of sums
+    few = _params(q_rows=2, k_rows=20000)
+    assert ws(few, 0) > 0 and _both(few, kb=OK16, bytes=ws(few, 0) - 1)[0] == L.EINVAL
+    assert _both(few, kb=OK16, ws=None)[0] == L.EINVAL
+    many = _params(q_rows=20000, k_rows=2)
+    assert ws(many, 0) == 0 and ws(many, 1) > 20000 * 4 * 8
+    for back in (0, 1):
+        assert ws(_params(type=3), back) == -1 and ws(_params(head_dim=136), back) == -1
+        assert ws(None, back) == -1
 
 
 def test_attention_binding_refusals():

@@ -141,6 +141,17 @@ def test_many_rows():
 
 
 @BOTH
+@pytest.mark.parametrize("shape", [dict(), dict(window=100), dict(prefix=[900, 5]),
+                                   dict(softcap=10.0, slopes=True), dict(causal=False)])
+def test_parts(shape, dtype):
+    """Few tiles of queries or keys: keys and queries in parts."""
+    run([700, 900], dtype=dtype, heads=1, dim=64, **shape)
+    run([3, 600], [1500, 1100], dtype=dtype, heads=2, dim=80, **shape)
+    run([900, 1200], [40, 1], dtype=dtype, heads=4, dim=128, **{**shape, "prefix": None})
+    run([1, 1], [2000, 1300], dtype=dtype, heads=4, **{**shape, "prefix": None})
+
+
+@BOTH
 def test_batches(dtype):
     g = torch.Generator().manual_seed(2)
     q, k, v = (torch.randn(3, n, h, 64, generator=g).to(dtype).cuda()

@@ -370,6 +370,124 @@ struct Items {
 };
 
 constexpr int64_t kMaxBlocks = 1 << 20;            // (a multiple of 8)
+inline int64_t capped(int64_t blocks) { return blocks < kMaxBlocks ? blocks : kMaxBlocks; }
+
+// A workgroup's tile of queries of one head, and which part of their keys it takes.
+struct Queries {
+  Sequence q;
+  int i0, last, head, kv, part;                    // last: the last query of the tile
+  bool any;
+  int64_t unit;                                    // tile and head
+  __device__ __forceinline__ Queries(const AttnArgs& g, const Items& items, int64_t item, int tiles,
+                                     int parts) {
+    int t, in;
+    items.take(item, g.kv_heads, t, kv, in);
+    part = in % parts;
+    head = kv * g.group + in / parts;
+    any = t < tiles;
+    t = tiles - 1 - t;                             // causal: the last see most
+    unit = (int64_t)head * tiles + t;
+    if (!any) return;
+    const int s = find_sequence(g.q_begin, g.sequences, g.q_rows, kRowsPerTile, t);
+    q = sequence_at(g, s);
+    i0 = (t - first_tile(g.q_begin, s, g.sequences, g.q_rows, kRowsPerTile)) * kRowsPerTile;
+    last = min(i0 + kRowsPerTile, q.lq) - 1;
+    any = i0 < q.lq;
+  }
+};
+
+// The tiles of KT keys that a tile of queries sees: those of the prefix, then those around
+// the positions; in order, and those of one of `parts` even parts.
+template <int KT>
+struct KeyTiles {
+  int before, from, first, count;
+  __device__ __forceinline__ KeyTiles(const AttnArgs& g, const Queries& w, int parts) {
+    const int shift = w.q.lk - w.q.lq;
+    const Sight lo = sight(g, w.q, w.i0 + shift), hi = sight(g, w.q, w.last + shift);
+    before = (w.q.prefix + KT - 1) / KT;
+    from = max(before, lo.low > 0 ? lo.low / KT : 0);
+    const int to = hi.high < 0 ? 0 : hi.high / KT + 1;
+    const int64_t all = before + max(0, to - from);
+    first = (int)(all * w.part / parts);
+    count = (int)(all * (w.part + 1) / parts) - first;
+  }
+  // the u-th of this part
+  __device__ __forceinline__ int tile(int u) const {
+    u += first;
+    return u < before ? u : from + (u - before);
+  }
+};
+
+// Room for a part's sums, as the lanes hold them: `vectors` of four for each.
+__device__ __forceinline__ f32x4* part_at(float* parts, int64_t unit, int vectors) {
+  return reinterpret_cast<f32x4*>(parts) + unit * (vectors * kAttnThreads) + threadIdx.x;
+}
+template <int BLOCKS>
+__device__ __forceinline__ void store_part(f32x4* to, const f32x16 (&acc)[BLOCKS]) {
+#pragma unroll
+  for (int n = 0; n < BLOCKS; ++n)
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      to[(n * 4 + c) * kAttnThreads] =
+          (f32x4){acc[n][4 * c], acc[n][4 * c + 1], acc[n][4 * c + 2], acc[n][4 * c + 3]};
+}
+template <int BLOCKS>
+__device__ __forceinline__ void add_part(f32x16 (&sum)[BLOCKS], const f32x4* from, float weight) {
+#pragma unroll
+  for (int n = 0; n < BLOCKS; ++n)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const f32x4 v = from[(n * 4 + c) * kAttnThreads];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sum[n][4 * c + r] = __builtin_fmaf(v[r], weight, sum[n][4 * c + r]);
+    }
+}
+template <int BLOCKS>
+__device__ __forceinline__ void clear(f32x16 (&acc)[BLOCKS]) {
+#pragma unroll
+  for (int n = 0; n < BLOCKS; ++n)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[n][r] = 0.0f;
+}
+
+// Rows of a result that lies as columns d by rows of lanes; its blocks of 32 columns are the
+// matrix's from `first` on.
+template <int DT, int BLOCKS>
+__device__ __forceinline__ void store_columns(char* to, const f32x16 (&acc)[BLOCKS], float scale,
+                                              int half, int head_dim, int first = 0) {
+#pragma unroll
+  for (int n = 0; n < BLOCKS; ++n)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int at = (first + n) * 32 + c * 8 + half * 4;
+      f32x4 v;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = acc[n][4 * c + r] * scale;
+      if (at < head_dim) {
+        if constexpr (DT == kF32) *reinterpret_cast<f32x4*>(to + at * 4) = v;
+        else *reinterpret_cast<u32x2*>(to + at * 2) =
+                 (u32x2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+      }
+    }
+}
+
+// The operands along a row of one matrix, straight from memory.
+template <int STEPS>
+__device__ __forceinline__ void load_rows(u32x4 (&f)[STEPS], const void* base, int64_t at, int half,
+                                          int width, bool any) {
+  const char* p = static_cast<const char*>(base) + at;
+#pragma unroll
+  for (int kk = 0; kk < STEPS; ++kk) {
+    const int c = kk * 32 + half * 16;
+    f[kk] = (u32x4){0, 0, 0, 0};
+    if (any && c < width) f[kk] = *reinterpret_cast<const u32x4*>(p + c);
+  }
+}
+template <int DT, int STEPS>
+__device__ __forceinline__ void negate(u32x4 (&f)[STEPS]) {
+#pragma unroll
+  for (int kk = 0; kk < STEPS; ++kk) f[kk] = negated<DT>(f[kk]);
+}
 
 }  // namespace
 

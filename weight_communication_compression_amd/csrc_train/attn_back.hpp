@@ -7,39 +7,6 @@ namespace lowbit {
 
 namespace {
 
-// Rows of a result that lies as columns d by rows of lanes: 32 x D.
-template <int DT, int BLOCKS>
-__device__ __forceinline__ void store_columns(char* to, const f32x16 (&acc)[BLOCKS], float scale,
-                                              int half, int head_dim) {
-#pragma unroll
-  for (int n = 0; n < BLOCKS; ++n)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int at = n * 32 + c * 8 + half * 4;
-      f32x4 v;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = acc[n][4 * c + r] * scale;
-      if (at < head_dim) {
-        if constexpr (DT == kF32) *reinterpret_cast<f32x4*>(to + at * 4) = v;
-        else *reinterpret_cast<u32x2*>(to + at * 2) =
-                 (u32x2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-      }
-    }
-}
-
-// The operands along a row of one matrix, straight from memory.
-template <int STEPS>
-__device__ __forceinline__ void load_rows(u32x4 (&f)[STEPS], const void* base, int64_t at, int half,
-                                          int width, bool any) {
-  const char* p = static_cast<const char*>(base) + at;
-#pragma unroll
-  for (int kk = 0; kk < STEPS; ++kk) {
-    const int c = kk * 32 + half * 16;
-    f[kk] = (u32x4){0, 0, 0, 0};
-    if (any && c < width) f[kk] = *reinterpret_cast<const u32x4*>(p + c);
-  }
-}
-
 // dq: four waves, each 32 queries, as in the forward pass; the scores and dout.v
 // are taken again, transposed, and their gradient is, as it lies, the operand
 // of the product with the keys.
@@ -62,31 +29,24 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
   along.init(lane);
   down.init(lane);
 
-  const Items items(tiles, g.kv_heads, g.group);
+  Score<DT, MODE> score(g);
+
+  const Items items(tiles, g.kv_heads, g.group * g.q_parts);
   for (int64_t item = blockIdx.x; item < items.total; item += gridDim.x) {
-    int t, kv, in;
-    items.take(item, g.kv_heads, t, kv, in);
-    if (t >= tiles) continue;
-    t = tiles - 1 - t;
-    const int head = kv * g.group + in;
-    const int s = find_sequence(g.q_begin, g.sequences, g.q_rows, kRowsPerTile, t);
-    const Sequence q = sequence_at(g, s);
-    const int i0 = (t - first_tile(g.q_begin, s, g.sequences, g.q_rows, kRowsPerTile)) * kRowsPerTile;
-    if (i0 >= q.lq) continue;
-    const int i = i0 + wave * 32 + col;
+    const Queries w(g, items, item, tiles, g.q_parts);
+    if (!w.any) continue;
+    const Sequence& q = w.q;
+    const int kv = w.kv, head = w.head, last = w.last;
+    const int i = w.i0 + wave * 32 + col;
     const int shift = q.lk - q.lq;
     const bool mine = i < q.lq;
     const int64_t row = (int64_t)q.q0 + i;
-    Score<DT, MODE> score(g);
     score.head(g, head);
 
     u32x4 fq[T::STEPS], fdo[T::STEPS];
     load_rows(fq, g.q.p, row * g.q.row + head * g.q.head, half, width, mine);
-    if (g.scale < 0.0f) {
-#pragma unroll
-      for (int kk = 0; kk < T::STEPS; ++kk) fq[kk] = negated<DT>(fq[kk]);
-    }
     load_rows(fdo, g.dout.p, row * g.dout.row + head * g.dout.head, half, width, mine);
+    if (g.scale < 0.0f) negate<DT>(fq);
     float lse = 0.0f, delta = 0.0f;
     if (mine) {
       const float* info = g.rows_info + (int64_t)head * g.q_rows + row;
@@ -94,14 +54,8 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
       delta = info[(int64_t)g.q_heads * g.q_rows];
     }
     const Sight see = sight(g, q, i + shift);
-    const int last = min(i0 + kRowsPerTile, q.lq) - 1;
-    const Sight lo = sight(g, q, i0 + shift), hi = sight(g, q, last + shift);
-    const int before = (q.prefix + KT - 1) / KT;
-    const int from = lo.low > 0 ? lo.low / KT : 0;
-    const int to = hi.high < 0 ? 0 : hi.high / KT + 1;
-    const int end = max(before, to);
-    auto after = [&](int t) { return t >= before && t < from ? from : t; };
-    const int w0 = i0 + wave * 32 + shift, w1 = min(w0 + 31, last + shift);
+    const KeyTiles<KT> keys(g, w, g.q_parts);
+    const int w0 = w.i0 + wave * 32 + shift, w1 = min(w0 + 31, last + shift);
     const Sight wl = sight(g, q, w0), wh = sight(g, q, w1);
 
     const char* kp = static_cast<const char*>(g.k.p) + q.k0 * g.k.row + kv * g.k.head;
@@ -117,10 +71,7 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
     };
 
     f32x16 acc[T::BLOCKS];
-#pragma unroll
-    for (int n = 0; n < T::BLOCKS; ++n)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[n][r] = 0.0f;
+    clear(acc);
 
     auto compute = [&](const char* lk, const char* lv, int t) {
       const int j0 = t * KT;
@@ -157,34 +108,49 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
       }
     };
 
-    // one tile, in lk and lv, while the next one's loads run
-    int now = after(0), next = after(now + 1);
-    auto step = [&](char* lk, char* lv, char* nk, char* nv) {
+    // tile u, in lk and lv, while the next one's loads run
+    auto step = [&](char* lk, char* lv, char* nk, char* nv, int u) {
       wait_all();
       barrier();
-      if (next < end) issue(next, nk, nv);
-      compute(lk, lv, now);
-      now = next;
-      next = after(now + 1);
+      if (u + 1 < keys.count) issue(keys.tile(u + 1), nk, nv);
+      compute(lk, lv, keys.tile(u));
     };
-    if (now < end) issue(now, lk0, lv0);
-    while (next < end) {
-      step(lk0, lv0, lk1, lv1);
-      step(lk1, lv1, lk0, lv0);
+    if (keys.count > 0) issue(keys.tile(0), lk0, lv0);
+    int u = 0;
+    for (; u + 1 < keys.count; u += 2) {
+      step(lk0, lv0, lk1, lv1, u);
+      step(lk1, lv1, lk0, lv0, u + 1);
     }
-    if (now < end) step(lk0, lv0, lk1, lv1);
+    if (u < keys.count) step(lk0, lv0, lk1, lv1, u);
     wait_all();
-    barrier();
-    if (mine)
+    barrier();                                     // (the next item writes the buffers)
+    if (g.q_parts > 1)
+      store_part(part_at(g.q_sums, w.unit * g.q_parts + w.part, T::BLOCKS * 4), acc);
+    else if (mine)
       store_columns<DT>(static_cast<char*>(const_cast<void*>(g.dq.p)) + row * g.dq.row +
                             head * g.dq.head, acc, g.scale, half, g.head_dim);
   }
 }
 
-// Room for the parts' sums of dk and dv, as the lanes hold them.
-template <int BLOCKS>
-__device__ __forceinline__ f32x4* part_at(float* parts, int64_t unit) {
-  return reinterpret_cast<f32x4*>(parts) + unit * (2 * BLOCKS * 4 * kAttnThreads) + threadIdx.x;
+// The parts' sums of dq, added in order; a workgroup 32 columns of a tile.
+template <int DT, int D>
+__global__ void __launch_bounds__(kAttnThreads) attn_dq_sum_kernel(AttnArgs g, int tiles) {
+  constexpr int BLOCKS = D / 32;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Items items(tiles, g.kv_heads, g.group * BLOCKS);
+  for (int64_t item = blockIdx.x; item < items.total; item += gridDim.x) {
+    const Queries w(g, items, item, tiles, BLOCKS);
+    const int i = w.i0 + wave * 32 + lane % 32;
+    if (!w.any || i >= w.q.lq) continue;
+    f32x16 sum[1];
+    clear(sum);
+    for (int p = 0; p < g.q_parts; ++p)
+      add_part(sum, part_at(g.q_sums, w.unit * g.q_parts + p, BLOCKS * 4) +
+                        w.part * (4 * kAttnThreads), 1.0f);
+    store_columns<DT>(static_cast<char*>(const_cast<void*>(g.dq.p)) +
+                          ((int64_t)w.q.q0 + i) * g.dq.row + w.head * g.dq.head, sum, g.scale,
+                      lane / 32, g.head_dim, w.part);
+  }
 }
 
 // Where a workgroup's keys are.
@@ -209,7 +175,7 @@ struct Keys {
 // dk and dv: four waves, each 32 keys; the queries of every head that reads them
 // pass by in tiles.  A key a lane and queries down the registers, so that the weights
 // and the scores' gradient are operands as they lie here too.  Where there are too few
-// tiles of keys for the chip, the queries of all heads are shared out in g.parts
+// tiles of keys for the chip, the queries of all heads are shared out in g.k_parts
 // even parts, whose sums a second kernel adds in order.
 template <int DT, int D, int MODE>
 __global__ void __launch_bounds__(kAttnThreads, DT == kF32 ? 1 : 2) attn_dkv_kernel(AttnArgs g, int tiles) {
@@ -238,7 +204,7 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 ? 1 : 2) attn_dkv_ker
   down.init(lane);
   Score<DT, MODE> score(g);
 
-  const Items items(tiles, g.kv_heads, g.parts);
+  const Items items(tiles, g.kv_heads, g.k_parts);
   for (int64_t item = blockIdx.x; item < items.total; item += gridDim.x) {
     const Keys w(g, items, item, tiles);
     if (!w.any) continue;
@@ -251,10 +217,7 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 ? 1 : 2) attn_dkv_ker
 
     u32x4 fk[T::STEPS], fv[T::STEPS];
     load_rows(fk, g.k.p, row * g.k.row + kv * g.k.head, half, width, mine);
-    if (g.scale < 0.0f) {
-#pragma unroll
-      for (int kk = 0; kk < T::STEPS; ++kk) fk[kk] = negated<DT>(fk[kk]);
-    }
+    if (g.scale < 0.0f) negate<DT>(fk);
     load_rows(fv, g.v.p, row * g.v.row + kv * g.v.head, half, width, mine);
     char* const lv = lvalues + wave * V::BYTES;
     if constexpr (!KEEP) {
@@ -279,15 +242,13 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 ? 1 : 2) attn_dkv_ker
     const int wlow = low_of(w1), whigh = high_of(max(w0, min(q.prefix, w1)));
     // this part's tiles of all heads' queries
     const int64_t all = (int64_t)across * g.group;
-    int left = (int)(all * (w.part + 1) / g.parts - all * w.part / g.parts);
-    const int first = (int)(all * w.part / g.parts);
+    int left = (int)(all * (w.part + 1) / g.k_parts - all * w.part / g.k_parts);
+    const int first = (int)(all * w.part / g.k_parts);
     int in = across ? first / across : 0, t = from + (across ? first % across : 0);
 
     f32x16 dk[T::BLOCKS], dv[T::BLOCKS];
-#pragma unroll
-    for (int n = 0; n < T::BLOCKS; ++n)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) dk[n][r] = dv[n][r] = 0.0f;
+    clear(dk);
+    clear(dv);
 
     auto issue = [&](char* lq, char* ld, char* li) {
       const int head = kv * g.group + in;
@@ -374,17 +335,10 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 ? 1 : 2) attn_dkv_ker
     if (left > 0) step(lq0, ld0, li0, lq1, ld1, li1, false);
     wait_all();
     barrier();                                     // (the next item writes the buffers)
-    if (g.parts > 1) {
-      f32x4* to = part_at<T::BLOCKS>(g.part_sums, w.unit * g.parts + w.part);
-#pragma unroll
-      for (int n = 0; n < T::BLOCKS; ++n)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          to[(n * 4 + c) * kAttnThreads] =
-              (f32x4){dk[n][4 * c], dk[n][4 * c + 1], dk[n][4 * c + 2], dk[n][4 * c + 3]};
-          to[((T::BLOCKS + n) * 4 + c) * kAttnThreads] =
-              (f32x4){dv[n][4 * c], dv[n][4 * c + 1], dv[n][4 * c + 2], dv[n][4 * c + 3]};
-        }
+    if (g.k_parts > 1) {
+      f32x4* to = part_at(g.k_sums, w.unit * g.k_parts + w.part, 2 * T::BLOCKS * 4);
+      store_part(to, dk);
+      store_part(to + T::BLOCKS * 4 * kAttnThreads, dv);
     } else if (mine) {
       store_columns<DT>(static_cast<char*>(const_cast<void*>(g.dk.p)) + row * g.dk.row +
                             kv * g.dk.head, dk, g.scale, half, g.head_dim);
@@ -394,53 +348,43 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 ? 1 : 2) attn_dkv_ker
   }
 }
 
-// The parts' sums, added in order; a workgroup a tile of keys and head, dk or dv.
+// The parts' sums, added in order; a workgroup 32 columns of a tile of dk or dv.
 template <int DT, int D>
 __global__ void __launch_bounds__(kAttnThreads) attn_dkv_sum_kernel(AttnArgs g, int tiles) {
   constexpr int BLOCKS = D / 32;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Items items(tiles, g.kv_heads, 2);
+  const Items items(tiles, g.kv_heads, 2 * BLOCKS);
   for (int64_t item = blockIdx.x; item < items.total; item += gridDim.x) {
     const Keys w(g, items, item, tiles);
-    if (!w.any) continue;
-    f32x16 sum[BLOCKS];
-#pragma unroll
-    for (int n = 0; n < BLOCKS; ++n)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) sum[n][r] = 0.0f;
-    for (int p = 0; p < g.parts; ++p) {
-      const f32x4* from = part_at<BLOCKS>(g.part_sums, w.unit * g.parts + p) +
-                          w.part * (BLOCKS * 4 * kAttnThreads);
-#pragma unroll
-      for (int n = 0; n < BLOCKS; ++n)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const f32x4 v = from[(n * 4 + c) * kAttnThreads];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) sum[n][4 * c + r] += v[r];
-        }
-    }
     const int j = w.j0 + wave * 32 + lane % 32;
-    const AttnMatrix& to = w.part ? g.dv : g.dk;
-    if (j < w.q.lk)
-      store_columns<DT>(static_cast<char*>(const_cast<void*>(to.p)) +
-                            ((int64_t)w.q.k0 + j) * to.row + w.kv * to.head, sum,
-                        w.part ? 1.0f : g.scale, lane / 32, g.head_dim);
+    if (!w.any || j >= w.q.lk) continue;
+    f32x16 sum[1];
+    clear(sum);
+    for (int p = 0; p < g.k_parts; ++p)
+      add_part(sum, part_at(g.k_sums, w.unit * g.k_parts + p, 2 * BLOCKS * 4) +
+                        w.part * (4 * kAttnThreads), 1.0f);
+    const bool is_dv = w.part >= BLOCKS;
+    const AttnMatrix& to = is_dv ? g.dv : g.dk;
+    store_columns<DT>(static_cast<char*>(const_cast<void*>(to.p)) +
+                          ((int64_t)w.q.k0 + j) * to.row + w.kv * to.head, sum,
+                      is_dv ? 1.0f : g.scale, lane / 32, g.head_dim, w.part % BLOCKS);
   }
 }
-
-inline int64_t capped(int64_t blocks) { return blocks < kMaxBlocks ? blocks : kMaxBlocks; }
 
 template <int DT, int D, int MODE>
 lowbit_status launch_back_width(const AttnArgs& a, hipStream_t s) {
   const int qt = attn_tiles(a.q_rows, a.sequences), kt = attn_tiles(a.k_rows, a.sequences);
-  const int64_t nk = capped(Items(kt, a.kv_heads, a.parts).total);
-  const int64_t nq = capped(Items(qt, a.kv_heads, a.group).total);
+  const int64_t nk = capped(Items(kt, a.kv_heads, a.k_parts).total);
+  const int64_t nq = capped(Items(qt, a.kv_heads, a.group * a.q_parts).total);
   lowbit_status st = launch(&attn_dkv_kernel<DT, D, MODE>, nk, kAttnThreads, s, a, kt);
-  if (st == LOWBIT_OK && a.parts > 1)
-    st = launch(&attn_dkv_sum_kernel<DT, D>, capped(Items(kt, a.kv_heads, 2).total), kAttnThreads, s,
-                a, kt);
-  return st == LOWBIT_OK ? launch(&attn_dq_kernel<DT, D, MODE>, nq, kAttnThreads, s, a, qt) : st;
+  if (st == LOWBIT_OK && a.k_parts > 1)
+    st = launch(&attn_dkv_sum_kernel<DT, D>, capped(Items(kt, a.kv_heads, 2 * (D / 32)).total),
+                kAttnThreads, s, a, kt);
+  if (st == LOWBIT_OK) st = launch(&attn_dq_kernel<DT, D, MODE>, nq, kAttnThreads, s, a, qt);
+  if (st == LOWBIT_OK && a.q_parts > 1)
+    st = launch(&attn_dq_sum_kernel<DT, D>, capped(Items(qt, a.kv_heads, a.group * (D / 32)).total),
+                kAttnThreads, s, a, qt);
+  return st;
 }
 
 template <int DT, int MODE>

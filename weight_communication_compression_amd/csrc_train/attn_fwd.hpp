@@ -19,6 +19,19 @@ struct Forward {
 
 constexpr float kSlack = 5.5f;                     // e^5.5 < 2^8; in units of log2 2^5.5
 
+// out and lse of a lane's row.
+template <int DT, int BLOCKS>
+__device__ __forceinline__ void finish_rows(const AttnArgs& g, const f32x16 (&acc)[BLOCKS],
+                                            int64_t row, int head, float top, float sum, int half,
+                                            int first = 0) {
+  const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
+  store_columns<DT>(static_cast<char*>(const_cast<void*>(g.o.p)) + row * g.o.row + head * g.o.head,
+                    acc, scale, half, g.head_dim, first);
+  if (half == 0 && first == 0)
+    g.lse[(int64_t)head * g.q_rows + row] =
+        sum == 0.0f ? -INFINITY : DT == kF32 ? top + logf(sum) : (top + log2f(sum)) * kLn2;
+}
+
 template <int DT, int D, int MODE>
 __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) attn_kernel(AttnArgs g, int tiles) {
   using F = Forward<DT, D, MODE>;
@@ -40,44 +53,24 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
   down.init(lane);
   Score<DT, MODE> score(g);
 
-  const Items items(tiles, g.kv_heads, g.group);
+  const Items items(tiles, g.kv_heads, g.group * g.q_parts);
   for (int64_t item = blockIdx.x; item < items.total; item += gridDim.x) {
-    int t, kv, in;
-    items.take(item, g.kv_heads, t, kv, in);
-    if (t >= tiles) continue;
-    t = tiles - 1 - t;                             // causal: the last see most
-    const int head = kv * g.group + in;
-    const int s = find_sequence(g.q_begin, g.sequences, g.q_rows, kRowsPerTile, t);
-    const Sequence q = sequence_at(g, s);
-    const int i0 = (t - first_tile(g.q_begin, s, g.sequences, g.q_rows, kRowsPerTile)) * kRowsPerTile;
-    if (i0 >= q.lq) continue;
-    const int i = i0 + wave * 32 + col;            // the lane's query
+    const Queries w(g, items, item, tiles, g.q_parts);
+    if (!w.any) continue;
+    const Sequence& q = w.q;
+    const int kv = w.kv, head = w.head, last = w.last;
+    const int i = w.i0 + wave * 32 + col;          // the lane's query
     const int shift = q.lk - q.lq;
     const bool mine = i < q.lq;
     const int64_t row = (int64_t)q.q0 + i;
 
     u32x4 fq[T::STEPS];
-    {
-      const char* p = static_cast<const char*>(g.q.p) + row * g.q.row + head * g.q.head;
-#pragma unroll
-      for (int kk = 0; kk < T::STEPS; ++kk) {
-        const int at = kk * 32 + half * 16;
-        fq[kk] = (u32x4){0, 0, 0, 0};
-        if (mine && at < width) fq[kk] = *reinterpret_cast<const u32x4*>(p + at);
-        if (g.scale < 0.0f) fq[kk] = negated<DT>(fq[kk]);
-      }
-    }
+    load_rows(fq, g.q.p, row * g.q.row + head * g.q.head, half, width, mine);
+    if (g.scale < 0.0f) negate<DT>(fq);
     const Sight see = sight(g, q, i + shift);
-    // tiles of keys: [0, before) of the prefix, [from, to) around the positions
-    const int last = min(i0 + kRowsPerTile, q.lq) - 1;
-    const Sight lo = sight(g, q, i0 + shift), hi = sight(g, q, last + shift);
-    const int before = (q.prefix + KT - 1) / KT;
-    const int from = lo.low > 0 ? lo.low / KT : 0;
-    const int to = hi.high < 0 ? 0 : hi.high / KT + 1;
-    const int end = max(before, to);
-    auto after = [&](int t) { return t >= before && t < from ? from : t; };
+    const KeyTiles<KT> keys(g, w, g.q_parts);
     // whether all 32 queries of the wave see all of a tile
-    const int w0 = i0 + wave * 32 + shift, w1 = min(w0 + 31, last + shift);
+    const int w0 = w.i0 + wave * 32 + shift, w1 = min(w0 + 31, last + shift);
     const Sight wl = sight(g, q, w0), wh = sight(g, q, w1);
 
     const char* kp = static_cast<const char*>(g.k.p) + q.k0 * g.k.row + kv * g.k.head;
@@ -93,10 +86,7 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
     };
 
     f32x16 acc[T::BLOCKS];
-#pragma unroll
-    for (int n = 0; n < T::BLOCKS; ++n)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[n][r] = 0.0f;
+    clear(acc);
     float top = -INFINITY, sum = 0.0f;             // sum: of this half's keys
     score.head(g, head);
 
@@ -162,63 +152,74 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
       }
     };
 
-    // one tile, in lk and lv, while the next one's loads run
-    int now = after(0), next = after(now + 1);
-    auto step = [&](char* lk, char* lv, char* nk, char* nv) {
+    // tile u, in lk and lv, while the next one's loads run
+    auto step = [&](char* lk, char* lv, char* nk, char* nv, int u) {
       wait_all();
       barrier();
-      if (next < end) issue(next, nk, nv);
-      compute(lk, lv, now);
-      now = next;
-      next = after(now + 1);
+      if (u + 1 < keys.count) issue(keys.tile(u + 1), nk, nv);
+      compute(lk, lv, keys.tile(u));
     };
-    if (now < end) issue(now, lk0, lv0);
-    while (next < end) {
-      step(lk0, lv0, lk1, lv1);
-      step(lk1, lv1, lk0, lv0);
+    if (keys.count > 0) issue(keys.tile(0), lk0, lv0);
+    int u = 0;
+    for (; u + 1 < keys.count; u += 2) {
+      step(lk0, lv0, lk1, lv1, u);
+      step(lk1, lv1, lk0, lv0, u + 1);
     }
-    if (now < end) step(lk0, lv0, lk1, lv1);
+    if (u < keys.count) step(lk0, lv0, lk1, lv1, u);
     wait_all();
     barrier();                                     // (the next item writes the buffers)
 
     sum = both_halves_sum(sum);
-    if (mine) {
-      const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
-      char* o = static_cast<char*>(const_cast<void*>(g.o.p)) + row * g.o.row + head * g.o.head;
-#pragma unroll
-      for (int n = 0; n < T::BLOCKS; ++n)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int at = n * 32 + c * 8 + half * 4;
-          f32x4 v;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] = acc[n][4 * c + r] * scale;
-          if (at < g.head_dim) {
-            if constexpr (DT == kF32) *reinterpret_cast<f32x4*>(o + at * 4) = v;
-            else *reinterpret_cast<u32x2*>(o + at * 2) =
-                     (u32x2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-          }
-        }
-      if (half == 0)
-        g.lse[(int64_t)head * g.q_rows + row] =
-            sum == 0.0f ? -INFINITY : DT == kF32 ? top + logf(sum) : (top + log2f(sum)) * kLn2;
+    if (g.q_parts > 1) {
+      f32x4* to = part_at(g.q_sums, w.unit * g.q_parts + w.part, T::BLOCKS * 4 + 1);
+      store_part(to, acc);
+      to[T::BLOCKS * 4 * kAttnThreads] = (f32x4){top, sum, 0.0f, 0.0f};
+    } else if (mine) {
+      finish_rows<DT>(g, acc, row, head, top, sum, half);
     }
+  }
+}
+
+// The parts of a row's keys joined, in order; a workgroup 32 columns of a tile.
+template <int DT, int D>
+__global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(AttnArgs g, int tiles) {
+  constexpr int BLOCKS = D / 32, VECTORS = BLOCKS * 4 + 1;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Items items(tiles, g.kv_heads, g.group * BLOCKS);
+  for (int64_t item = blockIdx.x; item < items.total; item += gridDim.x) {
+    const Queries w(g, items, item, tiles, BLOCKS);
+    const int i = w.i0 + wave * 32 + lane % 32;
+    if (!w.any || i >= w.q.lq) continue;
+    const int64_t first = w.unit * g.q_parts;
+    float top = -INFINITY, sum = 0.0f;
+    for (int p = 0; p < g.q_parts; ++p)
+      top = fmaxf(top, part_at(g.q_sums, first + p, VECTORS)[(VECTORS - 1) * kAttnThreads][0]);
+    f32x16 acc[1];
+    clear(acc);
+    for (int p = 0; p < g.q_parts; ++p) {
+      const f32x4* from = part_at(g.q_sums, first + p, VECTORS);
+      const f32x4 end = from[(VECTORS - 1) * kAttnThreads];
+      // (a part in which nothing is seen has sums of 0)
+      const float weight = end[0] == -INFINITY ? 1.0f : exp_unit<DT>(end[0] - top);
+      sum = __builtin_fmaf(end[1], weight, sum);
+      add_part(acc, from + w.part * (4 * kAttnThreads), weight);
+    }
+    finish_rows<DT>(g, acc, (int64_t)w.q.q0 + i, w.head, top, sum, lane / 32, w.part);
   }
 }
 
 template <int DT, int D>
 lowbit_status launch_attn_width(const AttnArgs& a, hipStream_t s) {
   const int tiles = attn_tiles(a.q_rows, a.sequences);
-  const Items items(tiles, a.kv_heads, a.group);
-  const int64_t blocks = items.total < kMaxBlocks ? items.total : kMaxBlocks;
-  switch (score_mode(a)) {
-    case kPlainScore:
-      return launch(&attn_kernel<DT, D, kPlainScore>, blocks, kAttnThreads, s, a, tiles);
-    case kBiasScore:
-      return launch(&attn_kernel<DT, D, kBiasScore>, blocks, kAttnThreads, s, a, tiles);
-    default:
-      return launch(&attn_kernel<DT, D, kCapScore>, blocks, kAttnThreads, s, a, tiles);
-  }
+  const int64_t blocks = capped(Items(tiles, a.kv_heads, a.group * a.q_parts).total);
+  const int mode = score_mode(a);
+  const lowbit_status st =
+      mode == kPlainScore  ? launch(&attn_kernel<DT, D, kPlainScore>, blocks, kAttnThreads, s, a, tiles)
+      : mode == kBiasScore ? launch(&attn_kernel<DT, D, kBiasScore>, blocks, kAttnThreads, s, a, tiles)
+                           : launch(&attn_kernel<DT, D, kCapScore>, blocks, kAttnThreads, s, a, tiles);
+  if (st != LOWBIT_OK || a.q_parts == 1) return st;
+  return launch(&attn_join_kernel<DT, D>, capped(Items(tiles, a.kv_heads, a.group * (D / 32)).total),
+                kAttnThreads, s, a, tiles);
 }
 
 template <int DT>

@@ -42,8 +42,10 @@ struct AttnArgs {
   const float* slopes;       // may be null
   float* lse;                // q_heads x q_rows
   float* rows_info;          // gradient: q_heads x q_rows of lse, then of D
-  float* part_sums;          // gradient: dk's and dv's, where there are several parts
-  int32_t parts;
+  // where there are too few tiles for the chip: into how many parts the keys of a tile of
+  // queries are cut, and the gradient's queries of a tile of keys; and the parts' sums
+  int32_t q_parts, k_parts;
+  float *q_sums, *k_sums;
   int32_t q_rows, k_rows, sequences;
   int32_t q_heads, kv_heads, group;
   int32_t head_dim;

@@ -129,25 +129,35 @@ AttnArgs attention_args(const void* q, const void* k, const void* v, const void*
   return a;
 }
 
-// The gradient's workspace: lse and D of each query row, the parts' sums of dk and dv.
+// Parts and the workspace: the gradient's lse and D of each query row, the parts' sums.
 struct AttnPlan {
-  int parts;
-  int64_t sums, bytes;
+  int q_parts, k_parts;
+  int64_t q_sums, k_sums, bytes;
 };
 
-// The chip holds 512 workgroups of the gradient by k and v at one time.  A causal
-// sequence's take from nothing to twice the mean, so two rounds of them, the long ones
-// first, are wanted; fewer are cut into parts of at least 256 queries of all heads.
-AttnPlan attn_plan(const lowbit_attention_params* p) {
+// The chip holds 512 workgroups at one time.  Where there are fewer tiles of
+// queries, their keys are cut, down to 256 on average (64 of binary32, whose products take
+// eight times as long).  By k and v the gradient's workgroups take from nothing to twice the
+// mean of a causal sequence, so that two rounds of them are wanted, the long ones first; their
+// queries are cut, down to as many of all heads.
+AttnPlan attn_plan(const lowbit_attention_params* p, bool backward) {
   AttnPlan w{};
-  const int64_t tiles = attn_tiles(p->k_rows, p->sequences) * (int64_t)p->kv_heads;
-  const int64_t group = p->q_heads / p->kv_heads;
-  int64_t parts = tiles ? (1024 + tiles - 1) / tiles : 1;
-  parts = std::min(parts, p->sequences ? p->q_rows * group / p->sequences / 256 : 1);
-  w.parts = (int)std::max<int64_t>(1, std::min<int64_t>(parts, 16));
-  w.sums = up(p->q_rows * p->q_heads * 8, 256);
-  const int width = p->head_dim <= 64 ? 64 : p->head_dim <= 96 ? 96 : 128;
-  w.bytes = w.sums + (w.parts > 1 ? tiles * w.parts * 2 * kAttnRows * width * 4 : 0);
+  const int64_t each = std::max(p->sequences, 1), group = p->q_heads / p->kv_heads;
+  auto parts = [](int64_t wanted, int64_t tiles, int64_t most) {
+    const int64_t n = tiles ? (wanted + tiles - 1) / tiles : 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({n, most, 16}));
+  };
+  const int64_t least = p->type == LOWBIT_F32 ? 64 : 256;
+  const int64_t width = p->head_dim <= 64 ? 64 : p->head_dim <= 96 ? 96 : 128;
+  const int64_t tile = kAttnRows * width * 4;      // a tile's sums
+  const int64_t q_tiles = attn_tiles(p->q_rows, p->sequences) * (int64_t)p->q_heads;
+  const int64_t k_tiles = attn_tiles(p->k_rows, p->sequences) * (int64_t)p->kv_heads;
+  w.q_parts = q_tiles >= 512 ? 1 : parts(768, q_tiles, p->k_rows / each / least);
+  w.k_parts = backward ? parts(1024, k_tiles, p->q_rows * group / each / least) : 1;
+  w.q_sums = backward ? up(p->q_rows * p->q_heads * 8, 256) : 0;
+  // (the forward call keeps the maximum and the sum of a row beside the two halves of it)
+  w.k_sums = w.q_sums + (w.q_parts > 1 ? q_tiles * w.q_parts * (tile + (backward ? 0 : kAttnRows * 32)) : 0);
+  w.bytes = w.k_sums + (w.k_parts > 1 ? k_tiles * w.k_parts * 2 * tile : 0);
   return w;
 }
 
@@ -236,7 +246,7 @@ lowbit_status lowbit_attention(const void* q, const void* k, const void* v,
                                const int32_t* q_begin, const int32_t* k_begin,
                                const int32_t* prefix, const float* slopes,
                                const lowbit_attention_params* p, void* out, float* lse,
-                               hipStream_t stream) {
+                               void* workspace, int64_t workspace_bytes, hipStream_t stream) {
   const lowbit_status st = check_attention(p);
   if (st != LOWBIT_OK) return st;
   for (const lowbit_strides* s : {&p->q, &p->k, &p->v, &p->out})
@@ -247,12 +257,16 @@ lowbit_status lowbit_attention(const void* q, const void* k, const void* v,
   if (p->q_rows == 0 || p->sequences == 0) return LOWBIT_OK;
   if (!good(q) || (p->k_rows > 0 && (!good(k) || !good(v))) || !good(out) || !good(lse))
     return LOWBIT_EINVAL;
-  const AttnArgs a = attention_args(q, k, v, out, lse, q_begin, k_begin, prefix, slopes, p);
+  const AttnPlan plan = attn_plan(p, false);
+  if (plan.bytes > 0 && (!good(workspace) || workspace_bytes < plan.bytes)) return LOWBIT_EINVAL;
+  AttnArgs a = attention_args(q, k, v, out, lse, q_begin, k_begin, prefix, slopes, p);
+  a.q_parts = plan.q_parts;
+  a.q_sums = static_cast<float*>(workspace);
   return p->type == LOWBIT_F32 ? launch_attn_f32(a, stream) : launch_attn_bf16(a, stream);
 }
 
-int64_t lowbit_attention_backward_workspace(const lowbit_attention_params* p) {
-  return check_attention(p) == LOWBIT_OK ? attn_plan(p).bytes : -1;
+int64_t lowbit_attention_workspace(const lowbit_attention_params* p, int32_t backward) {
+  return check_attention(p) == LOWBIT_OK ? attn_plan(p, backward != 0).bytes : -1;
 }
 
 lowbit_status lowbit_attention_backward(const void* dout, const void* q, const void* k,
@@ -275,7 +289,7 @@ lowbit_status lowbit_attention_backward(const void* dout, const void* q, const v
   if (p->q_rows > 0 && (!good(q) || !good(dout) || !good(out) || !good(lse) || !good(dq)))
     return LOWBIT_EINVAL;
   if (p->k_rows > 0 && (!good(k) || !good(v) || !good(dk) || !good(dv))) return LOWBIT_EINVAL;
-  const AttnPlan plan = attn_plan(p);
+  const AttnPlan plan = attn_plan(p, true);
   if (plan.bytes > 0 && (!good(workspace) || workspace_bytes < plan.bytes)) return LOWBIT_EINVAL;
   AttnArgs a = attention_args(q, k, v, out, const_cast<float*>(lse), q_begin, k_begin, prefix,
                               slopes, p);
@@ -285,8 +299,10 @@ lowbit_status lowbit_attention_backward(const void* dout, const void* q, const v
   a.dk = matrix(dk, p->dk, es);
   a.dv = matrix(dv, p->dv, es);
   a.rows_info = static_cast<float*>(workspace);
-  a.parts = plan.parts;
-  a.part_sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.sums);
+  a.q_parts = plan.q_parts;
+  a.k_parts = plan.k_parts;
+  a.q_sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.q_sums);
+  a.k_sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.k_sums);
   if (p->q_rows > 0) {
     const lowbit_status sd = launch_attn_delta(p->type, a, stream);
     if (sd != LOWBIT_OK) return sd;

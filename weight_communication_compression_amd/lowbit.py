@@ -150,8 +150,8 @@ def lib() -> ctypes.CDLL:
             "lowbit_rotary_frequencies": (ctypes.c_int, [i32, f64, i32, f64, i64, f64, f64, P, P]),
             "lowbit_rotary": (ctypes.c_int, [P, P, P, RP, P, P]),
             "lowbit_rotary_backward": (ctypes.c_int, [P, P, P, RP, P, P]),
-            "lowbit_attention": (ctypes.c_int, [P] * 7 + [AP] + [P] * 3),
-            "lowbit_attention_backward_workspace": (i64, [AP]),
+            "lowbit_attention_workspace": (i64, [AP, i32]),
+            "lowbit_attention": (ctypes.c_int, [P] * 7 + [AP] + [P] * 3 + [i64, P]),
             "lowbit_attention_backward": (ctypes.c_int, [P] * 10 + [AP] + [P] * 4 + [i64, P]),
             "lowbit_orthogonalize_workspace": (i64, [OP]),
             "lowbit_orthogonalize": (ctypes.c_int, [P, OP, P, P, i64, P]),
@@ -946,6 +946,18 @@ def _attention_params(q, k, v, q_begin, k_begin, scale, causal, window, prefix, 
     return p
 
 
+def _attention_scratch(L, p, backward, like, workspace, what):
+    """The workspace's pointer (torch frees the tensor for work that comes after the call's on
+    its stream) and size."""
+    nbytes = L.lowbit_attention_workspace(p, backward)
+    if nbytes < 0 and p.head_dim % 8 == 0 and p.head_dim > 128:
+        raise LowbitError(EUNSUPPORTED, f"{what}: head_dim above 128")
+    if nbytes == 0 and workspace is None:
+        return None, 0
+    ws = _scratch(nbytes, like, workspace, what)
+    return _dev(ws, "workspace"), ws.numel()
+
+
 def _attention_out(t, like, what):
     if t is None:
         return torch.empty(like.shape, dtype=like.dtype, device=like.device)
@@ -958,8 +970,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
               q_begin: Optional[torch.Tensor] = None, k_begin: Optional[torch.Tensor] = None,
               scale: Optional[float] = None, causal: bool = True, window: int = 0,
               prefix: Optional[torch.Tensor] = None, softcap: float = 0.0,
-              slopes: Optional[torch.Tensor] = None,
-              out: Optional[torch.Tensor] = None) -> Attention:
+              slopes: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+              workspace: Optional[torch.Tensor] = None) -> Attention:
     """Softmax attention within each sequence of packed rows.
 
     q (rows, heads, head_dim), k and v (key rows, key-value heads, head_dim), float32 or
@@ -979,10 +991,13 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     out = _attention_out(out, q, "out")
     p.out = _heads(out, "out")[1]
     lse = torch.empty(p.q_heads, p.q_rows, dtype=torch.float32, device=q.device)
-    _check(lib().lowbit_attention(_gpu(q, "q"), _gpu(k, "k"), _gpu(v, "v"),
-                                  _opt(q_begin, "q_begin"), _opt(k_begin, "k_begin"),
-                                  _opt(prefix, "prefix"), _opt(slopes, "slopes"), p,
-                                  _gpu(out, "out"), lse.data_ptr(), _stream(q)), "lowbit_attention")
+    L = lib()
+    ws, nbytes = _attention_scratch(L, p, 0, q, workspace, "attention")
+    _check(L.lowbit_attention(_gpu(q, "q"), _gpu(k, "k"), _gpu(v, "v"),
+                              _opt(q_begin, "q_begin"), _opt(k_begin, "k_begin"),
+                              _opt(prefix, "prefix"), _opt(slopes, "slopes"), p,
+                              _gpu(out, "out"), lse.data_ptr(), ws, nbytes, _stream(q)),
+           "lowbit_attention")
     return Attention(out, lse)
 
 
@@ -1007,15 +1022,12 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     for name, t in (("out", out), ("dout", dout), ("dq", dq), ("dk", dk), ("dv", dv)):
         setattr(p, name, _heads(t, name)[1])
     L = lib()
-    nbytes = L.lowbit_attention_backward_workspace(p)
-    if nbytes < 0 and p.head_dim % 8 == 0 and p.head_dim > 128:
-        raise LowbitError(EUNSUPPORTED, "attention_backward: head_dim above 128")
-    ws = _scratch(nbytes, q, workspace, "attention_backward")
+    ws, nbytes = _attention_scratch(L, p, 1, q, workspace, "attention_backward")
     _check(L.lowbit_attention_backward(
         _gpu(dout, "dout"), _gpu(q, "q"), _gpu(k, "k"), _gpu(v, "v"), _gpu(out, "out"),
         _dev(lse, "lse"), _opt(q_begin, "q_begin"), _opt(k_begin, "k_begin"),
         _opt(prefix, "prefix"), _opt(slopes, "slopes"), p, _gpu(dq, "dq"), _gpu(dk, "dk"),
-        _gpu(dv, "dv"), _dev(ws, "workspace"), ws.numel(), _stream(q)), "lowbit_attention_backward")
+        _gpu(dv, "dv"), ws, nbytes, _stream(q)), "lowbit_attention_backward")
     return AttentionGrads(dq, dk, dv)
 
 
