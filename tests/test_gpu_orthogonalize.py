@@ -65,6 +65,23 @@ def test_large():
     check(matrix(1300, 500, 6))
 
 
+@pytest.mark.parametrize("batch,rows,cols", [
+    (1, 100, 5000), (1, 200, 9000), (3, 70, 3000), (1, 4100, 64), (2, 640, 640), (1, 1500, 1300),
+    (1, 2100, 2000), (40, 130, 140)])
+def test_every_form(batch, rows, cols):
+    """Sizes that take each form of the products, some cut along k; against the form in 64 bits on
+    the GPU (the same bound as above)."""
+    g = matrix(rows, cols, batch + rows, batch=(batch,)).cuda()
+    got = L.orthogonalize(g).double()
+    for i in {0, batch - 1}:
+        x = g[i].double()
+        want = R.newton_schulz(x, 5, ABC, 1e-7, 1.0)
+        same = R.newton_schulz(x, 5, ABC, 1e-7, 1.0, R.to_f16)
+        bound = 2 * torch.linalg.vector_norm(same - want) + \
+            (2 ** -20 + half_step(torch.bfloat16)) * torch.linalg.vector_norm(want)
+        assert torch.linalg.vector_norm(got[i] - want) <= bound
+
+
 def test_singular_values():
     s = torch.linalg.svdvals(L.orthogonalize(matrix(256, 512, 7).cuda()).float())
     assert s.max() < 1.25 and s.min() > 0.6

@@ -72,6 +72,8 @@ struct OrthoArgs {
   float* x;                  // batch x m x ldn
   void *xh, *xh_next;        // X in binary16, times kOrthoX
   void *ah, *bh;             // A and b A + c A A in binary16, times kOrthoA and kOrthoB
+  float* partial;            // sums of parts of tiles that are cut along k
+  int32_t k_parts;           // of the product that is launched
   int64_t batch;
   int32_t m, n, ldm, ldn;
   int32_t turned, nparts;

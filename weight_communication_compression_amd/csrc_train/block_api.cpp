@@ -9,6 +9,7 @@
 #include <stdint.h>
 
 #include "block.hpp"
+#include "ortho_choice.hpp"
 
 namespace lowbit {
 
@@ -171,7 +172,7 @@ bool check_ortho(const lowbit_orthogonalize_params* p) {
 }
 
 struct OrthoPlan {
-  int64_t parts, x, xh, xh_next, ah, bh, bytes;
+  int64_t parts, x, xh, xh_next, ah, bh, partial, bytes;
   int m, n, ldm, ldn;
 };
 
@@ -193,6 +194,9 @@ OrthoPlan ortho_plan(const lowbit_orthogonalize_params* p) {
   w.xh_next = take(rows * w.ldn * 2);
   w.ah = take(rows * w.ldm * 2);
   w.bh = take(rows * w.ldm * 2);
+  w.partial = take(std::max({ortho_part_bytes(ortho_choice(true, true, p->batch, w.m, w.n)),
+                             ortho_part_bytes(ortho_choice(true, false, p->batch, w.m, w.n)),
+                             ortho_part_bytes(ortho_choice(false, false, p->batch, w.m, w.n))}));
   return w;
 }
 
@@ -331,6 +335,7 @@ lowbit_status lowbit_orthogonalize(const void* g, const lowbit_orthogonalize_par
   a.xh_next = at + w.xh_next;
   a.ah = at + w.ah;
   a.bh = at + w.bh;
+  a.partial = reinterpret_cast<float*>(at + w.partial);
   a.batch = p->batch;
   a.m = w.m;
   a.n = w.n;

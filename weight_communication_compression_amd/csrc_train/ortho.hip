@@ -1,5 +1,6 @@
 // ortho.hip -- orthogonalize: Newton-Schulz products.
 #include "block.hpp"
+#include "ortho_choice.hpp"
 #include "tile_feed.hpp"
 #include "train_device.hpp"
 #include "../csrc/launch.hpp"
@@ -130,116 +131,254 @@ enum OrthoKind : int {
   kGram = 0,                 // A = X X^T
   kPoly = 1,                 // B = b A + c A A
   kUpdate = 2,               // X = a X + B X
+  kLast = 3,                 // the same, and out = scale X, turned back, in its place
 };
 
-// What becomes of four consecutive columns of a row.
+// Tiles of A and B lie on and below the diagonal; the others are their mirror images.
 template <int KIND>
-__device__ __forceinline__ void emit(const OrthoArgs& g, int64_t matrix, int row, int col, f32x4 v) {
-  if (row >= g.m) return;
-  if constexpr (KIND == kUpdate) {
-    if (col >= g.ldn) return;
-    const int64_t at = (matrix * g.m + row) * g.ldn + col;
-    const f32x4 x = *reinterpret_cast<const f32x4*>(g.x + at);
-    f32x4 y;
+constexpr bool kMirrored = KIND == kGram || KIND == kPoly;
+
+// Where a tile lies.  Tiles are counted in bands of 8 rows of tiles (4 of a mirrored product),
+// down a band's columns: the 32 that an XCD's CUs hold at one time then share the panels that
+// they read through its L2.
+struct Place {
+  int tm, tn;
+};
+template <int KIND>
+__device__ __forceinline__ Place place(int tile, int across, int down) {
+  if constexpr (kMirrored<KIND>) {
+    // band b begins at tile b (8 b + 2): rows 0 .. 4 b - 1 have 1, 2, ... tiles
+    int b = (int)(sqrtf((float)tile * 0.125f));
+    while ((b + 1) * (8 * (b + 1) + 2) <= tile) ++b;
+    while (b * (8 * b + 2) > tile) --b;
+    const int high = min(4, down - 4 * b), whole = 4 * b + 1;
+    int in = tile - b * (8 * b + 2);
+    if (in < high * whole) return {4 * b + in % high, in / high};
+    in -= high * whole;                            // beyond the band's first diagonal tile
+    int j = 1;
+    while (in >= high - j) in -= high - j++;
+    return {4 * b + j + in, 4 * b + j};
+  } else {
+    const int band = tile / (8 * across), in = tile % (8 * across), high = min(8, down - band * 8);
+    return {band * 8 + in % high, in / high};
+  }
+}
+
+// Four columns col .. col + 3 of a row of the result, from the products' sums.
+template <int KIND>
+__device__ __forceinline__ f32x4 value(const OrthoArgs& g, int64_t matrix, int row, int col, f32x4 v) {
+  if constexpr (KIND == kGram) {
+    return v * (kA / (kX * kX));
+  } else if constexpr (KIND == kPoly) {
+    f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (row >= g.m || col >= g.ldm) return y;
+    const f32x4 a = unpack_f16(*reinterpret_cast<const u32x2*>(
+        static_cast<_Float16*>(g.ah) + (matrix * g.m + row) * g.ldm + col));
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      y[r] = __builtin_fmaf(g.b * (kB / kA), a[r], v[r] * (g.c * (kB / (kA * kA))));
+    return y;
+  } else {
+    f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (row >= g.m || col >= g.ldn) return y;
+    const f32x4 x = *reinterpret_cast<const f32x4*>(g.x + (matrix * g.m + row) * g.ldn + col);
 #pragma unroll
     for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(g.a, x[r], v[r] * (1.0f / (kB * kX)));
+    return y;
+  }
+}
+
+// n (at most 4) consecutive values as bfloat16.
+__device__ __forceinline__ void put_bf16(uint16_t* p, f32x4 v, int n) {
+  const uint32_t lo = pack_bf16(v[0], v[1]), hi = pack_bf16(v[2], v[3]);
+  if (n >= 4) {
+    *reinterpret_cast<u32x2_2*>(p) = (u32x2_2){lo, hi};
+  } else {
+    if (n > 0) p[0] = (uint16_t)lo;
+    if (n > 1) p[1] = (uint16_t)(lo >> 16);
+    if (n > 2) p[2] = (uint16_t)hi;
+  }
+}
+
+template <int KIND>
+__device__ __forceinline__ void put(const OrthoArgs& g, int64_t matrix, int row, int col, f32x4 y) {
+  if (row >= g.m) return;
+  if constexpr (KIND == kLast) {
+    if (col < g.n)
+      put_bf16(static_cast<uint16_t*>(g.out) + (matrix * g.m + row) * g.n + col, y * g.scale, g.n - col);
+  } else if constexpr (KIND == kUpdate) {
+    if (col >= g.ldn) return;
+    const int64_t at = (matrix * g.m + row) * g.ldn + col;
     *reinterpret_cast<f32x4*>(g.x + at) = y;
     *reinterpret_cast<u32x2*>(static_cast<_Float16*>(g.xh_next) + at) = pack_f16(y * kX);
   } else {
     if (col >= g.ldm) return;
-    const int64_t at = (matrix * g.m + row) * g.ldm + col;
-    if constexpr (KIND == kGram) {
-      *reinterpret_cast<u32x2*>(static_cast<_Float16*>(g.ah) + at) = pack_f16(v * (kA / (kX * kX)));
-    } else {
-      const f32x4 a = unpack_f16(*reinterpret_cast<const u32x2*>(static_cast<_Float16*>(g.ah) + at));
-      f32x4 y;
+    *reinterpret_cast<u32x2*>(static_cast<_Float16*>(KIND == kGram ? g.ah : g.bh) +
+                              (matrix * g.m + row) * g.ldm + col) = pack_f16(y);
+  }
+}
+
+// 32 x 32 sums, as the lanes hold them, become results: through LDS (4 KB of the wave's own), so
+// that loads and stores take whole lines of a row, and once more, turned, for a mirror image or a
+// result that is turned back.
+template <int KIND>
+__device__ __forceinline__ void finish_block(const OrthoArgs& g, int64_t matrix, const f32x16& acc,
+                                             int row0, int col0, bool mirror, int lane, char* lds) {
+  const int r = lane % 32, h = lane / 32, line = lane / 8, piece = lane % 8;
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        y[r] = __builtin_fmaf(g.b * (kB / kA), a[r], v[r] * (g.c * (kB / (kA * kA))));
-      *reinterpret_cast<u32x2*>(static_cast<_Float16*>(g.bh) + at) = pack_f16(y);
+  for (int q = 0; q < 4; ++q)
+    *reinterpret_cast<f32x4*>(lds + r * 128 + ((2 * q + h) ^ (r & 7)) * 16) = quad(acc, q);
+  f32x4 y[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int row = k * 8 + line;
+    y[k] = *reinterpret_cast<const f32x4*>(lds + row * 128 + (piece ^ (row & 7)) * 16);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    y[k] = value<KIND>(g, matrix, row0 + k * 8 + line, col0 + piece * 4, y[k]);
+  if (KIND != kLast || !g.turned) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) put<KIND>(g, matrix, row0 + k * 8 + line, col0 + piece * 4, y[k]);
+  }
+  if constexpr (kMirrored<KIND> || KIND == kLast) {
+    if (!mirror) return;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = piece * 4 + e, row = k * 8 + line;
+        *reinterpret_cast<float*>(lds + c * 128 + ((row / 4) ^ (c >> 2 & 7)) * 16 + row % 4 * 4) = y[k][e];
+      }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = k * 8 + line;
+      const f32x4 v = *reinterpret_cast<const f32x4*>(lds + c * 128 + (piece ^ (c >> 2 & 7)) * 16);
+      if constexpr (KIND == kLast) {
+        const int row = row0 + piece * 4;          // of X; a column of the result
+        if (col0 + c < g.n && row < g.m)
+          put_bf16(static_cast<uint16_t*>(g.out) + (matrix * g.n + col0 + c) * g.m + row, v * g.scale,
+                   g.m - row);
+      } else {
+        put<KIND>(g, matrix, col0 + c, row0 + piece * 4, v);
+      }
     }
   }
 }
 
+// Where the sums of a part of a tile are, as the lanes hold them.
+template <class F>
+__device__ __forceinline__ f32x4* part_of(float* partial, int64_t part) {
+  return reinterpret_cast<f32x4*>(partial) + part * (F::TM * F::TN / 4) + threadIdx.x;
+}
+
+// A form of the tile kernel: TM x TN by W = WM x WN waves, STAGES steps of k in LDS, PER_CU
+// workgroups on a CU.
+template <int TM_, int TN_, int WM_, int WN_, int STAGES_, int PER_CU_>
+struct Shape {
+  static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, STAGES = STAGES_, PER_CU = PER_CU_;
+  static constexpr int W = WM * WN, I = TM / WM / 32, J = TN / WN / 32, THREADS = 64 * W;
+  static constexpr int A = TM * kRowBytes, STAGE = (TM + TN) * kRowBytes;
+};
+
+// All loads but the last N are done, and all that the wave has read in LDS.
+template <int N>
+__device__ __forceinline__ void wait_loads_but() {
+  if constexpr (N == 0) wait_loads();
+  else {
+    static_assert(N < 64, "");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 7 << 4 | 0 << 8);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// W waves, each I x J products of 32 x 32; lanes hold of one what finish_block says.  STAGES
+// buffers in LDS: while the matrix units work on one, the others are filled, so that a step's
+// loads have STAGES - 1 steps' time.
 template <class F, int KIND>
-__global__ void __launch_bounds__(F::THREADS, F::SLOTS * F::W / 1024) ortho_tile_kernel(OrthoArgs g) {
-  constexpr int DT = F::DT, TM = F::TM, TN = F::TN, W = F::W, I = F::I, J = F::J;
-  constexpr bool BO = KIND == kUpdate;
+__global__ void __launch_bounds__(F::THREADS, F::PER_CU * F::W / 4) ortho_tile_kernel(OrthoArgs g) {
+  constexpr int TM = F::TM, TN = F::TN, W = F::W, I = F::I, J = F::J, S = F::STAGES;
+  constexpr bool BO = !kMirrored<KIND>;
   constexpr int K = kRowBytes / 2;
-  __shared__ __attribute__((aligned(1024))) char la0[TM * kRowBytes];
-  __shared__ __attribute__((aligned(1024))) char lb0[TN * kRowBytes];
-  __shared__ __attribute__((aligned(1024))) char la1[TM * kRowBytes];
-  __shared__ __attribute__((aligned(1024))) char lb1[TN * kRowBytes];
+  constexpr bool OWN_SIDE = F::STAGE < W * 4096;
+  __shared__ __attribute__((aligned(1024))) char l0[F::STAGE];
+  __shared__ __attribute__((aligned(1024))) char l1[F::STAGE];
+  __shared__ __attribute__((aligned(1024))) char l2[S > 2 ? F::STAGE : 16];
+  __shared__ __attribute__((aligned(1024))) char l3[S > 3 ? F::STAGE : 16];
+  __shared__ __attribute__((aligned(1024))) char own_side[OWN_SIDE ? W * 4096 : 16];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / F::WN, wn = wave % F::WN;
-  const int k = KIND == kGram ? g.n : g.m, n = KIND == kUpdate ? g.n : g.m;
+  char* const side = (OWN_SIDE ? own_side : l0) + wave * 4096;
+  const int k = KIND == kGram ? g.n : g.m, n = kMirrored<KIND> ? g.m : g.n;
   const int lda = KIND == kGram ? g.ldn : g.ldm, ldb = KIND == kPoly ? g.ldm : g.ldn;
   const int across = (n + TN - 1) / TN, down = (g.m + TM - 1) / TM;
-  const int64_t tiles = (int64_t)across * down;
-  const int steps = (k + K - 1) / K;
+  const int64_t tiles = kMirrored<KIND> ? (int64_t)down * (down + 1) / 2 : (int64_t)across * down;
+  const int all_steps = (k + K - 1) / K;
 
-  constexpr int NA = Feed<DT, TM, W, false>::LOADS, NB = Feed<DT, TN, W, BO>::LOADS, N = NA + NB;
+  constexpr int NA = Feed<kF16, TM, W, false>::LOADS, NB = Feed<kF16, TN, W, BO>::LOADS, N = NA + NB;
   constexpr int RD = I + J * (BO ? 2 : 1);
-  Feed<DT, TM, W, false> fa;
-  Feed<DT, TN, W, BO> fb;
-  Frag<DT, TM, false> ra;
-  Frag<DT, TN, BO> rb;
+  Feed<kF16, TM, W, false> fa;
+  Feed<kF16, TN, W, BO> fb;
+  Frag<kF16, TM, false> ra;
+  Frag<kF16, TN, BO> rb;
   fa.init(lda, wave, lane);
   fb.init(ldb, wave, lane);
   ra.init(wm * (TM / F::WM), lane);
   rb.init(wn * (TN / F::WN), lane);
   u32x4 fra[2][I], frb[2][J];
   f32x16 acc[I][J];
+  int s0, s1;                                      // steps of this unit
 
   auto kleft = [&](int s) { return min(k - s * K, K); };
-  auto issue = [&](char* la, char* lb, int s) {
-    const auto qa = fa.open(s < steps), qb = fb.open(s < steps);
+  auto issue = [&](char* l, int s) {
+    const auto qa = fa.open(s < s1), qb = fb.open(s < s1);
 #pragma unroll
-    for (int j = 0; j < NA; ++j) fa.load(qa, la, wave, kleft(s), j);
+    for (int j = 0; j < NA; ++j) fa.load(qa, l, wave, kleft(s), j);
 #pragma unroll
-    for (int j = 0; j < NB; ++j) fb.load(qb, lb, wave, kleft(s), j);
+    for (int j = 0; j < NB; ++j) fb.load(qb, l + F::A, wave, kleft(s), j);
     fa.next();
     fb.next();
   };
-  auto read = [&](int to, const char* la, const char* lb, int kk) {
+  auto read = [&](int to, const char* l, int kk) {
 #pragma unroll
-    for (int j = 0; j < J; ++j) frb[to][j] = rb.load(lb, j, kk);
+    for (int j = 0; j < J; ++j) frb[to][j] = rb.load(l + F::A, j, kk);
 #pragma unroll
-    for (int i = 0; i < I; ++i) fra[to][i] = ra.load(la, i, kk);
+    for (int i = 0; i < I; ++i) fra[to][i] = ra.load(l, i, kk);
   };
   auto mul = [&](int f) {
 #pragma unroll
     for (int i = 0; i < I; ++i)
 #pragma unroll
-      for (int j = 0; j < J; ++j) acc[i][j] = mma<DT>(frb[f][j], fra[f][i], acc[i][j]);
+      for (int j = 0; j < J; ++j) acc[i][j] = mma<kF16>(frb[f][j], fra[f][i], acc[i][j]);
     spread_reads<RD, I * J>();
     __builtin_amdgcn_sched_barrier(0);
   };
-  // Step s, in la and lb, whose first quarter is in registers.  While a quarter is
-  // multiplied the next is read; before the last, everybody has read all of
-  // this step, the next one has arrived, and the loads of the one after it begin.
-  auto step = [&](char* la, char* lb, const char* na, const char* nb, int s) {
-    const auto qa = fa.open(s + 2 < steps), qb = fb.open(s + 2 < steps);
-    const int kl = kleft(s + 2);
-    read(1, la, lb, 1);
+  // Step s, in l, whose first quarter is in registers.  While a quarter is multiplied the next
+  // is read; before the last, everybody has read all of this step, the next one has arrived (in
+  // `next`), and the loads of step s + STAGES begin.
+  auto step = [&](char* l, const char* next, int s) {
+    const auto qa = fa.open(s + S < s1), qb = fb.open(s + S < s1);
+    const int kl = kleft(s + S);
+    read(1, l, 1);
     mul(0);
-    read(0, la, lb, 2);
+    read(0, l, 2);
     mul(1);
-    read(1, la, lb, 3);
+    read(1, l, 3);
     mul(0);
-    wait_loads();
+    wait_loads_but<(S - 2) * N>();
     barrier();
-    read(0, na, nb, 0);
+    read(0, next, 0);
 #pragma unroll
     for (int i = 0; i < I; ++i)
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        acc[i][j] = mma<DT>(frb[1][j], fra[1][i], acc[i][j]);
+        acc[i][j] = mma<kF16>(frb[1][j], fra[1][i], acc[i][j]);
         const int p = i * J + j;
 #pragma unroll
         for (int u = N * p / (I * J); u < N * (p + 1) / (I * J); ++u) {
-          if (u < NA) fa.load(qa, la, wave, kl, u);
-          else fb.load(qb, lb, wave, kl, u - NA);
+          if (u < NA) fa.load(qa, l, wave, kl, u);
+          else fb.load(qb, l + F::A, wave, kl, u - NA);
         }
       }
     fa.next();
@@ -248,56 +387,140 @@ __global__ void __launch_bounds__(F::THREADS, F::SLOTS * F::W / 1024) ortho_tile
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  for (int64_t unit = blockIdx.x; unit < tiles * g.batch; unit += gridDim.x) {
-    const int64_t matrix = unit / tiles;
-    const int in = (int)(unit - matrix * tiles);
-    const int tm = in / across, tn = in % across;
+  const int64_t total = tiles * g.batch * g.k_parts;
+  for (int64_t unit = blockIdx.x; unit < total; unit += gridDim.x) {
+    // unit u is a workgroup's of XCD u mod 8, of which each takes a contiguous run
+    const int64_t x = unit % 8, each = total / 8, more = total % 8;
+    const int64_t mine = x * each + (x < more ? x : more) + unit / 8;
+    const int64_t which = mine / g.k_parts;
+    const int part = (int)(mine - which * g.k_parts);
+    const int64_t matrix = which / tiles;
+    const Place at = place<KIND>((int)(which - matrix * tiles), across, down);
+    const int tm = __builtin_amdgcn_readfirstlane(at.tm), tn = __builtin_amdgcn_readfirstlane(at.tn);
+    s0 = __builtin_amdgcn_readfirstlane((int)((int64_t)all_steps * part / g.k_parts));
+    s1 = __builtin_amdgcn_readfirstlane((int)((int64_t)all_steps * (part + 1) / g.k_parts));
     const int64_t mm = matrix * g.m;
     const _Float16* a = static_cast<const _Float16*>(KIND == kGram ? g.xh : KIND == kPoly ? g.ah : g.bh);
     const _Float16* b = static_cast<const _Float16*>(KIND == kPoly ? g.ah : g.xh);
-    fa.seek(a + mm * lda, lda, g.m, (int64_t)tm * TM, 0);
-    fb.seek(b + mm * ldb, ldb, g.m, (int64_t)tn * TN, 0);
-    issue(la0, lb0, 0);
-    issue(la1, lb1, 1);
+    fa.seek(a + mm * lda, lda, g.m, (int64_t)tm * TM, (int64_t)s0 * K);
+    fb.seek(b + mm * ldb, ldb, g.m, (int64_t)tn * TN, (int64_t)s0 * K);
+    issue(l0, s0);
+    issue(l1, s0 + 1);
+    if constexpr (S > 2) issue(l2, s0 + 2);
+    if constexpr (S > 3) issue(l3, s0 + 3);
 #pragma unroll
     for (int i = 0; i < I; ++i)
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-    wait_loads();
+    wait_loads_but<(S - 1) * N>();
     barrier();
-    read(0, la0, lb0, 0);
+    read(0, l0, 0);
     __builtin_amdgcn_sched_barrier(0);
-    int s = 0;
-    for (; s + 1 < steps; s += 2) {
-      step(la0, lb0, la1, lb1, s);
-      step(la1, lb1, la0, lb0, s + 1);
+    int s = s0;
+    for (; s + S <= s1; s += S) {
+      step(l0, l1, s);
+      if constexpr (S == 2) {
+        step(l1, l0, s + 1);
+      } else if constexpr (S == 3) {
+        step(l1, l2, s + 1);
+        step(l2, l0, s + 2);
+      } else {
+        step(l1, l2, s + 1);
+        step(l2, l3, s + 2);
+        step(l3, l0, s + 3);
+      }
     }
-    if (s < steps) step(la0, lb0, la1, lb1, s);
+    if (s < s1) step(l0, l1, s);
+    if constexpr (S > 2) {
+      if (s + 1 < s1) step(l1, l2, s + 1);
+    }
+    if constexpr (S > 3) {
+      if (s + 2 < s1) step(l2, l3, s + 2);
+    }
     wait_loads();
-    barrier();
-    const int row = tm * TM + wm * (TM / F::WM) + lane % 32;
-    const int col = tn * TN + wn * (TN / F::WN) + lane / 32 * 4;
+    barrier();                                     // (nobody reads the buffers any more)
+    if (g.k_parts > 1) {
+      f32x4* const to = part_of<F>(g.partial, which * g.k_parts + part);
 #pragma unroll
-    for (int i = 0; i < I; ++i)
+      for (int i = 0; i < I; ++i)
 #pragma unroll
-      for (int j = 0; j < J; ++j)
+        for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          emit<KIND>(g, matrix, row + 32 * i, col + 32 * j + 8 * q, quad(acc[i][j], q));
+          for (int q = 0; q < 4; ++q) to[((i * J + j) * 4 + q) * F::THREADS] = quad(acc[i][j], q);
+    } else {
+      const bool mirror = KIND == kLast ? g.turned != 0 : tm != tn;
+#pragma unroll
+      for (int i = 0; i < I; ++i)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          finish_block<KIND>(g, matrix, acc[i][j], tm * TM + wm * (TM / F::WM) + 32 * i,
+                             tn * TN + wn * (TN / F::WN) + 32 * j, mirror, lane, side);
+    }
+    __syncthreads();                               // (the next tile's loads go where the waves wrote)
   }
 }
 
+// The parts' sums of a tile that is cut along k, added in order.
+template <class F, int KIND>
+__global__ void __launch_bounds__(F::THREADS) ortho_add_kernel(OrthoArgs g) {
+  constexpr int I = F::I, J = F::J;
+  __shared__ __attribute__((aligned(1024))) char side[F::W * 4096];
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = kMirrored<KIND> ? g.m : g.n;
+  const int across = (n + F::TN - 1) / F::TN, down = (g.m + F::TM - 1) / F::TM;
+  const int64_t tiles = kMirrored<KIND> ? (int64_t)down * (down + 1) / 2 : (int64_t)across * down;
+  // a workgroup takes one 32 x 32 block of each wave
+  for (int64_t unit = blockIdx.x; unit < tiles * g.batch * (I * J); unit += gridDim.x) {
+    const int64_t which = unit / (I * J);
+    const int block = (int)(unit - which * (I * J)), i = block / J, j = block % J;
+    const int64_t matrix = which / tiles;
+    const Place at = place<KIND>((int)(which - matrix * tiles), across, down);
+    f32x16 acc;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
+    for (int p = 0; p < g.k_parts; ++p) {
+      const f32x4* const from = part_of<F>(g.partial, which * g.k_parts + p) + block * 4 * F::THREADS;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 v = from[q * F::THREADS];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[4 * q + r] += v[r];
+      }
+    }
+    finish_block<KIND>(g, matrix, acc, at.tm * F::TM + wave / F::WN * (F::TM / F::WM) + 32 * i,
+                       at.tn * F::TN + wave % F::WN * (F::TN / F::WN) + 32 * j,
+                       KIND == kLast ? g.turned != 0 : at.tm != at.tn, lane, side + wave * 4096);
+  }
+}
+
+template <class F, int KIND>
+lowbit_status launch_form(const OrthoArgs& g, hipStream_t s) {
+  const int64_t down = (g.m + F::TM - 1) / F::TM, across = (g.n + F::TN - 1) / F::TN;
+  const int64_t tiles = g.batch * (kMirrored<KIND> ? down * (down + 1) / 2 : down * across);
+  if (g.k_parts > 1 && !g.partial) return LOWBIT_EINVAL;
+  const lowbit_status st = launch(&ortho_tile_kernel<F, KIND>,
+                                  std::min<int64_t>(tiles * g.k_parts, 1 << 20), F::THREADS, s, g);
+  if (st != LOWBIT_OK || g.k_parts == 1) return st;
+  return launch(&ortho_add_kernel<F, KIND>, std::min<int64_t>(tiles * F::I * F::J, 1 << 20),
+                F::THREADS, s, g);
+}
+
 template <int KIND>
-lowbit_status launch_product(const OrthoArgs& g, hipStream_t s) {
-  const int n = KIND == kUpdate ? g.n : g.m;
-  auto tiles = [&](int t) { return g.batch * ((g.m + t - 1) / t) * ((n + t - 1) / t); };
-  if (tiles(256) >= 256)
-    return launch(&ortho_tile_kernel<Form<kF16, 256, 256, 2, 4, 256>, KIND>,
-                  std::min<int64_t>(tiles(256), 1 << 20), 512, s, g);
-  return launch(&ortho_tile_kernel<Form<kF16, 128, 128, 2, 2, 512>, KIND>,
-                std::min<int64_t>(tiles(128), 1 << 20), 256, s, g);
+lowbit_status launch_product(const OrthoArgs& args, hipStream_t s) {
+  OrthoArgs g = args;
+  const OrthoChoice c = ortho_choice(kMirrored<KIND>, KIND == kGram, g.batch, g.m, g.n);
+  g.k_parts = c.parts;
+  switch (c.form) {
+    case 0: return launch_form<Shape<256, 256, 2, 4, 2, 1>, KIND>(g, s);
+    case 1:
+      if constexpr (kMirrored<KIND>) return launch_form<Shape<192, 192, 2, 2, 2, 1>, KIND>(g, s);
+      return LOWBIT_EINVAL;                        // (not among the other products' forms)
+    case 2: return launch_form<Shape<128, 128, 2, 2, 2, 2>, KIND>(g, s);
+    case 3: return launch_form<Shape<128, 128, 2, 4, 4, 1>, KIND>(g, s);
+    default: return launch_form<Shape<64, 64, 2, 2, 4, 2>, KIND>(g, s);
+  }
 }
 
 }  // namespace
@@ -316,10 +539,11 @@ lowbit_status launch_ortho(int dt, const OrthoArgs& args, int steps, hipStream_t
   for (int k = 0; k < steps && st == LOWBIT_OK; ++k) {
     st = launch_product<kGram>(g, s);
     if (st == LOWBIT_OK) st = launch_product<kPoly>(g, s);
-    if (st == LOWBIT_OK) st = launch_product<kUpdate>(g, s);
+    if (st == LOWBIT_OK)
+      st = k + 1 < steps ? launch_product<kUpdate>(g, s) : launch_product<kLast>(g, s);
     std::swap(g.xh, g.xh_next);
   }
-  return st == LOWBIT_OK ? launch(&ortho_end_kernel, blocks, 256, s, g) : st;
+  return st == LOWBIT_OK && steps == 0 ? launch(&ortho_end_kernel, blocks, 256, s, g) : st;
 }
 
 }  // namespace lowbit

@@ -1,0 +1,68 @@
+// ortho_choice.hpp -- which form of the tile kernel a product of orthogonalize takes, and
+// whether it is cut along k.  Integer and float arithmetic with no HIP dependency, for the
+// launches, the workspace and a CPU test.
+#pragma once
+
+#include <stdint.h>
+
+namespace lowbit {
+
+// The forms: rows and columns of a tile; microseconds of a step of 64 of k where a CU has one
+// tile (all CUs busy), of a step of one tile where it has several, and of a launch with its
+// ends.  Measured at 10 sizes from 256 x 1024 to 2048 x 8192.
+struct OrthoForm {
+  int tile;
+  float lone, shared, base;
+};
+constexpr int kOrthoForms = 5;
+constexpr OrthoForm kOrthoForm[kOrthoForms] = {
+    {256, 1.60f, 1.60f, 9.0f},   // eight waves, two stages
+    {192, 1.15f, 1.20f, 7.0f},   // four waves of 96 x 96; only of mirrored products
+    {128, 0.85f, 0.60f, 6.0f},   // four waves, two stages, two workgroups a CU
+    {128, 0.67f, 0.75f, 6.0f},   // eight waves, four stages
+    {64, 0.27f, 0.25f, 4.5f},    // four waves, four stages, two workgroups a CU
+};
+
+struct OrthoChoice {
+  int form, parts;
+  int64_t tiles;
+};
+
+inline float ortho_cost(int form, int parts, int64_t tiles, int64_t steps) {
+  const OrthoForm& f = kOrthoForm[form];
+  const int64_t each = (tiles * parts + 255) / 256, run = (steps + parts - 1) / parts;
+  const float step = each > 1 ? each * f.shared > f.lone ? each * f.shared : f.lone : f.lone;
+  const float add = parts > 1 ? 6.0f + (float)tiles * parts * f.tile * f.tile * 8.0f / 4.0e6f : 0.0f;
+  return f.base + run * step + add;
+}
+
+// The cheapest form for a product with m rows: of A A^T kinds (mirrored, of their tiles only
+// those on and below the diagonal) with k = n (gram) or m, else m x n with k = m.
+inline OrthoChoice ortho_choice(bool mirrored, bool gram, int64_t batch, int64_t m, int64_t n) {
+  const int64_t steps = ((gram ? n : m) + 63) / 64;
+  OrthoChoice best{-1, 1, 0};
+  float least = 0.0f;
+  for (int f = 0; f < kOrthoForms; ++f) {
+    if (f == 1 && !mirrored) continue;
+    const int64_t t = kOrthoForm[f].tile, down = (m + t - 1) / t;
+    const int64_t tiles = batch * (mirrored ? down * (down + 1) / 2 : down * ((n + t - 1) / t));
+    for (int parts = 1; parts <= 16; parts *= 2) {
+      // (a part has 8 steps at least, and never more parts than there are CUs)
+      if (parts > 1 && (steps / parts < 8 || tiles * parts > 256)) break;
+      const float cost = ortho_cost(f, parts, tiles, steps);
+      if (best.form < 0 || cost < least) {
+        best = {f, parts, tiles};
+        least = cost;
+      }
+    }
+  }
+  return best;
+}
+
+// Bytes for the parts' sums of a product.
+inline int64_t ortho_part_bytes(const OrthoChoice& c) {
+  const int64_t t = kOrthoForm[c.form].tile;
+  return c.parts > 1 ? c.tiles * c.parts * t * t * 4 : 0;
+}
+
+}  // namespace lowbit
