@@ -62,20 +62,35 @@ __device__ __forceinline__ void wait_all() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// Order for the compiler: N times M matrix instructions, whose operands take R reads of
-// LDS; the reads run AHEAD times ahead.  (Left alone it takes all reads first, for
-// which the registers do not suffice.)
-template <int N, int R, int M, int AHEAD, int I = 0>
-__device__ __forceinline__ void reads_ahead() {
-  if constexpr (I == 0) __builtin_amdgcn_sched_group_barrier(0x100, R * (AHEAD < N ? AHEAD : N), 0);
-  if constexpr (I < N) {
-    __builtin_amdgcn_sched_group_barrier(0x008, M, 0);
-    if constexpr (I + AHEAD < N) __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
-    reads_ahead<N, R, M, AHEAD, I + 1>();
-  } else {
+// N products whose operands come from LDS: load(i) reads the i-th's, use(i, operands)
+// multiplies.  The reads run A products ahead, in this order: left alone, the compiler reads
+// each operand right before its product and waits for it.
+template <int A, class Load>
+__device__ __forceinline__ auto read_first(Load load) {
+  struct Ahead {
+    decltype(load(0)) f[A];
+  } r;
+#pragma unroll
+  for (int i = 0; i < A; ++i) r.f[i] = load(i);
+  __builtin_amdgcn_sched_barrier(0);
+  return r;
+}
+template <int N, int A, class Ahead, class Load, class Use>
+__device__ __forceinline__ void products(Ahead& r, Load load, Use use) {
+  static_assert(A <= N, "");
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    use(i, r.f[i % A]);
+    if (i + A < N) r.f[i % A] = load(i + A);
     __builtin_amdgcn_sched_barrier(0);
   }
 }
+struct Two {
+  u32x4 a, b;
+};
+struct Three {
+  u32x4 a, b, c;
+};
 
 // d[row of first][column of second] += sum over 32 bytes of k.  Lane l gives row (column)
 // l mod 32 and the (l / 32)-th 16 bytes, and holds of the result column l mod 32
@@ -172,6 +187,8 @@ struct Tile {
   // Operands along a row: row b * 32 + lane mod 32, step kk.
   struct Along {
     uint32_t at;
+    // makes the compiler take the addresses anew instead of keeping all of them in registers
+    __device__ __forceinline__ void refresh() { asm volatile("" : "+v"(at)); }
     __device__ __forceinline__ void init(int lane) {
       const int r = lane % 32;
       at = r * PITCH + ((lane / 32) ^ mix(r)) * 16;
@@ -187,6 +204,7 @@ struct Tile {
   // Operands down a column: column i * 32 + lane mod 32, rows of chunk c.
   struct Down {
     uint32_t at;
+    __device__ __forceinline__ void refresh() { asm volatile("" : "+v"(at)); }
     __device__ __forceinline__ void init(int lane) {
       const int h = lane / 32;
       if constexpr (DT == kF32) {
@@ -276,6 +294,12 @@ struct Score {
     return exp_unit<DT>(MODE == kPlainScore ? __builtin_fmaf(y, factor, -base) : y - base);
   }
 };
+
+// The gradient's sums of products may begin with -lse / factor and -D, so that both are
+// subtracted for nothing.  Not of capped scores, whose lse is no sum's; nor of binary32,
+// whose scores would lose digits beside a large lse.
+template <int DT, int MODE>
+constexpr bool lse_in_sum() { return DT == kBF16 && MODE != kCapScore; }
 
 // The signs of an operand's elements turned.
 template <int DT>

@@ -47,11 +47,11 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
     load_rows(fq, g.q.p, row * g.q.row + head * g.q.head, half, width, mine);
     load_rows(fdo, g.dout.p, row * g.dout.row + head * g.dout.head, half, width, mine);
     if (g.scale < 0.0f) negate<DT>(fq);
-    float lse = 0.0f, delta = 0.0f;
+    float lse = 0.0f, minus_d = 0.0f;
     if (mine) {
       const float* info = g.rows_info + (int64_t)head * g.q_rows + row;
       lse = info[0];
-      delta = info[(int64_t)g.q_heads * g.q_rows];
+      minus_d = info[(int64_t)g.q_heads * g.q_rows];
     }
     const Sight see = sight(g, q, i + shift);
     const KeyTiles<KT> keys(g, w, g.q_parts);
@@ -60,8 +60,9 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
 
     const char* kp = static_cast<const char*>(g.k.p) + q.k0 * g.k.row + kv * g.k.head;
     const char* vp = static_cast<const char*>(g.v.p) + q.k0 * g.v.row + kv * g.v.head;
-    auto issue = [&](int t, char* lk, char* lv) {
-      const int rows = q.lk - t * KT;
+    // (no rows where there is no such tile: a branch would make the compiler wait for the loads)
+    auto issue = [&](int t, char* lk, char* lv, bool any) {
+      const int rows = any ? q.lk - t * KT : 0;
       const auto rk = load_k.rows_at(kp + (int64_t)t * KT * g.k.row, (int)g.k.row, width, rows);
       const auto rv = load_v.rows_at(vp + (int64_t)t * KT * g.v.row, (int)g.v.row, width, rows);
 #pragma unroll
@@ -79,32 +80,47 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
       const float distance = (float)(i + shift - j0 - 4 * half);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
+        along.refresh();
+        down.refresh();
         f32x16 x, dp;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) x[r] = dp[r] = 0.0f;
-#pragma unroll
-        for (int kk = 0; kk < T::STEPS; ++kk) {
-          x = mma<DT>(along.load(lk, b, kk), fq[kk], x);
-          dp = mma<DT>(along.load(lv, b, kk), fdo[kk], dp);
+        for (int r = 0; r < 16; ++r) {
+          x[r] = lse_in_sum<DT, MODE>() ? lse : 0.0f;
+          dp[r] = minus_d;
         }
+        auto rows = [&](int kk) { return Two{along.load(lk, b, kk), along.load(lv, b, kk)}; };
+        auto ahead = read_first<3>(rows);
+        products<T::STEPS, 3>(ahead, rows, [&](int kk, const Two& f) {
+          x = mma<DT>(f.a, fq[kk], x);
+          dp = mma<DT>(f.b, fdo[kk], dp);
+        });
+        auto key = [&](int i) { return down.load(lk, i % T::BLOCKS, b * chunks<DT>() + i / T::BLOCKS); };
+        auto keys_ahead = read_first<4>(key);
         const int base = j0 + 32 * b + 4 * half;
         const int low = see.low - base, high = see.high - base, pre = see.prefix - base;
+        auto seen = [&](int r) {
+          const int j = r / 4 * 8 + r % 4;
+          return (j < pre) | ((j >= low) & (j <= high));
+        };
+        // (a capped -infinity would be finite: there the weight is cleared)
+        if (MODE != kCapScore && !whole) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) x[r] = seen(r) ? x[r] : -INFINITY;
+        }
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const int j = r / 4 * 8 + r % 4;
           float bend;
-          const float y = score.at(x[r], distance, 32 * b + j, bend);
-          float p = score.weight(y, lse) * (dp[r] - delta) * bend;
-          if (!whole && !(j < pre || (j >= low && j <= high))) p = 0.0f;
-          x[r] = p;
+          const float y = score.at(x[r], distance, 32 * b + r / 4 * 8 + r % 4, bend);
+          float p = score.weight(y, lse_in_sum<DT, MODE>() ? 0.0f : lse);
+          if (MODE == kCapScore) p = whole | seen(r) ? p : 0.0f;
+          x[r] = p * dp[r] * bend;
         }
+        u32x4 p[chunks<DT>()];
 #pragma unroll
-        for (int c = 0; c < chunks<DT>(); ++c) {
-          const u32x4 p = pack_chunk<DT>(x, c);
-#pragma unroll
-          for (int n = 0; n < T::BLOCKS; ++n)
-            acc[n] = mma<DT>(down.load(lk, n, b * chunks<DT>() + c), p, acc[n]);
-        }
+        for (int c = 0; c < chunks<DT>(); ++c) p[c] = pack_chunk<DT>(x, c);
+        products<chunks<DT>() * T::BLOCKS, 4>(keys_ahead, key, [&](int i, const u32x4& f) {
+          acc[i % T::BLOCKS] = mma<DT>(f, p[i / T::BLOCKS], acc[i % T::BLOCKS]);
+        });
       }
     };
 
@@ -112,10 +128,10 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
     auto step = [&](char* lk, char* lv, char* nk, char* nv, int u) {
       wait_all();
       barrier();
-      if (u + 1 < keys.count) issue(keys.tile(u + 1), nk, nv);
+      issue(keys.tile(u + 1), nk, nv, u + 1 < keys.count);
       compute(lk, lv, keys.tile(u));
     };
-    if (keys.count > 0) issue(keys.tile(0), lk0, lv0);
+    issue(keys.tile(0), lk0, lv0, keys.count > 0);
     int u = 0;
     for (; u + 1 < keys.count; u += 2) {
       step(lk0, lv0, lk1, lv1, u);
@@ -183,15 +199,14 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 ? 1 : 2) attn_dkv_ker
   constexpr bool KEEP = D <= (DT == kF32 ? 96 : 64);
   constexpr int QT = DT == kF32 || !KEEP ? 32 : 64, NB = QT / 32, ES = elem_size<DT>();
   using T = Tile<DT, D, QT>;
-  constexpr int INSTR = DT == kF32 ? 4 : 1;        // matrix instructions of a product
   using V = Tile<DT, D, 32>;                       // a wave's values
   __shared__ __attribute__((aligned(1024))) char lvalues[KEEP ? 16 : kWaves * V::BYTES];
   __shared__ __attribute__((aligned(1024))) char lq0[T::BYTES];
   __shared__ __attribute__((aligned(1024))) char ld0[T::BYTES];
   __shared__ __attribute__((aligned(1024))) char lq1[T::BYTES];
   __shared__ __attribute__((aligned(1024))) char ld1[T::BYTES];
-  __shared__ __attribute__((aligned(1024))) char li0[512];   // lse, D of 64 queries
-  __shared__ __attribute__((aligned(1024))) char li1[512];
+  __shared__ __attribute__((aligned(1024))) char li0[1024];  // lse, -D of 64 queries, twice
+  __shared__ __attribute__((aligned(1024))) char li1[1024];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane % 32, half = lane / 32;
   const int width = g.head_dim * ES;
@@ -250,9 +265,10 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 ? 1 : 2) attn_dkv_ker
     clear(dk);
     clear(dv);
 
-    auto issue = [&](char* lq, char* ld, char* li) {
+    // (no rows where there is no next tile: a branch would make the compiler wait for the loads)
+    auto issue = [&](char* lq, char* ld, char* li, bool any) {
       const int head = kv * g.group + in;
-      const int rows = q.lq - t * QT;
+      const int rows = any ? q.lq - t * QT : 0;
       const int64_t at = (int64_t)q.q0 + t * QT;
       const auto rq = load_q.rows_at(static_cast<const char*>(g.q.p) + at * g.q.row + head * g.q.head,
                                      (int)g.q.row, width, rows);
@@ -262,11 +278,10 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 ? 1 : 2) attn_dkv_ker
       for (int j = 0; j < T::LOADS; ++j) load_q.load(rq, lq, wave, j);
 #pragma unroll
       for (int j = 0; j < T::LOADS; ++j) load_d.load(rd, ld, wave, j);
-      if (wave < 2) {                              // lse, or D
-        const auto r = open(g.rows_info + ((int64_t)wave * g.q_heads + head) * g.q_rows + at,
-                            max(0, min(rows, 64)) * 4);
-        load_floats(r, li + wave * 256, lane);
-      }
+      // lse (even waves) and -D (odd ones), each twice
+      const auto r = open(g.rows_info + ((int64_t)(wave % 2) * g.q_heads + head) * g.q_rows + at,
+                          max(0, min(rows, 64)) * 4);
+      load_floats(r, li + wave * 256, lane);
     };
     auto compute = [&](const char* lq, const char* ld, const char* li, int t) {
       const int i0 = t * QT;
@@ -274,44 +289,72 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 ? 1 : 2) attn_dkv_ker
       const float distance = (float)(i0 + 4 * half + shift - j);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
+        along.refresh();
+        down.refresh();
+        // a lane's sixteen queries: 4 consecutive ones, four times
+        auto info = [&](int which, int c) {
+          return *reinterpret_cast<const f32x4*>(li + which * 256 + (32 * b + 8 * c + 4 * half) * 4);
+        };
         f32x16 x, dp;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) x[r] = dp[r] = 0.0f;
-#pragma unroll
-        for (int kk = 0; kk < T::STEPS; ++kk) {
-          x = mma<DT>(along.load(lq, b, kk), fk[kk], x);
-          dp = mma<DT>(along.load(ld, b, kk), KEEP ? fv[kk] : along.load(lv, 0, kk), dp);
-        }
-        reads_ahead<T::STEPS, KEEP ? 2 : 3, 2 * INSTR, 2>();
-        const int base = i0 + 32 * b + 4 * half;
-#pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const f32x4 lse = *reinterpret_cast<const f32x4*>(li + (32 * b + 8 * c + 4 * half) * 4);
-          const f32x4 delta =
-              *reinterpret_cast<const f32x4*>(li + 256 + (32 * b + 8 * c + 4 * half) * 4);
+          const f32x4 minus_d = info(1, c);
+          const f32x4 lse = lse_in_sum<DT, MODE>() ? info(0, c) : (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int r = 4 * c + e, i = base + 8 * c + e;
+            x[4 * c + e] = lse[e];
+            dp[4 * c + e] = minus_d[e];
+          }
+        }
+        auto rows = [&](int kk) {
+          return Three{along.load(lq, b, kk), along.load(ld, b, kk),
+                       KEEP ? fv[kk] : along.load(lv, 0, kk)};
+        };
+        auto ahead = read_first<2>(rows);
+        products<T::STEPS, 2>(ahead, rows, [&](int kk, const Three& f) {
+          x = mma<DT>(f.a, fk[kk], x);
+          dp = mma<DT>(f.b, f.c, dp);
+        });
+        auto columns = [&](int i) {
+          const int n = i % T::BLOCKS, c = b * chunks<DT>() + i / T::BLOCKS;
+          return Two{down.load(ld, n, c), down.load(lq, n, c)};
+        };
+        auto columns_ahead = read_first<2>(columns);
+        const int base = i0 + 32 * b + 4 * half;
+        const int from = low - base, to = high - base;
+        auto seen = [&](int r) {
+          const int i = r / 4 * 8 + r % 4;
+          return (i >= from) & (i <= to);
+        };
+        if (MODE != kCapScore && !whole) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) x[r] = seen(r) ? x[r] : -INFINITY;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const f32x4 lse = lse_in_sum<DT, MODE>() ? (f32x4){0.0f, 0.0f, 0.0f, 0.0f} : info(0, c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = 4 * c + e;
             float bend;
             const float y = score.at(x[r], distance, -(32 * b + 8 * c + e), bend);
             float p = score.weight(y, lse[e]);
-            float d = p * (dp[r] - delta[e]) * bend;
-            if (!whole && !(i >= low && i <= high)) p = d = 0.0f;
+            if (MODE == kCapScore) p = whole | seen(r) ? p : 0.0f;
             x[r] = p;
-            dp[r] = d;
+            dp[r] = p * dp[r] * bend;
           }
         }
-        __builtin_amdgcn_sched_barrier(0);
+        u32x4 p[chunks<DT>()], d[chunks<DT>()];
 #pragma unroll
         for (int c = 0; c < chunks<DT>(); ++c) {
-          const u32x4 p = pack_chunk<DT>(x, c), d = pack_chunk<DT>(dp, c);
-#pragma unroll
-          for (int n = 0; n < T::BLOCKS; ++n) {
-            dv[n] = mma<DT>(down.load(ld, n, b * chunks<DT>() + c), p, dv[n]);
-            dk[n] = mma<DT>(down.load(lq, n, b * chunks<DT>() + c), d, dk[n]);
-          }
+          p[c] = pack_chunk<DT>(x, c);
+          d[c] = pack_chunk<DT>(dp, c);
         }
-        reads_ahead<chunks<DT>() * T::BLOCKS, DT == kF32 ? 8 : 4, 2 * INSTR, 2>();
+        products<chunks<DT>() * T::BLOCKS, 2>(columns_ahead, columns, [&](int i, const Two& f) {
+          const int n = i % T::BLOCKS, c = i / T::BLOCKS;
+          dv[n] = mma<DT>(f.a, p[c], dv[n]);
+          dk[n] = mma<DT>(f.b, d[c], dk[n]);
+        });
       }
     };
     // one step: the tile in lq .. li, while the next one's loads run
@@ -324,10 +367,10 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 ? 1 : 2) attn_dkv_ker
         t = from;
         ++in;
       }
-      if (more) issue(nq, nd, ni);
+      issue(nq, nd, ni, more);
       compute(lq, ld, li, now);
     };
-    if (left > 0) issue(lq0, ld0, li0);
+    issue(lq0, ld0, li0, left > 0);
     for (; left > 1; left -= 2) {
       step(lq0, ld0, li0, lq1, ld1, li1, true);
       step(lq1, ld1, li1, lq0, ld0, li0, left > 2);

@@ -6,7 +6,7 @@ namespace lowbit {
 namespace {
 
 // lse in the kernels' units (0 where a row sees nothing: every weight is exp(-infinity)
-// then) and D, the sum of dout out: 16 lanes a row of a head, all heads of a row in turn.
+// then) and -D, D being the sum of dout out: 16 lanes a row of a head, all heads of a row in turn.
 template <int DT>
 __global__ void __launch_bounds__(256) attn_delta_kernel(AttnArgs g) {
   const int lane = threadIdx.x % 16;
@@ -27,8 +27,11 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(AttnArgs g) {
     if (lane == 0) {
       const int64_t at = (int64_t)head * g.q_rows + row;
       const float lse = g.lse[at];
-      g.rows_info[at] = lse == -INFINITY ? 0.0f : lse * unit_of<DT>();
-      g.rows_info[pairs + at] = sum;
+      // as the gradient's kernels take it (lse_in_sum)
+      float own = lse == -INFINITY ? 0.0f : lse * unit_of<DT>();
+      if (DT == kBF16 && !(g.softcap > 0.0f)) own = -own / Score<DT, kPlainScore>(g).factor;
+      g.rows_info[at] = own;
+      g.rows_info[pairs + at] = -sum;
     }
   }
 }

@@ -75,8 +75,9 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
 
     const char* kp = static_cast<const char*>(g.k.p) + q.k0 * g.k.row + kv * g.k.head;
     const char* vp = static_cast<const char*>(g.v.p) + q.k0 * g.v.row + kv * g.v.head;
-    auto issue = [&](int t, char* lk, char* lv) {
-      const int rows = q.lk - t * KT;
+    // (no rows where there is no such tile: a branch would make the compiler wait for the loads)
+    auto issue = [&](int t, char* lk, char* lv, bool any) {
+      const int rows = any ? q.lk - t * KT : 0;
       const auto rk = load_k.rows_at(kp + (int64_t)t * KT * g.k.row, (int)g.k.row, width, rows);
       const auto rv = load_v.rows_at(vp + (int64_t)t * KT * g.v.row, (int)g.v.row, width, rows);
 #pragma unroll
@@ -91,37 +92,45 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
     score.head(g, head);
 
     auto compute = [&](const char* lk, const char* lv, int t) {
+      along.refresh();
+      down.refresh();
       f32x16 x[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) x[b][r] = 0.0f;
-#pragma unroll
-        for (int kk = 0; kk < T::STEPS; ++kk) x[b] = mma<DT>(along.load(lk, b, kk), fq[kk], x[b]);
-      }
+      clear(x);
+      auto key = [&](int i) { return along.load(lk, i % NB, i / NB); };
+      auto ahead = read_first<6>(key);
+      products<NB * T::STEPS, 6>(ahead, key, [&](int i, const u32x4& f) {
+        x[i % NB] = mma<DT>(f, fq[i / NB], x[i % NB]);
+      });
+      // product i: block b of keys, chunk c, columns n
+      auto val = [&](int i) { return down.load(lv, i % T::BLOCKS, i / T::BLOCKS); };
+      auto values = read_first<4>(val);
+
       const int j0 = t * KT;
       const bool whole = (j0 + KT <= see.prefix) || (j0 >= wh.low && j0 + KT - 1 <= wl.high);
       const float distance = (float)(i + shift - j0 - 4 * half);
       float most = -INFINITY;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           float bend;
           x[b][r] = score.at(x[b][r], distance, 32 * b + r / 4 * 8 + r % 4, bend);
         }
-        if (!whole) {
-          const int base = j0 + 32 * b + 4 * half;
-          const int low = see.low - base, high = see.high - base, pre = see.prefix - base;
+      if (!whole) {
+        const int base = j0 + 4 * half;
+        const int low = see.low - base, high = see.high - base, pre = see.prefix - base;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
-            const int j = r / 4 * 8 + r % 4;
-            if (!(j < pre || (j >= low && j <= high))) x[b][r] = -INFINITY;
+            const int j = 32 * b + r / 4 * 8 + r % 4;
+            x[b][r] = (j < pre) | ((j >= low) & (j <= high)) ? x[b][r] : -INFINITY;
           }
-        }
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int r = 0; r < 16; ++r) most = fmaxf(most, x[b][r]);
-      }
       most = score.scaled(other_half_max(most));
       // the sums stand relative to `top`, which follows the largest score only when it is
       // passed by more than kSlack: weights then are up to 2^8, which loses nothing, and
@@ -135,6 +144,7 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
         for (int n = 0; n < T::BLOCKS; ++n) acc[n] *= shrink;
       }
       const float base = top == -INFINITY ? 0.0f : top;
+      u32x4 p[NB * chunks<DT>()];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
 #pragma unroll
@@ -143,23 +153,21 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
           sum += x[b][r];
         }
 #pragma unroll
-        for (int c = 0; c < chunks<DT>(); ++c) {
-          const u32x4 p = pack_chunk<DT>(x[b], c);
-#pragma unroll
-          for (int n = 0; n < T::BLOCKS; ++n)
-            acc[n] = mma<DT>(down.load(lv, n, b * chunks<DT>() + c), p, acc[n]);
-        }
+        for (int c = 0; c < chunks<DT>(); ++c) p[b * chunks<DT>() + c] = pack_chunk<DT>(x[b], c);
       }
+      products<NB * chunks<DT>() * T::BLOCKS, 4>(values, val, [&](int i, const u32x4& f) {
+        acc[i % T::BLOCKS] = mma<DT>(f, p[i / T::BLOCKS], acc[i % T::BLOCKS]);
+      });
     };
 
     // tile u, in lk and lv, while the next one's loads run
     auto step = [&](char* lk, char* lv, char* nk, char* nv, int u) {
       wait_all();
       barrier();
-      if (u + 1 < keys.count) issue(keys.tile(u + 1), nk, nv);
+      issue(keys.tile(u + 1), nk, nv, u + 1 < keys.count);
       compute(lk, lv, keys.tile(u));
     };
-    if (keys.count > 0) issue(keys.tile(0), lk0, lv0);
+    issue(keys.tile(0), lk0, lv0, keys.count > 0);
     int u = 0;
     for (; u + 1 < keys.count; u += 2) {
       step(lk0, lv0, lk1, lv1, u);
