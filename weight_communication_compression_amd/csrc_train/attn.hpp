@@ -78,12 +78,15 @@ __device__ __forceinline__ auto read_first(Load load) {
 template <int N, int A, class Ahead, class Load, class Use>
 __device__ __forceinline__ void products(Ahead& r, Load load, Use use) {
   static_assert(A <= N, "");
+  // (before the other wave's exps: 2 to 4 % of the whole)
+  __builtin_amdgcn_s_setprio(1);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     use(i, r.f[i % A]);
     if (i + A < N) r.f[i % A] = load(i + A);
     __builtin_amdgcn_sched_barrier(0);
   }
+  __builtin_amdgcn_s_setprio(0);
 }
 struct Two {
   u32x4 a, b;
@@ -237,16 +240,19 @@ struct Tile {
   };
 };
 
-// Which scores a kernel is built for: plain ones, ones with a distance bias, or capped
-// ones (with a bias, which may be 0).
-enum ScoreMode : int { kPlainScore = 0, kBiasScore = 1, kCapScore = 2 };
+// Which scores a kernel is built for: plain ones, ones with a distance bias, capped ones, both.
+enum ScoreMode : int { kPlainScore = 0, kBiasScore = 1, kCapScore = 2, kCapBiasScore = 3 };
 inline int score_mode(const AttnArgs& a) {
-  return a.softcap > 0.0f ? kCapScore : a.slopes ? kBiasScore : kPlainScore;
+  return a.softcap > 0.0f ? a.slopes ? kCapBiasScore : kCapScore
+                          : a.slopes ? kBiasScore : kPlainScore;
 }
+constexpr bool has_cap(int mode) { return mode >= kCapScore; }
+constexpr bool has_bias(int mode) { return mode % 2 == 1; }
 
-// What a score is from the products' sum.  Plain ones stay unscaled until their exp, whose
-// argument then is one fused product and sum; a negative scale is turned into the sign of
-// the operand that is held in registers.
+// What a score is from the products' sum.  Without a bias it grows with the sum, so that a
+// row's largest score is that of its largest sum, and the others are taken only within their
+// exp, whose argument then is one fused product and sum.  A negative scale is turned
+// into the sign of the operand that is held in registers.
 template <int DT, int MODE>
 struct Score {
   float factor, cap, slope;
@@ -254,44 +260,55 @@ struct Score {
     const float unit = unit_of<DT>(), scale = fabsf(g.scale);
     cap = g.softcap * unit;
     // (a scale of 0 as 2^-100: -infinity times it has to stay what it is)
-    factor = MODE != kCapScore ? fmaxf(scale * unit, 0x1p-100f)
-             : DT == kF32      ? scale / g.softcap
-                               : scale / g.softcap * (2.0f * kLog2e);
+    factor = !has_cap(MODE) ? fmaxf(scale * unit, 0x1p-100f)
+             : DT == kF32   ? scale / g.softcap
+                            : scale / g.softcap * (2.0f * kLog2e);
     slope = 0.0f;
   }
   __device__ __forceinline__ void head(const AttnArgs& g, int h) {
-    if (MODE != kPlainScore && g.slopes) slope = g.slopes[h] * unit_of<DT>();
+    if (has_bias(MODE)) slope = g.slopes[h] * unit_of<DT>();
   }
-  // x: a sum of products; distance: |distance - c| to the key.  bend: what the gradient is
-  // multiplied by, 1 - tanh^2
+  // (1 - tanh) / 2 of the capped sum: 1 / (exp(2 x) + 1), off by 2^-24 or so, well below what
+  // bfloat16 weights are rounded to
+  __device__ __forceinline__ float below(float x) const {
+    if constexpr (DT == kF32) return 0.5f - 0.5f * tanhf(x * factor);
+    else return __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * factor) + 1.0f);
+  }
+  // the gradient's factor 1 - tanh^2
+  static __device__ __forceinline__ float bend_of(float r) { return 4.0f * __builtin_fmaf(-r, r, r); }
+
+  // x: a sum of products; distance: |distance - c| to the key
   __device__ __forceinline__ float at(float x, float distance, int c, float& bend) const {
     bend = 1.0f;
-    if constexpr (MODE == kPlainScore) return x;
-    float y;
-    if constexpr (MODE == kCapScore) {
-      if constexpr (DT == kF32) {
-        const float t = tanhf(x * factor);
-        bend = __builtin_fmaf(-t, t, 1.0f);
-        y = cap * t;
-      } else {
-        // t = 1 - 2 / (exp(2 x) + 1), off by 2^-23, well below what the weights are rounded to
-        const float r = __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * factor) + 1.0f);
-        const float t = __builtin_fmaf(-2.0f, r, 1.0f);
-        bend = __builtin_fmaf(-t, t, 1.0f);
-        y = cap * t;
-      }
+    if constexpr (!has_bias(MODE)) {
+      return x;
     } else {
-      y = x * factor;
+      float y = x * factor;
+      if constexpr (has_cap(MODE)) {
+        const float r = below(x);
+        bend = bend_of(r);
+        y = __builtin_fmaf(-2.0f * cap, r, cap);
+      }
+      return __builtin_fmaf(-slope, fabsf(distance - (float)c), y);
     }
-    return __builtin_fmaf(-slope, fabsf(distance - (float)c), y);
   }
-  // of a largest score, in units
+  // the largest score, in units, from the largest of what `at` gives
   __device__ __forceinline__ float scaled(float y) const {
-    return MODE == kPlainScore ? y * factor : y;
+    if (MODE == kPlainScore) return y * factor;
+    if (MODE == kCapScore) return y == -INFINITY ? y : __builtin_fmaf(-2.0f * cap, below(y), cap);
+    return y;
   }
-  // exp(y - base)
-  __device__ __forceinline__ float weight(float y, float base) const {
-    return exp_unit<DT>(MODE == kPlainScore ? __builtin_fmaf(y, factor, -base) : y - base);
+  // exp(score - base); of a masked -infinity 0, but where MODE is kCapScore
+  __device__ __forceinline__ float weight(float y, float base, float& bend) const {
+    if constexpr (MODE == kPlainScore) {
+      return exp_unit<DT>(__builtin_fmaf(y, factor, -base));
+    } else if constexpr (MODE == kCapScore) {
+      const float r = below(y);
+      bend = bend_of(r);
+      return exp_unit<DT>(__builtin_fmaf(-2.0f * cap, r, cap - base));
+    } else {
+      return exp_unit<DT>(y - base);
+    }
   }
 };
 
@@ -299,7 +316,7 @@ struct Score {
 // subtracted for nothing.  Not of capped scores, whose lse is no sum's; nor of binary32,
 // whose scores would lose digits beside a large lse.
 template <int DT, int MODE>
-constexpr bool lse_in_sum() { return DT == kBF16 && MODE != kCapScore; }
+constexpr bool lse_in_sum() { return DT == kBF16 && !has_cap(MODE); }
 
 // The signs of an operand's elements turned.
 template <int DT>

@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
           return (j < pre) | ((j >= low) & (j <= high));
         };
         // (a capped -infinity would be finite: there the weight is cleared)
-        if (MODE != kCapScore && !whole) {
+        if (!has_cap(MODE) && !whole) {
 #pragma unroll
           for (int r = 0; r < 16; ++r) x[r] = seen(r) ? x[r] : -INFINITY;
         }
@@ -111,8 +111,8 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
         for (int r = 0; r < 16; ++r) {
           float bend;
           const float y = score.at(x[r], distance, 32 * b + r / 4 * 8 + r % 4, bend);
-          float p = score.weight(y, lse_in_sum<DT, MODE>() ? 0.0f : lse);
-          if (MODE == kCapScore) p = whole | seen(r) ? p : 0.0f;
+          float p = score.weight(y, lse_in_sum<DT, MODE>() ? 0.0f : lse, bend);
+          if (has_cap(MODE)) p = whole | seen(r) ? p : 0.0f;
           x[r] = p * dp[r] * bend;
         }
         u32x4 p[chunks<DT>()];
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 ? 1 : 2) attn_dkv_ker
           const int i = r / 4 * 8 + r % 4;
           return (i >= from) & (i <= to);
         };
-        if (MODE != kCapScore && !whole) {
+        if (!has_cap(MODE) && !whole) {
 #pragma unroll
           for (int r = 0; r < 16; ++r) x[r] = seen(r) ? x[r] : -INFINITY;
         }
@@ -338,8 +338,8 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 ? 1 : 2) attn_dkv_ker
             const int r = 4 * c + e;
             float bend;
             const float y = score.at(x[r], distance, -(32 * b + 8 * c + e), bend);
-            float p = score.weight(y, lse[e]);
-            if (MODE == kCapScore) p = whole | seen(r) ? p : 0.0f;
+            float p = score.weight(y, lse[e], bend);
+            if (has_cap(MODE)) p = whole | seen(r) ? p : 0.0f;
             x[r] = p;
             dp[r] = p * dp[r] * bend;
           }
@@ -442,7 +442,8 @@ lowbit_status launch_attn_back(const AttnArgs& a, hipStream_t s) {
   switch (score_mode(a)) {
     case kPlainScore: return launch_back_mode<DT, kPlainScore>(a, s);
     case kBiasScore: return launch_back_mode<DT, kBiasScore>(a, s);
-    default: return launch_back_mode<DT, kCapScore>(a, s);
+    case kCapScore: return launch_back_mode<DT, kCapScore>(a, s);
+    default: return launch_back_mode<DT, kCapBiasScore>(a, s);
   }
 }
 

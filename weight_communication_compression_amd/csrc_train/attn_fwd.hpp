@@ -91,7 +91,8 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
     float top = -INFINITY, sum = 0.0f;             // sum: of this half's keys
     score.head(g, head);
 
-    auto compute = [&](const char* lk, const char* lv, int t) {
+    auto compute = [&](const char* lk, const char* lv, int t, auto whole_tile) {
+      const bool whole = whole_tile;
       along.refresh();
       down.refresh();
       f32x16 x[NB];
@@ -106,7 +107,6 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
       auto values = read_first<4>(val);
 
       const int j0 = t * KT;
-      const bool whole = (j0 + KT <= see.prefix) || (j0 >= wh.low && j0 + KT - 1 <= wl.high);
       const float distance = (float)(i + shift - j0 - 4 * half);
       float most = -INFINITY;
 #pragma unroll
@@ -116,16 +116,15 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
           float bend;
           x[b][r] = score.at(x[b][r], distance, 32 * b + r / 4 * 8 + r % 4, bend);
         }
+      const int base_key = j0 + 4 * half;
+      const int low = see.low - base_key, high = see.high - base_key, pre = see.prefix - base_key;
+      auto seen = [&](int j) { return (j < pre) | ((j >= low) & (j <= high)); };
       if (!whole) {
-        const int base = j0 + 4 * half;
-        const int low = see.low - base, high = see.high - base, pre = see.prefix - base;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int j = 32 * b + r / 4 * 8 + r % 4;
-            x[b][r] = (j < pre) | ((j >= low) & (j <= high)) ? x[b][r] : -INFINITY;
-          }
+          for (int r = 0; r < 16; ++r)
+            x[b][r] = seen(32 * b + r / 4 * 8 + r % 4) ? x[b][r] : -INFINITY;
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b)
@@ -149,9 +148,15 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
       for (int b = 0; b < NB; ++b) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          x[b][r] = score.weight(x[b][r], base);
-          sum += x[b][r];
+          float bend;
+          x[b][r] = score.weight(x[b][r], base, bend);
         }
+        if (MODE == kCapScore && !whole) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) x[b][r] = seen(32 * b + r / 4 * 8 + r % 4) ? x[b][r] : 0.0f;
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sum += x[b][r];
 #pragma unroll
         for (int c = 0; c < chunks<DT>(); ++c) p[b * chunks<DT>() + c] = pack_chunk<DT>(x[b], c);
       }
@@ -165,7 +170,13 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
       wait_all();
       barrier();
       issue(keys.tile(u + 1), nk, nv, u + 1 < keys.count);
-      compute(lk, lv, keys.tile(u));
+      const int t = keys.tile(u), j0 = t * KT;
+      const bool whole = (j0 + KT <= q.prefix) || (j0 >= wh.low && j0 + KT - 1 <= wl.high);
+      // (capped scores are masked twice, so that the compiler would take the masks of whole tiles
+      // too: a build for each)
+      if (MODE != kCapScore) compute(lk, lv, t, whole);
+      else if (whole) compute(lk, lv, t, std::true_type());
+      else compute(lk, lv, t, std::false_type());
     };
     issue(keys.tile(0), lk0, lv0, keys.count > 0);
     int u = 0;
@@ -224,7 +235,8 @@ lowbit_status launch_attn_width(const AttnArgs& a, hipStream_t s) {
   const lowbit_status st =
       mode == kPlainScore  ? launch(&attn_kernel<DT, D, kPlainScore>, blocks, kAttnThreads, s, a, tiles)
       : mode == kBiasScore ? launch(&attn_kernel<DT, D, kBiasScore>, blocks, kAttnThreads, s, a, tiles)
-                           : launch(&attn_kernel<DT, D, kCapScore>, blocks, kAttnThreads, s, a, tiles);
+      : mode == kCapScore  ? launch(&attn_kernel<DT, D, kCapScore>, blocks, kAttnThreads, s, a, tiles)
+                           : launch(&attn_kernel<DT, D, kCapBiasScore>, blocks, kAttnThreads, s, a, tiles);
   if (st != LOWBIT_OK || a.q_parts == 1) return st;
   return launch(&attn_join_kernel<DT, D>, capped(Items(tiles, a.kv_heads, a.group * (D / 32)).total),
                 kAttnThreads, s, a, tiles);
