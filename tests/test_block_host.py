@@ -24,9 +24,8 @@ def _rotary(x=OK16, freqs=OK16, positions=OK16, y=OK16, back=False, **change):
         y = ctypes.c_void_p(0x100000)
     v.update(change if "y_strides" not in change else {k: w for k, w in change.items() if k != "y_strides"})
     ys = change.get("y_strides", v["y"])
-    p = L.RotaryParams(v["rows"], v["rows_per_sequence"], L.Strides(*v["x"]) if isinstance(v["x"], tuple)
-                       else v["x"], L.Strides(*ys), v["heads"], v["head_dim"], v["rot_dim"],
-                       v["layout"], v["type"], v["scale"])
+    p = L.RotaryParams(v["rows"], v["rows_per_sequence"], *v["x"], *ys, v["heads"], v["head_dim"],
+                       v["rot_dim"], v["layout"], v["type"], v["scale"])
     call = L.lib().lowbit_rotary_backward if back else L.lib().lowbit_rotary
     return call(x, freqs, positions, p, y, None)
 
@@ -46,12 +45,12 @@ def test_rotary_refusals(back):
     assert _rotary(back=back, rows=0, y_strides=(1, 64)) == L.OK
     call = L.lib().lowbit_rotary
     assert call(OK16, OK16, OK16, None, OK16, None) == L.EINVAL
-    p = L.RotaryParams(10, 0, L.Strides(256, 64), L.Strides(256, 64), 4, 64, 32, 0, 0, 1.0)
+    p = L.RotaryParams(10, 0, 256, 64, 256, 64, 4, 64, 32, 0, 0, 1.0)
     assert call(None, OK16, OK16, p, OK16, None) == L.EINVAL
     assert call(OK16, OK16, OK16, p, None, None) == L.EINVAL
     assert call(ctypes.c_void_p(0x1002), OK16, OK16, p, OK16, None) == L.EINVAL
     # in place with other strides
-    p.x = L.Strides(512, 64)
+    p.x_row = 512
     assert call(OK16, OK16, OK16, p, OK16, None) == L.EINVAL
 
 
@@ -107,7 +106,7 @@ def _params(**change):
     strides = {n: (64 * (2 if n[-1] in "kv" else 4), 64) for n in NAMES}
     for k, w in change.items():
         (strides if k in NAMES else v)[k] = w
-    return L.AttentionParams(*v.values(), *[L.Strides(*strides[n]) for n in NAMES])
+    return L.AttentionParams(*v.values(), *[s for n in NAMES for s in strides[n]])
 
 
 def _both(p, q=OK16, k=OK16, v=OK16, qb=OK16, kb=None, pre=None, sl=None, out=OK16, lse=OK16,
@@ -188,17 +187,15 @@ def test_attention_binding_refusals():
 
 def test_strides_that_the_binding_passes_on():
     t = torch.zeros(6, 7, 16)
-    assert [(r, s.row, s.head) for r, s in (L._heads(v, "t") for v in (t, t[:, 2:5], t[:1], t[:, :1]))] \
+    assert [L._heads(v, "t") for v in (t, t[:, 2:5], t[:1], t[:, :1])] \
         == [(6, 112, 16), (6, 112, 16), (1, 112, 16), (6, 112, 16)]
     four = torch.zeros(2, 3, 5, 8)
-    r, s = L._heads(four[:, :, 1:3], "t")
-    assert (r, s.row, s.head) == (6, 40, 8)
+    assert L._heads(four[:, :, 1:3], "t") == (6, 40, 8)
     with pytest.raises(L.LowbitError):
         L._heads(four[:, :2], "t")
     with pytest.raises(L.LowbitError):
         L._heads(four.transpose(-1, -2), "t")
-    r, s = L._heads(four[:, :1], "t")                              # a step of 120 from batch to batch
-    assert (r, s.row, s.head) == (2, 120, 8)
+    assert L._heads(four[:, :1], "t") == (2, 120, 8)                # a step of 120 between batches
 
 
 def test_windows_beyond_64_bits():

@@ -17,7 +17,7 @@ struct RotaryArgs {
   int64_t rows, rows_per_sequence;
   int64_t x_row, x_head, y_row, y_head;
   int32_t heads, head_dim, rot_dim;
-  int32_t lanes;             // units of a head: of 8 pairs, then of 8 copied elements
+  int32_t lanes;             // units of a head: of pairs, then of 16 copied bytes
   int32_t turning;           // units that turn pairs
   int32_t groups;            // the heads are shared out among so many lanes
   int32_t rows_per_block;

@@ -73,15 +73,15 @@ class XentParams(ctypes.Structure):
                 ("ignore_index", ctypes.c_int64), ("type", ctypes.c_int32)]
 
 
-class Strides(ctypes.Structure):
-    """lowbit_strides"""
-    _fields_ = [("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+def _strides_of(*names):
+    """lowbit_strides, one after the other (flat: nested structures take a microsecond each)"""
+    return [(f"{n}_{w}", ctypes.c_int64) for n in names for w in ("row", "head")]
 
 
 class RotaryParams(ctypes.Structure):
     """lowbit_rotary_params"""
-    _fields_ = [("rows", ctypes.c_int64), ("rows_per_sequence", ctypes.c_int64), ("x", Strides),
-                ("y", Strides), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+    _fields_ = [("rows", ctypes.c_int64), ("rows_per_sequence", ctypes.c_int64),
+                *_strides_of("x", "y"), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("type", ctypes.c_int32),
                 ("scale", ctypes.c_float)]
 
@@ -92,8 +92,8 @@ class AttentionParams(ctypes.Structure):
                 ("sequences", ctypes.c_int32), ("q_heads", ctypes.c_int32),
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("type", ctypes.c_int32), ("causal", ctypes.c_int32), ("scale", ctypes.c_float),
-                ("softcap", ctypes.c_float)] + [
-                    (name, Strides) for name in ("q", "k", "v", "out", "dout", "dq", "dk", "dv")]
+                ("softcap", ctypes.c_float),
+                *_strides_of("q", "k", "v", "out", "dout", "dq", "dk", "dv")]
 
 
 class OrthogonalizeParams(ctypes.Structure):
@@ -826,43 +826,52 @@ def _gpu(t: torch.Tensor, what: str) -> int:
 
 
 def _heads(t: torch.Tensor, what: str):
-    """Rows and strides of (..., heads, head_dim): one step for all leading dimensions, dense
-    heads.  (A step of a dimension of one element is of no account.)"""
-    if t.dim() < 2:
-        raise LowbitError(EINVAL, f"{what} must be (..., heads, head_dim)")
+    """Rows, and the steps from row to row and from head to head, of (..., heads, head_dim): one
+    step for all leading dimensions, dense heads.  (A step of a dimension of one element is of no
+    account.)"""
     size, step = t.shape, t.stride()
-    if size[-1] > 1 and step[-1] != 1:
+    if len(size) < 2:
+        raise LowbitError(EINVAL, f"{what} must be (..., heads, head_dim)")
+    heads, dim = size[-2], size[-1]
+    if dim > 1 and step[-1] != 1:
         raise LowbitError(EINVAL, f"{what}: the elements of a head must be dense")
-    rows, row = 1, None
-    for n, s in zip(size[-3::-1], step[-3::-1]):
-        if n != 1:
-            if row is None:
-                row = s
-            elif s != row * rows and t.numel():
-                raise LowbitError(EINVAL, f"{what}: the leading dimensions must have one step")
-            rows *= n
-    head = step[-2] if size[-2] > 1 else size[-1]
-    return rows, Strides(row if row is not None and rows > 1 else size[-2] * size[-1], head)
+    if len(size) == 3:
+        rows, row = size[0], step[0]
+    else:
+        rows, row = 1, 0
+        for n, s in zip(size[-3::-1], step[-3::-1]):
+            if n != 1:
+                if rows == 1:
+                    row = s
+                elif s != row * rows and t.numel():
+                    raise LowbitError(EINVAL, f"{what}: the leading dimensions must have one step")
+                rows *= n
+    return rows, row if rows > 1 else heads * dim, step[-2] if heads > 1 else dim
 
 
-def _rotary(call, x, freqs, positions, rows_per_sequence, layout, scale, out, what):
+def _rotary(fn, name, x, freqs, positions, rows_per_sequence, layout, scale, out, what):
     if layout not in _LAYOUTS:
         raise LowbitError(EINVAL, "layout must be 'half' or 'interleaved'")
-    rows, xs = _heads(x, what)
-    if freqs.dtype != torch.float64 or freqs.device != x.device:
+    rows, x_row, x_head = _heads(x, what)
+    device = x.device
+    if freqs.dtype != torch.float64 or freqs.device != device:
         raise LowbitError(EINVAL, "freqs must be float64 on the device of the tensor to turn")
     if positions is not None and (positions.dtype != torch.int64 or positions.numel() != rows
-                                  or positions.device != x.device):
+                                  or positions.device != device):
         raise LowbitError(EINVAL, "positions must be int64, one for each row")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
-        raise LowbitError(EINVAL, "out must match the input in shape, dtype and device")
-    _, ys = _heads(out, "out")
-    p = RotaryParams(rows, int(rows_per_sequence) or max(rows, 1), xs, ys, x.shape[-2],
-                     x.shape[-1], 2 * freqs.numel(), _LAYOUTS[layout], _dtype_code(x), scale)
-    _check(getattr(lib(), call)(_gpu(x, what), _dev(freqs, "freqs"), _opt(positions, "positions"),
-                                p, _gpu(out, "out"), _stream(x)), call)
+        out = torch.empty(x.shape, dtype=x.dtype, device=device)
+        y_row, y_head = x.shape[-2] * x.shape[-1], x.shape[-1]
+    else:
+        if out.shape != x.shape or out.dtype != x.dtype or out.device != device:
+            raise LowbitError(EINVAL, "out must match the input in shape, dtype and device")
+        _, y_row, y_head = _heads(out, "out")
+    p = RotaryParams(rows, int(rows_per_sequence) or max(rows, 1), x_row, x_head, y_row, y_head,
+                     x.shape[-2], x.shape[-1], 2 * freqs.numel(), _LAYOUTS[layout],
+                     _dtype_code(x), scale)
+    _check(fn(_gpu(x, what), _dev(freqs, "freqs"),
+              None if positions is None else _dev(positions, "positions"), p, out.data_ptr(),
+              _stream(x)), name)
     return out
 
 
@@ -879,7 +888,7 @@ def rotary(x: torch.Tensor, freqs: torch.Tensor, positions: Optional[torch.Tenso
     (0: never).  `out` may be x."""
     if x.requires_grad:
         _outside_autograd("rotary")
-    return _rotary("lowbit_rotary", x, freqs, positions, rows_per_sequence, layout, scale, out, "x")
+    return _rotary(lib().lowbit_rotary, "lowbit_rotary", x, freqs, positions, rows_per_sequence, layout, scale, out, "x")
 
 
 def rotary_backward(dy: torch.Tensor, freqs: torch.Tensor,
@@ -887,8 +896,8 @@ def rotary_backward(dy: torch.Tensor, freqs: torch.Tensor,
                     layout: str = "half", scale: float = 1.0,
                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of `rotary` by x, with its options.  `out` may be dy."""
-    return _rotary("lowbit_rotary_backward", dy, freqs, positions, rows_per_sequence, layout,
-                   scale, out, "dy")
+    return _rotary(lib().lowbit_rotary_backward, "lowbit_rotary_backward", dy, freqs, positions,
+                   rows_per_sequence, layout, scale, out, "dy")
 
 
 class Attention(NamedTuple):
@@ -937,13 +946,15 @@ def _attention_params(q, k, v, q_begin, k_begin, scale, causal, window, prefix, 
     if slopes is not None and (slopes.dtype != torch.float32 or slopes.numel() != q.shape[-2]
                                or slopes.device != q.device):
         raise LowbitError(EINVAL, "slopes must be float32, one for each head of q")
-    (q_rows, qs), (k_rows, ks), (_, vs) = _heads(q, "q"), _heads(k, "k"), _heads(v, "v")
+    q_rows, q_row, q_head = _heads(q, "q")
+    k_rows, k_row, k_head = _heads(k, "k")
+    _, v_row, v_head = _heads(v, "v")
     d = q.shape[-1]
     # (a window beyond 64 bits hides nothing either)
-    p = AttentionParams(q_rows, k_rows, max(-1, min(int(window), 1 << 40)), sequences, q.shape[-2],
-                        k.shape[-2], d, _dtype_code(q), int(bool(causal)),
-                        d ** -0.5 if scale is None else scale, softcap, qs, ks, vs)
-    return p
+    return AttentionParams(q_rows, k_rows, max(-1, min(int(window), 1 << 40)), sequences,
+                           q.shape[-2], k.shape[-2], d, _dtype_code(q), int(bool(causal)),
+                           d ** -0.5 if scale is None else scale, softcap,
+                           q_row, q_head, k_row, k_head, v_row, v_head)
 
 
 def _attention_scratch(L, p, backward, like, workspace, what):
@@ -989,7 +1000,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         _outside_autograd("attention")
     p = _attention_params(q, k, v, q_begin, k_begin, scale, causal, window, prefix, softcap, slopes)
     out = _attention_out(out, q, "out")
-    p.out = _heads(out, "out")[1]
+    _, p.out_row, p.out_head = _heads(out, "out")
     lse = torch.empty(p.q_heads, p.q_rows, dtype=torch.float32, device=q.device)
     L = lib()
     ws, nbytes = _attention_scratch(L, p, 0, q, workspace, "attention")
@@ -1019,8 +1030,11 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
         raise LowbitError(EINVAL, "lse must be the forward call's")
     dq, dk, dv = (_attention_out(dq, q, "dq"), _attention_out(dk, k, "dk"),
                   _attention_out(dv, v, "dv"))
-    for name, t in (("out", out), ("dout", dout), ("dq", dq), ("dk", dk), ("dv", dv)):
-        setattr(p, name, _heads(t, name)[1])
+    _, p.out_row, p.out_head = _heads(out, "out")
+    _, p.dout_row, p.dout_head = _heads(dout, "dout")
+    _, p.dq_row, p.dq_head = _heads(dq, "dq")
+    _, p.dk_row, p.dk_head = _heads(dk, "dk")
+    _, p.dv_row, p.dv_head = _heads(dv, "dv")
     L = lib()
     ws, nbytes = _attention_scratch(L, p, 1, q, workspace, "attention_backward")
     _check(L.lowbit_attention_backward(
