@@ -462,6 +462,109 @@ __global__ void __launch_bounds__(F::THREADS, F::PER_CU * F::W / 4) ortho_tile_k
   }
 }
 
+// Matrices of at most M = 64 or 128 rows: b A + c A A and the product with X in one launch.  A
+// workgroup takes 64 columns of X with all rows and makes all of B for itself, a 2 M^3 of
+// operations that the launch of its own (5 us) costs many times over.
+template <int M, int KIND>
+__global__ void __launch_bounds__(256) ortho_short_kernel(OrthoArgs g) {
+  constexpr int W = 4, I = M / 64, STEPS = M / 64;       // waves 2 x 2; steps of 64 of k
+  __shared__ __attribute__((aligned(1024))) char la[STEPS * M * kRowBytes];
+  __shared__ __attribute__((aligned(1024))) char lb[STEPS * M * kRowBytes];
+  __shared__ __attribute__((aligned(1024))) char lx[STEPS * 64 * kRowBytes];
+  __shared__ __attribute__((aligned(1024))) char side[W * 4096];
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / 2, wn = wave % 2, r = lane % 32, h = lane / 32;
+  Feed<kF16, M, W, false> fa;
+  Feed<kF16, 64, W, true> fx;
+  Frag<kF16, M, false> rows, columns;
+  Frag<kF16, 64, true> rx;
+  fa.init(g.ldm, wave, lane);
+  fx.init(g.ldn, wave, lane);
+  rows.init(wm * (M / 2), lane);
+  columns.init(wn * (M / 2), lane);
+  rx.init(wn * 32, lane);
+  const int across = (g.n + 63) / 64;
+  // where four columns from col on of a row lie, as the operands are read
+  auto place_of = [&](char* l, int row, int col) {
+    return reinterpret_cast<u32x2*>(l + col / 64 * (M * kRowBytes) + row * kRowBytes +
+                                    ((col % 64 / 8) ^ (row >> 1 & 7)) * 16 + col % 8 * 2);
+  };
+  for (int64_t unit = blockIdx.x; unit < g.batch * across; unit += gridDim.x) {
+    const int64_t matrix = unit / across;
+    const int col0 = (int)(unit - matrix * across) * 64;
+    const int64_t mm = matrix * g.m;
+    fa.seek(static_cast<const _Float16*>(g.ah) + mm * g.ldm, g.ldm, g.m, 0, 0);
+    fx.seek(static_cast<const _Float16*>(g.xh) + mm * g.ldn, g.ldn, g.m, col0, 0);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const auto qa = fa.open(true), qx = fx.open(true);
+#pragma unroll
+      for (int j = 0; j < Feed<kF16, M, W, false>::LOADS; ++j)
+        fa.load(qa, la + s * M * kRowBytes, wave, g.m - s * 64, j);
+#pragma unroll
+      for (int j = 0; j < Feed<kF16, 64, W, true>::LOADS; ++j)
+        fx.load(qx, lx + s * 64 * kRowBytes, wave, 64, j);
+      fa.next();
+      fx.next();
+    }
+    wait_loads();
+    barrier();
+    f32x16 acc[I][I];
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+      for (int j = 0; j < I; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4 * STEPS; ++k) {
+      const char* const l = la + k / 4 * (M * kRowBytes);
+      u32x4 fm[I], fn[I];
+#pragma unroll
+      for (int i = 0; i < I; ++i) {
+        fm[i] = rows.load(l, i, k % 4);
+        fn[i] = columns.load(l, i, k % 4);
+      }
+#pragma unroll
+      for (int i = 0; i < I; ++i)
+#pragma unroll
+        for (int j = 0; j < I; ++j) acc[i][j] = mma<kF16>(fn[j], fm[i], acc[i][j]);
+    }
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+      for (int j = 0; j < I; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = wm * (M / 2) + 32 * i + r, col = wn * (M / 2) + 32 * j + 8 * q + 4 * h;
+          const f32x4 a = unpack_f16(*place_of(la, row, col)), v = quad(acc[i][j], q);
+          f32x4 y;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            y[e] = __builtin_fmaf(g.b * (kB / kA), a[e], v[e] * (g.c * (kB / (kA * kA))));
+          *place_of(lb, row, col) = pack_f16(y);
+        }
+    __syncthreads();
+    f32x16 sum[I];
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sum[i][e] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4 * STEPS; ++k) {
+      const u32x4 x = rx.load(lx + k / 4 * (64 * kRowBytes), 0, k % 4);
+#pragma unroll
+      for (int i = 0; i < I; ++i)
+        sum[i] = mma<kF16>(x, rows.load(lb + k / 4 * (M * kRowBytes), i, k % 4), sum[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+      finish_block<KIND>(g, matrix, sum[i], wm * (M / 2) + 32 * i, col0 + wn * 32,
+                         KIND == kLast && g.turned, lane, side + wave * 4096);
+    __syncthreads();                               // (the next unit's loads go where the waves read)
+  }
+}
+
 // The parts' sums of a tile that is cut along k, added in order.
 template <class F, int KIND>
 __global__ void __launch_bounds__(F::THREADS) ortho_add_kernel(OrthoArgs g) {
@@ -523,6 +626,13 @@ lowbit_status launch_product(const OrthoArgs& args, hipStream_t s) {
   }
 }
 
+template <int KIND>
+lowbit_status launch_short(const OrthoArgs& g, hipStream_t s) {
+  const int64_t blocks = std::min<int64_t>(g.batch * ((g.n + 63) / 64), 1 << 20);
+  return g.m <= 64 ? launch(&ortho_short_kernel<64, KIND>, blocks, 256, s, g)
+                   : launch(&ortho_short_kernel<128, KIND>, blocks, 256, s, g);
+}
+
 }  // namespace
 
 lowbit_status launch_ortho(int dt, const OrthoArgs& args, int steps, hipStream_t s) {
@@ -538,9 +648,13 @@ lowbit_status launch_ortho(int dt, const OrthoArgs& args, int steps, hipStream_t
                           : launch(&ortho_start_kernel<kBF16>, blocks, 256, s, g);
   for (int k = 0; k < steps && st == LOWBIT_OK; ++k) {
     st = launch_product<kGram>(g, s);
-    if (st == LOWBIT_OK) st = launch_product<kPoly>(g, s);
-    if (st == LOWBIT_OK)
-      st = k + 1 < steps ? launch_product<kUpdate>(g, s) : launch_product<kLast>(g, s);
+    const bool last = k + 1 == steps;
+    if (g.m <= 128) {
+      if (st == LOWBIT_OK) st = last ? launch_short<kLast>(g, s) : launch_short<kUpdate>(g, s);
+    } else {
+      if (st == LOWBIT_OK) st = launch_product<kPoly>(g, s);
+      if (st == LOWBIT_OK) st = last ? launch_product<kLast>(g, s) : launch_product<kUpdate>(g, s);
+    }
     std::swap(g.xh, g.xh_next);
   }
   return st == LOWBIT_OK && steps == 0 ? launch(&ortho_end_kernel, blocks, 256, s, g) : st;
