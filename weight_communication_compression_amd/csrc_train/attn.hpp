@@ -268,14 +268,31 @@ struct Score {
   __device__ __forceinline__ void head(const AttnArgs& g, int h) {
     if (has_bias(MODE)) slope = g.slopes[h] * unit_of<DT>();
   }
-  // (1 - tanh) / 2 of the capped sum: 1 / (exp(2 x) + 1), off by 2^-24 or so, well below what
-  // bfloat16 weights are rounded to
-  __device__ __forceinline__ float below(float x) const {
-    if constexpr (DT == kF32) return 0.5f - 0.5f * tanhf(x * factor);
-    else return __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * factor) + 1.0f);
+  // The capped score of a sum, and the gradient's factor 1 - tanh^2.
+  __device__ __forceinline__ float capped(float x, float& bend) const {
+    x *= factor;
+    if constexpr (DT == kF32) {
+      // tanh by its series where it is small, so that scores keep their relative accuracy
+      const float z = x * x;
+      float s = __builtin_fmaf(z, 3.59212803e-3f, -8.86323552e-3f);
+      s = __builtin_fmaf(z, s, 2.18694885e-2f);
+      s = __builtin_fmaf(z, s, -5.39682540e-2f);
+      s = __builtin_fmaf(z, s, 1.33333333e-1f);
+      s = __builtin_fmaf(z, s, -3.33333333e-1f);
+      s = __builtin_fmaf(x * z, s, x);
+      const float e = exp_unit<kF32>(2.0f * fabsf(x));
+      const float l = copysignf(__builtin_fmaf(-2.0f, __builtin_amdgcn_rcpf(e + 1.0f), 1.0f), x);
+      const float t = fabsf(x) < 0.4f ? s : l;
+      bend = __builtin_fmaf(-t, t, 1.0f);
+      return cap * t;
+    } else {
+      // r = (1 - tanh) / 2 = 1 / (exp(2 x) + 1), off by 2^-24 or so, well below what the weights
+      // are rounded to
+      const float r = __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x) + 1.0f);
+      bend = 4.0f * __builtin_fmaf(-r, r, r);
+      return __builtin_fmaf(-2.0f * cap, r, cap);
+    }
   }
-  // the gradient's factor 1 - tanh^2
-  static __device__ __forceinline__ float bend_of(float r) { return 4.0f * __builtin_fmaf(-r, r, r); }
 
   // x: a sum of products; distance: |distance - c| to the key
   __device__ __forceinline__ float at(float x, float distance, int c, float& bend) const {
@@ -284,18 +301,15 @@ struct Score {
       return x;
     } else {
       float y = x * factor;
-      if constexpr (has_cap(MODE)) {
-        const float r = below(x);
-        bend = bend_of(r);
-        y = __builtin_fmaf(-2.0f * cap, r, cap);
-      }
+      if constexpr (has_cap(MODE)) y = capped(x, bend);
       return __builtin_fmaf(-slope, fabsf(distance - (float)c), y);
     }
   }
   // the largest score, in units, from the largest of what `at` gives
   __device__ __forceinline__ float scaled(float y) const {
     if (MODE == kPlainScore) return y * factor;
-    if (MODE == kCapScore) return y == -INFINITY ? y : __builtin_fmaf(-2.0f * cap, below(y), cap);
+    float bend;
+    if (MODE == kCapScore) return y == -INFINITY ? y : capped(y, bend);
     return y;
   }
   // exp(score - base); of a masked -infinity 0, but where MODE is kCapScore
@@ -303,9 +317,7 @@ struct Score {
     if constexpr (MODE == kPlainScore) {
       return exp_unit<DT>(__builtin_fmaf(y, factor, -base));
     } else if constexpr (MODE == kCapScore) {
-      const float r = below(y);
-      bend = bend_of(r);
-      return exp_unit<DT>(__builtin_fmaf(-2.0f * cap, r, cap - base));
+      return exp_unit<DT>(capped(y, bend) - base);
     } else {
       return exp_unit<DT>(y - base);
     }

@@ -139,8 +139,9 @@ struct AttnPlan {
 // The chip holds 512 workgroups at one time.  Where there are fewer tiles of
 // queries, their keys are cut, down to 256 on average (64 of binary32, whose products take
 // eight times as long).  By k and v the gradient's workgroups take from nothing to twice the
-// mean of a causal sequence, so that two rounds of them are wanted, the long ones first; their
-// queries are cut, down to as many of all heads.
+// mean of a causal sequence, so that more than one round of them is wanted, the long ones first;
+// their queries are cut, down to as many of all heads.  (Five ragged documents, 144 tiles of
+// keys, gradient by k and v and the parts' sums: 8 parts 78 us, 6 70, 5 67, 4 72.)
 AttnPlan attn_plan(const lowbit_attention_params* p, bool backward) {
   AttnPlan w{};
   const int64_t each = std::max(p->sequences, 1), group = p->q_heads / p->kv_heads;
@@ -154,7 +155,7 @@ AttnPlan attn_plan(const lowbit_attention_params* p, bool backward) {
   const int64_t q_tiles = attn_tiles(p->q_rows, p->sequences) * (int64_t)p->q_heads;
   const int64_t k_tiles = attn_tiles(p->k_rows, p->sequences) * (int64_t)p->kv_heads;
   w.q_parts = q_tiles >= 512 ? 1 : parts(768, q_tiles, p->k_rows / each / least);
-  w.k_parts = backward ? parts(1024, k_tiles, p->q_rows * group / each / least) : 1;
+  w.k_parts = backward ? parts(640, k_tiles, p->q_rows * group / each / least) : 1;
   w.q_sums = backward ? up(p->q_rows * p->q_heads * 8, 256) : 0;
   // (the forward call keeps the maximum and the sum of a row beside the two halves of it)
   w.k_sums = w.q_sums + (w.q_parts > 1 ? q_tiles * w.q_parts * (tile + (backward ? 0 : kAttnRows * 32)) : 0);
