@@ -137,16 +137,18 @@ struct AttnPlan {
 };
 
 // The chip holds 512 workgroups at one time.  Where there are fewer tiles of
-// queries, their keys are cut, down to 256 on average (64 of binary32, whose products take
-// eight times as long).  By k and v the gradient's workgroups take from nothing to twice the
-// mean of a causal sequence, so that more than one round of them is wanted, the long ones first;
-// their queries are cut, down to as many of all heads.  (Five ragged documents, 144 tiles of
-// keys, gradient by k and v and the parts' sums: 8 parts 78 us, 6 70, 5 67, 4 72.)
+// queries, their keys are cut, down to 256 on average.  By k and v the gradient's workgroups
+// take from nothing to twice the mean of a causal sequence, so that more than one round of them
+// is wanted, the long ones first; their queries are cut, down to as many of all heads.  (Five
+// ragged documents, 144 tiles of keys, gradient by k and v and the parts' sums: 8 parts 78 us, 6
+// 70, 5 67, 4 72; by q, 432 tiles: 1 part 55 us, 2 54, 3 61.)  Of binary32 products take eight times as long, so that parts go down to
+// 64, and of wide heads a CU holds one workgroup: as many parts as fill one round.
 AttnPlan attn_plan(const lowbit_attention_params* p, bool backward) {
   AttnPlan w{};
   const int64_t each = std::max(p->sequences, 1), group = p->q_heads / p->kv_heads;
-  auto parts = [](int64_t wanted, int64_t tiles, int64_t most) {
-    const int64_t n = tiles ? (wanted + tiles - 1) / tiles : 1;
+  const bool alone = p->type == LOWBIT_F32 && p->head_dim > 64;
+  auto parts = [&](int64_t wanted, int64_t tiles, int64_t most) {
+    const int64_t n = !tiles ? 1 : alone ? 256 / tiles : (wanted + tiles - 1) / tiles;
     return (int)std::max<int64_t>(1, std::min<int64_t>({n, most, 16}));
   };
   const int64_t least = p->type == LOWBIT_F32 ? 64 : 256;
