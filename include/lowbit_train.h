@@ -355,7 +355,7 @@ int64_t lowbit_orthogonalize_workspace(const lowbit_orthogonalize_params* p);
  * relative, and summed in binary32: three bits more than
  * bfloat16 operands, whose errors the iteration raises to several hundredths.  They hold singular
  * values up to 4; coefficients that let X grow beyond give infinities or NaN.  A matrix of zeros gives
- * zeros if eps > 0, one with an infinity or NaN gives NaN.
+ * zeros if eps > 0, one with an infinity or NaN gives NaN (from the first step on).
  * EINVAL: p == NULL, a size, type or option outside its range, NULL or misaligned
  * pointer with batch > 0, workspace too small.
  */

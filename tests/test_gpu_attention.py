@@ -167,8 +167,9 @@ def test_batches(dtype):
     assert all(torch.equal(x.reshape(y.shape), y) for x, y in zip(a, b))
 
 
-def test_rows_outside_are_left():
-    lens, first, behind = [40, 30], 9, 50
+@pytest.mark.parametrize("first,behind", [(9, 50), (128, 0), (301, 300)])
+def test_rows_outside_are_left(first, behind):
+    lens = [40, 30]
     q, k, v = inputs(lens, lens, 2, 1, 64, torch.bfloat16, True, 4, first, behind)
     for t in (q, k, v):                               # nothing of these is used
         t[:first] = math.nan

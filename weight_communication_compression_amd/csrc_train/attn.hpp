@@ -445,7 +445,7 @@ struct Queries {
     q = sequence_at(g, s);
     i0 = (t - first_tile(g.q_begin, s, g.sequences, g.q_rows, kRowsPerTile)) * kRowsPerTile;
     last = min(i0 + kRowsPerTile, q.lq) - 1;
-    any = i0 < q.lq;
+    any = i0 >= 0 && i0 < q.lq;                    // (below 0: rows before the first sequence)
   }
 };
 

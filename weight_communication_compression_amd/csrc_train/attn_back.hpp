@@ -184,7 +184,7 @@ struct Keys {
     const int s = find_sequence(g.k_begin, g.sequences, g.k_rows, kRowsPerTile, t);
     q = sequence_at(g, s);
     j0 = (t - first_tile(g.k_begin, s, g.sequences, g.k_rows, kRowsPerTile)) * kRowsPerTile;
-    any = j0 < q.lk;
+    any = j0 >= 0 && j0 < q.lk;                    // (below 0: rows before the first sequence)
   }
 };
 

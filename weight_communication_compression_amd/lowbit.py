@@ -995,7 +995,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     key j if  j < prefix[s]  or  (not causal or j <= position) and (window == 0 or
     |position - j| < window).  Scores are softcap * tanh(scale q.k / softcap) (softcap 0: scale
     q.k; scale None: head_dim ** -0.5) minus slopes[head] * |position - j|.  A query that sees
-    nothing gives 0 and lse -infinity.  Rows outside all sequences are left as they were."""
+    nothing gives 0 and lse -infinity.  Rows outside all sequences are left as they were: in
+    `out` and lse that are allocated here whatever the memory held."""
     if q.requires_grad or k.requires_grad or v.requires_grad:
         _outside_autograd("attention")
     p = _attention_params(q, k, v, q_begin, k_begin, scale, causal, window, prefix, softcap, slopes)
@@ -1022,7 +1023,8 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
                        dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
                        workspace: Optional[torch.Tensor] = None) -> AttentionGrads:
     """Gradients of `attention` by q, k and v from that of out, with the forward call's out, lse
-    and options.  dq, dk, dv may be views, as of a packed projection's gradient."""
+    and options.  dq, dk, dv may be views, as of a packed projection's gradient; rows outside all
+    sequences are left as they were."""
     p = _attention_params(q, k, v, q_begin, k_begin, scale, causal, window, prefix, softcap, slopes)
     for t, what in ((dout, "dout"), (out, "out")):
         _attention_out(t, q, what)
