@@ -138,32 +138,6 @@ enum OrthoKind : int {
 template <int KIND>
 constexpr bool kMirrored = KIND == kGram || KIND == kPoly;
 
-// Where a tile lies.  Tiles are counted in bands of 8 rows of tiles (4 of a mirrored product),
-// down a band's columns: the 32 that an XCD's CUs hold at one time then share the panels that
-// they read through its L2.
-struct Place {
-  int tm, tn;
-};
-template <int KIND>
-__device__ __forceinline__ Place place(int tile, int across, int down) {
-  if constexpr (kMirrored<KIND>) {
-    // band b begins at tile b (8 b + 2): rows 0 .. 4 b - 1 have 1, 2, ... tiles
-    int b = (int)(sqrtf((float)tile * 0.125f));
-    while ((b + 1) * (8 * (b + 1) + 2) <= tile) ++b;
-    while (b * (8 * b + 2) > tile) --b;
-    const int high = min(4, down - 4 * b), whole = 4 * b + 1;
-    int in = tile - b * (8 * b + 2);
-    if (in < high * whole) return {4 * b + in % high, in / high};
-    in -= high * whole;                            // beyond the band's first diagonal tile
-    int j = 1;
-    while (in >= high - j) in -= high - j++;
-    return {4 * b + j + in, 4 * b + j};
-  } else {
-    const int band = tile / (8 * across), in = tile % (8 * across), high = min(8, down - band * 8);
-    return {band * 8 + in % high, in / high};
-  }
-}
-
 // Four columns col .. col + 3 of a row of the result, from the products' sums.
 template <int KIND>
 __device__ __forceinline__ f32x4 value(const OrthoArgs& g, int64_t matrix, int row, int col, f32x4 v) {
@@ -389,13 +363,11 @@ __global__ void __launch_bounds__(F::THREADS, F::PER_CU * F::W / 4) ortho_tile_k
 
   const int64_t total = tiles * g.batch * g.k_parts;
   for (int64_t unit = blockIdx.x; unit < total; unit += gridDim.x) {
-    // unit u is a workgroup's of XCD u mod 8, of which each takes a contiguous run
-    const int64_t x = unit % 8, each = total / 8, more = total % 8;
-    const int64_t mine = x * each + (x < more ? x : more) + unit / 8;
+    const int64_t mine = ortho_run(unit, total);
     const int64_t which = mine / g.k_parts;
     const int part = (int)(mine - which * g.k_parts);
     const int64_t matrix = which / tiles;
-    const Place at = place<KIND>((int)(which - matrix * tiles), across, down);
+    const OrthoPlace at = ortho_place(kMirrored<KIND>, (int)(which - matrix * tiles), across, down);
     const int tm = __builtin_amdgcn_readfirstlane(at.tm), tn = __builtin_amdgcn_readfirstlane(at.tn);
     s0 = __builtin_amdgcn_readfirstlane((int)((int64_t)all_steps * part / g.k_parts));
     s1 = __builtin_amdgcn_readfirstlane((int)((int64_t)all_steps * (part + 1) / g.k_parts));
@@ -579,7 +551,7 @@ __global__ void __launch_bounds__(F::THREADS) ortho_add_kernel(OrthoArgs g) {
     const int64_t which = unit / (I * J);
     const int block = (int)(unit - which * (I * J)), i = block / J, j = block % J;
     const int64_t matrix = which / tiles;
-    const Place at = place<KIND>((int)(which - matrix * tiles), across, down);
+    const OrthoPlace at = ortho_place(kMirrored<KIND>, (int)(which - matrix * tiles), across, down);
     f32x16 acc;
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[r] = 0.0f;

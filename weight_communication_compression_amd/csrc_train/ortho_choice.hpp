@@ -1,9 +1,16 @@
-// ortho_choice.hpp -- which form of the tile kernel a product of orthogonalize takes, and
-// whether it is cut along k.  Integer and float arithmetic with no HIP dependency, for the
+// ortho_choice.hpp -- which form of the tile kernel a product of orthogonalize takes,
+// whether it is cut along k, and where its tiles lie.  Integer and float arithmetic with no HIP dependency, for the
 // launches, the workspace and a CPU test.
 #pragma once
 
+#include <math.h>
 #include <stdint.h>
+
+#ifdef __HIPCC__
+#define LOWBIT_HD __host__ __device__
+#else
+#define LOWBIT_HD
+#endif
 
 namespace lowbit {
 
@@ -57,6 +64,36 @@ inline OrthoChoice ortho_choice(bool mirrored, bool gram, int64_t batch, int64_t
     }
   }
   return best;
+}
+
+// Where a tile lies.  Tiles are counted in bands of 8 rows of tiles (4 of a mirrored product, of
+// which only those on and below the diagonal count), down a band's columns: the 32 that an XCD's
+// CUs hold at one time then share the panels that they read through its L2.
+struct OrthoPlace {
+  int tm, tn;
+};
+inline LOWBIT_HD OrthoPlace ortho_place(bool mirrored, int tile, int across, int down) {
+  if (!mirrored) {
+    const int band = tile / (8 * across), in = tile % (8 * across);
+    const int high = down - band * 8 < 8 ? down - band * 8 : 8;
+    return {band * 8 + in % high, in / high};
+  }
+  // band b begins at tile b (8 b + 2): rows 0 .. 4 b - 1 have 1, 2, ... tiles
+  int b = (int)sqrtf((float)tile * 0.125f);
+  while ((b + 1) * (8 * (b + 1) + 2) <= tile) ++b;
+  while (b * (8 * b + 2) > tile) --b;
+  const int high = down - 4 * b < 4 ? down - 4 * b : 4, whole = 4 * b + 1;
+  int in = tile - b * (8 * b + 2);
+  if (in < high * whole) return {4 * b + in % high, in / high};
+  in -= high * whole;                              // beyond the band's first diagonal tile
+  int j = 1;
+  while (in >= high - j) in -= high - j++;
+  return {4 * b + j + in, 4 * b + j};
+}
+// Unit u is a workgroup's of XCD u mod 8, of which each takes a contiguous run.
+inline LOWBIT_HD int64_t ortho_run(int64_t u, int64_t count) {
+  const int64_t x = u % 8, each = count / 8, more = count % 8;
+  return x * each + (x < more ? x : more) + u / 8;
 }
 
 // Bytes for the parts' sums of a product.
