@@ -7,17 +7,27 @@ namespace lowbit {
 
 namespace {
 
+// Sizes of the two halves of the gradient.  By k and v, the wide forms' values stay in LDS,
+// since a lane's registers do not hold them too.
+template <int DT, int D>
+struct Back {
+  static constexpr int KT = DT == kF32 ? 32 : 64;  // keys of a tile that passes by
+  static constexpr bool KEEP = D <= (DT == kF32 ? 96 : 64);
+  static constexpr int QT = DT == kF32 || !KEEP ? 32 : 64;
+  static constexpr int BYTES = Tile<DT, D, KT>::BYTES, Q_BYTES = Tile<DT, D, QT>::BYTES;
+  static constexpr int VALUES = Tile<DT, D, 32>::BYTES;      // of a wave
+  // the values of bfloat16 fit where the other half has its second two tiles
+  static constexpr bool APART = !KEEP && 4 * Q_BYTES + kWaves * VALUES > 4 * BYTES;
+};
+
 // dq: four waves, each 32 queries, as in the forward pass; the scores and dout.v
 // are taken again, transposed, and their gradient is, as it lies, the operand
 // of the product with the keys.
 template <int DT, int D, int MODE>
-__global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) attn_dq_kernel(AttnArgs g, int tiles) {
-  constexpr int KT = DT == kF32 ? 32 : 64, NB = KT / 32, ES = elem_size<DT>();
+__device__ __forceinline__ void attn_dq(const AttnArgs& g, int tiles, int64_t block, int64_t blocks,
+                                        char* lk0, char* lv0, char* lk1, char* lv1) {
+  constexpr int KT = Back<DT, D>::KT, NB = KT / 32, ES = elem_size<DT>();
   using T = Tile<DT, D, KT>;
-  __shared__ __attribute__((aligned(1024))) char lk0[T::BYTES];
-  __shared__ __attribute__((aligned(1024))) char lv0[T::BYTES];
-  __shared__ __attribute__((aligned(1024))) char lk1[T::BYTES];
-  __shared__ __attribute__((aligned(1024))) char lv1[T::BYTES];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane % 32, half = lane / 32;
   const int width = g.head_dim * ES;
@@ -32,7 +42,7 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
   Score<DT, MODE> score(g);
 
   const Items items(tiles, g.kv_heads, g.group * g.q_parts);
-  for (int64_t item = blockIdx.x; item < items.total; item += gridDim.x) {
+  for (int64_t item = block; item < items.total; item += blocks) {
     const Queries w(g, items, item, tiles, g.q_parts);
     if (!w.any) continue;
     const Sequence& q = w.q;
@@ -148,27 +158,6 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
   }
 }
 
-// The parts' sums of dq, added in order; a workgroup 32 columns of a tile.
-template <int DT, int D>
-__global__ void __launch_bounds__(kAttnThreads) attn_dq_sum_kernel(AttnArgs g, int tiles) {
-  constexpr int BLOCKS = D / 32;
-  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Items items(tiles, g.kv_heads, g.group * BLOCKS);
-  for (int64_t item = blockIdx.x; item < items.total; item += gridDim.x) {
-    const Queries w(g, items, item, tiles, BLOCKS);
-    const int i = w.i0 + wave * 32 + lane % 32;
-    if (!w.any || i >= w.q.lq) continue;
-    f32x16 sum[1];
-    clear(sum);
-    for (int p = 0; p < g.q_parts; ++p)
-      add_part(sum, part_at(g.q_sums, w.unit * g.q_parts + p, BLOCKS * 4) +
-                        w.part * (4 * kAttnThreads), 1.0f);
-    store_columns<DT>(static_cast<char*>(const_cast<void*>(g.dq.p)) +
-                          ((int64_t)w.q.q0 + i) * g.dq.row + w.head * g.dq.head, sum, g.scale,
-                      lane / 32, g.head_dim, w.part);
-  }
-}
-
 // Where a workgroup's keys are.
 struct Keys {
   Sequence q;
@@ -194,19 +183,12 @@ struct Keys {
 // tiles of keys for the chip, the queries of all heads are shared out in g.k_parts
 // even parts, whose sums a second kernel adds in order.
 template <int DT, int D, int MODE>
-__global__ void __launch_bounds__(kAttnThreads, DT == kF32 ? 1 : 2) attn_dkv_kernel(AttnArgs g, int tiles) {
-  // the wide form's values stay in LDS, since a lane's 256 registers do not hold them too
-  constexpr bool KEEP = D <= (DT == kF32 ? 96 : 64);
-  constexpr int QT = DT == kF32 || !KEEP ? 32 : 64, NB = QT / 32, ES = elem_size<DT>();
+__device__ __forceinline__ void attn_dkv(const AttnArgs& g, int tiles, int64_t block, int64_t blocks,
+                                         char* lq0, char* ld0, char* li0, char* lq1, char* ld1,
+                                         char* li1, char* values) {
+  constexpr bool KEEP = Back<DT, D>::KEEP;
+  constexpr int QT = Back<DT, D>::QT, NB = QT / 32, ES = elem_size<DT>();
   using T = Tile<DT, D, QT>;
-  using V = Tile<DT, D, 32>;                       // a wave's values
-  __shared__ __attribute__((aligned(1024))) char lvalues[KEEP ? 16 : kWaves * V::BYTES];
-  __shared__ __attribute__((aligned(1024))) char lq0[T::BYTES];
-  __shared__ __attribute__((aligned(1024))) char ld0[T::BYTES];
-  __shared__ __attribute__((aligned(1024))) char lq1[T::BYTES];
-  __shared__ __attribute__((aligned(1024))) char ld1[T::BYTES];
-  __shared__ __attribute__((aligned(1024))) char li0[1024];  // lse, -D of 64 queries, twice
-  __shared__ __attribute__((aligned(1024))) char li1[1024];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane % 32, half = lane / 32;
   const int width = g.head_dim * ES;
@@ -220,7 +202,7 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 ? 1 : 2) attn_dkv_ker
   Score<DT, MODE> score(g);
 
   const Items items(tiles, g.kv_heads, g.k_parts);
-  for (int64_t item = blockIdx.x; item < items.total; item += gridDim.x) {
+  for (int64_t item = block; item < items.total; item += blocks) {
     const Keys w(g, items, item, tiles);
     if (!w.any) continue;
     const Sequence& q = w.q;
@@ -234,7 +216,7 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 ? 1 : 2) attn_dkv_ker
     load_rows(fk, g.k.p, row * g.k.row + kv * g.k.head, half, width, mine);
     if (g.scale < 0.0f) negate<DT>(fk);
     load_rows(fv, g.v.p, row * g.v.row + kv * g.v.head, half, width, mine);
-    char* const lv = lvalues + wave * V::BYTES;
+    char* const lv = values;                       // the wave's own
     if constexpr (!KEEP) {
 #pragma unroll
       for (int kk = 0; kk < T::STEPS; ++kk) along.store(lv, kk, fv[kk]);
@@ -391,13 +373,34 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 ? 1 : 2) attn_dkv_ker
   }
 }
 
+// The parts' sums of dq, added in order; a workgroup 32 columns of a tile.
+template <int DT, int D>
+__device__ __forceinline__ void attn_dq_sum(const AttnArgs& g, int tiles, int64_t block, int64_t blocks) {
+  constexpr int BLOCKS = D / 32;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Items items(tiles, g.kv_heads, g.group * BLOCKS);
+  for (int64_t item = block; item < items.total; item += blocks) {
+    const Queries w(g, items, item, tiles, BLOCKS);
+    const int i = w.i0 + wave * 32 + lane % 32;
+    if (!w.any || i >= w.q.lq) continue;
+    f32x16 sum[1];
+    clear(sum);
+    for (int p = 0; p < g.q_parts; ++p)
+      add_part(sum, part_at(g.q_sums, w.unit * g.q_parts + p, BLOCKS * 4) +
+                        w.part * (4 * kAttnThreads), 1.0f);
+    store_columns<DT>(static_cast<char*>(const_cast<void*>(g.dq.p)) +
+                          ((int64_t)w.q.q0 + i) * g.dq.row + w.head * g.dq.head, sum, g.scale,
+                      lane / 32, g.head_dim, w.part);
+  }
+}
+
 // The parts' sums, added in order; a workgroup 32 columns of a tile of dk or dv.
 template <int DT, int D>
-__global__ void __launch_bounds__(kAttnThreads) attn_dkv_sum_kernel(AttnArgs g, int tiles) {
+__device__ __forceinline__ void attn_dkv_sum(const AttnArgs& g, int tiles, int64_t block, int64_t blocks) {
   constexpr int BLOCKS = D / 32;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Items items(tiles, g.kv_heads, 2 * BLOCKS);
-  for (int64_t item = blockIdx.x; item < items.total; item += gridDim.x) {
+  for (int64_t item = block; item < items.total; item += blocks) {
     const Keys w(g, items, item, tiles);
     const int j = w.j0 + wave * 32 + lane % 32;
     if (!w.any || j >= w.q.lk) continue;
@@ -414,20 +417,52 @@ __global__ void __launch_bounds__(kAttnThreads) attn_dkv_sum_kernel(AttnArgs g, 
   }
 }
 
+// Both halves in one launch: neither waits for the other's last workgroups.  The first k_blocks
+// workgroups, whose work is longer, take dk and dv.
+template <int DT, int D, int MODE>
+__global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2)
+    attn_back_kernel(AttnArgs g, int q_tiles, int k_tiles, int k_blocks) {
+  using B = Back<DT, D>;
+  __shared__ __attribute__((aligned(1024))) char l0[B::BYTES];
+  __shared__ __attribute__((aligned(1024))) char l1[B::BYTES];
+  __shared__ __attribute__((aligned(1024))) char l2[B::BYTES];
+  __shared__ __attribute__((aligned(1024))) char l3[B::BYTES];
+  __shared__ __attribute__((aligned(1024))) char li0[1024];  // lse, -D of 64 queries, twice
+  __shared__ __attribute__((aligned(1024))) char li1[1024];
+  __shared__ __attribute__((aligned(1024))) char values[B::APART ? kWaves * B::VALUES : 16];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if ((int)blockIdx.x >= k_blocks) {
+    attn_dq<DT, D, MODE>(g, q_tiles, blockIdx.x - k_blocks, gridDim.x - k_blocks, l0, l1, l2, l3);
+  } else if constexpr (B::KEEP || B::APART) {
+    attn_dkv<DT, D, MODE>(g, k_tiles, blockIdx.x, k_blocks, l0, l1, li0, l2, l3, li1,
+                          values + wave * (B::APART ? B::VALUES : 0));
+  } else {
+    static_assert(2 * B::Q_BYTES <= B::BYTES && 2 * B::VALUES <= B::BYTES, "");
+    attn_dkv<DT, D, MODE>(g, k_tiles, blockIdx.x, k_blocks, l0, l0 + B::Q_BYTES, li0, l1,
+                          l1 + B::Q_BYTES, li1, (wave < 2 ? l2 : l3) + wave % 2 * B::VALUES);
+  }
+}
+
+template <int DT, int D>
+__global__ void __launch_bounds__(kAttnThreads)
+    attn_sum_kernel(AttnArgs g, int q_tiles, int k_tiles, int k_blocks) {
+  if ((int)blockIdx.x >= k_blocks)
+    attn_dq_sum<DT, D>(g, q_tiles, blockIdx.x - k_blocks, gridDim.x - k_blocks);
+  else
+    attn_dkv_sum<DT, D>(g, k_tiles, blockIdx.x, k_blocks);
+}
+
 template <int DT, int D, int MODE>
 lowbit_status launch_back_width(const AttnArgs& a, hipStream_t s) {
   const int qt = attn_tiles(a.q_rows, a.sequences), kt = attn_tiles(a.k_rows, a.sequences);
   const int64_t nk = capped(Items(kt, a.kv_heads, a.k_parts).total);
   const int64_t nq = capped(Items(qt, a.kv_heads, a.group * a.q_parts).total);
-  lowbit_status st = launch(&attn_dkv_kernel<DT, D, MODE>, nk, kAttnThreads, s, a, kt);
-  if (st == LOWBIT_OK && a.k_parts > 1)
-    st = launch(&attn_dkv_sum_kernel<DT, D>, capped(Items(kt, a.kv_heads, 2 * (D / 32)).total),
-                kAttnThreads, s, a, kt);
-  if (st == LOWBIT_OK) st = launch(&attn_dq_kernel<DT, D, MODE>, nq, kAttnThreads, s, a, qt);
-  if (st == LOWBIT_OK && a.q_parts > 1)
-    st = launch(&attn_dq_sum_kernel<DT, D>, capped(Items(qt, a.kv_heads, a.group * (D / 32)).total),
-                kAttnThreads, s, a, qt);
-  return st;
+  const lowbit_status st = launch(&attn_back_kernel<DT, D, MODE>, nk + nq, kAttnThreads, s, a, qt, kt,
+                                  (int)nk);
+  if (st != LOWBIT_OK || (a.k_parts == 1 && a.q_parts == 1)) return st;
+  const int64_t sk = a.k_parts > 1 ? capped(Items(kt, a.kv_heads, 2 * (D / 32)).total) : 0;
+  const int64_t sq = a.q_parts > 1 ? capped(Items(qt, a.kv_heads, a.group * (D / 32)).total) : 0;
+  return launch(&attn_sum_kernel<DT, D>, sk + sq, kAttnThreads, s, a, qt, kt, (int)sk);
 }
 
 template <int DT, int MODE>
