@@ -385,6 +385,7 @@ __device__ __forceinline__ void attn_dq_sum(const AttnArgs& g, int tiles, int64_
     if (!w.any || i >= w.q.lq) continue;
     f32x16 sum[1];
     clear(sum);
+#pragma unroll 4
     for (int p = 0; p < g.q_parts; ++p)
       add_part(sum, part_at(g.q_sums, w.unit * g.q_parts + p, BLOCKS * 4) +
                         w.part * (4 * kAttnThreads), 1.0f);
@@ -406,6 +407,7 @@ __device__ __forceinline__ void attn_dkv_sum(const AttnArgs& g, int tiles, int64
     if (!w.any || j >= w.q.lk) continue;
     f32x16 sum[1];
     clear(sum);
+#pragma unroll 4
     for (int p = 0; p < g.k_parts; ++p)
       add_part(sum, part_at(g.k_sums, w.unit * g.k_parts + p, 2 * BLOCKS * 4) +
                         w.part * (4 * kAttnThreads), 1.0f);
