@@ -7,6 +7,7 @@ namespace {
 
 // lse in the kernels' units (0 where a row sees nothing: every weight is exp(-infinity)
 // then) and -D, D being the sum of dout out: 16 lanes a row of a head, all heads of a row in turn.
+// Bound by memory: 8 Ki x 32 heads of 128 bfloat16 28 us, 4.8 TB/s.
 template <int DT>
 __global__ void __launch_bounds__(256) attn_delta_kernel(AttnArgs g) {
   const int lane = threadIdx.x % 16;

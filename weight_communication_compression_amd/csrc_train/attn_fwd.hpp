@@ -11,6 +11,14 @@ namespace {
 // The scores are taken transposed, keys down the registers and a query a lane,
 // so that the maximum and the sum of a row stay in the lane (and its other half) and
 // the weights are, as they lie, the operand of the product with the values.
+//
+// Bound by the matrix units and the vector ALU together, at the clock that power leaves: two
+// workgroups a CU, two waves a SIMD, one of which takes exps while the other multiplies (32
+// products of 32 cycles and about 260 vector instructions a tile and wave).  8 Ki tokens,
+// causal, 32 / 8 heads of 128 bfloat16: 525 us, 1.05 PFLOP/s of what is visible; matrix units
+// busy 52 % of the time, no bank of LDS met twice.  With the operands read right before their
+// products 577 us.  Capped scores take two exps and a reciprocal each: nine ragged documents of 8 Ki
+// tokens, 16 heads of 64, window 1024, 82 us (tanh of the mathematical library: 129).
 template <int DT, int D, int MODE>
 struct Forward {
   static constexpr int ES = elem_size<DT>(), KT = DT == kF32 ? 32 : 64, NB = KT / 32;

@@ -130,7 +130,9 @@ struct Pairs {
 
 // A lane takes a unit of a row (of pairs, or 16 bytes that are copied) through all heads of
 // its group, so that sines are taken once for them; a group's heads lie `groups` apart.  The
-// first heads are loaded before the sines are taken.
+// first heads are loaded before the sines are taken.  Bound by memory: 16 Ki x 40 heads of 128
+// bfloat16 64 us, 5.2 TB/s; 5003 x 24 heads of 80 binary32, half of each turned, 18 us (with
+// units of eight pairs, whose loads lie 64 bytes apart from lane to lane, 29).
 template <int DT, int LAYOUT>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs g) {
   constexpr int ES = elem_size<DT>(), E = Vec<DT>::E, N = 4;   // N heads under way

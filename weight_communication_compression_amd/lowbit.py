@@ -913,46 +913,53 @@ class AttentionGrads(NamedTuple):
     dv: torch.Tensor
 
 
+def _offset_count(t, device, what):
+    """How many sequences the offsets are of."""
+    if t.dtype != torch.int32 or t.dim() != 1 or t.numel() < 1 or t.device != device:
+        raise LowbitError(EINVAL, f"{what} must be int32 offsets, one more than sequences")
+    return t.numel() - 1
+
+
 def _attention_params(q, k, v, q_begin, k_begin, scale, causal, window, prefix, softcap, slopes):
     """Checks of the tensors' types and sizes, which the C ABI cannot see."""
-    for t, what in ((q, "q"), (k, "k"), (v, "v")):
-        if t.dtype != q.dtype or t.device != q.device:
-            raise LowbitError(EINVAL, "q, k and v must match in dtype and device")
-    if q.dim() not in (3, 4) or k.dim() != q.dim() or k.shape != v.shape:
+    device, dtype, size, k_size = q.device, q.dtype, q.shape, k.shape
+    if k.dtype != dtype or v.dtype != dtype or k.device != device or v.device != device:
+        raise LowbitError(EINVAL, "q, k and v must match in dtype and device")
+    n = len(size)
+    if n not in (3, 4) or len(k_size) != n or k_size != v.shape:
         raise LowbitError(EINVAL, "q, k and v must be (rows, heads, head_dim), or (batch, length, "
                                   "heads, head_dim) for sequences of equal lengths")
-    if q.shape[-1] != k.shape[-1]:
+    d = size[-1]
+    if d != k_size[-1]:
         raise LowbitError(EINVAL, "q, k and v must have one head_dim")
-    if q.shape[-2] < 1 or k.shape[-2] < 1 or q.shape[-2] % k.shape[-2]:
+    if size[-2] < 1 or k_size[-2] < 1 or size[-2] % k_size[-2]:
         raise LowbitError(EINVAL, "k's heads must divide q's")
     sequences = 1
-    if q.dim() == 4:
+    if n == 4:
         if q_begin is not None or k_begin is not None:
             raise LowbitError(EINVAL, "offsets go with (rows, heads, head_dim)")
-        if k.shape[0] != q.shape[0]:
+        if k_size[0] != size[0]:
             raise LowbitError(EINVAL, "q and k must have one batch")
-        sequences = q.shape[0]
-    for t, what in ((q_begin, "q_begin"), (k_begin, "k_begin")):
-        if t is None:
-            continue
-        if t.dtype != torch.int32 or t.dim() != 1 or t.numel() < 1 or t.device != q.device:
-            raise LowbitError(EINVAL, f"{what} must be int32 offsets, one more than sequences")
-        if what == "k_begin" and q_begin is not None and t.numel() != q_begin.numel():
+        sequences = size[0]
+    if q_begin is not None:
+        sequences = _offset_count(q_begin, device, "q_begin")
+    if k_begin is not None:
+        count = _offset_count(k_begin, device, "k_begin")
+        if q_begin is not None and count != sequences:
             raise LowbitError(EINVAL, "q_begin and k_begin must have the same length")
-        sequences = t.numel() - 1
+        sequences = count
     if prefix is not None and (prefix.dtype != torch.int32 or prefix.numel() != sequences
-                               or prefix.device != q.device):
+                               or prefix.device != device):
         raise LowbitError(EINVAL, "prefix must be int32, one for each sequence")
-    if slopes is not None and (slopes.dtype != torch.float32 or slopes.numel() != q.shape[-2]
-                               or slopes.device != q.device):
+    if slopes is not None and (slopes.dtype != torch.float32 or slopes.numel() != size[-2]
+                               or slopes.device != device):
         raise LowbitError(EINVAL, "slopes must be float32, one for each head of q")
     q_rows, q_row, q_head = _heads(q, "q")
     k_rows, k_row, k_head = _heads(k, "k")
     _, v_row, v_head = _heads(v, "v")
-    d = q.shape[-1]
     # (a window beyond 64 bits hides nothing either)
     return AttentionParams(q_rows, k_rows, max(-1, min(int(window), 1 << 40)), sequences,
-                           q.shape[-2], k.shape[-2], d, _dtype_code(q), int(bool(causal)),
+                           size[-2], k_size[-2], d, _dtype_code(q), 1 if causal else 0,
                            d ** -0.5 if scale is None else scale, softcap,
                            q_row, q_head, k_row, k_head, v_row, v_head)
 
@@ -1000,15 +1007,20 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     if q.requires_grad or k.requires_grad or v.requires_grad:
         _outside_autograd("attention")
     p = _attention_params(q, k, v, q_begin, k_begin, scale, causal, window, prefix, softcap, slopes)
-    out = _attention_out(out, q, "out")
-    _, p.out_row, p.out_head = _heads(out, "out")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        p.out_row, p.out_head = p.q_heads * p.head_dim, p.head_dim
+    else:
+        _attention_out(out, q, "out")
+        _, p.out_row, p.out_head = _heads(out, "out")
     lse = torch.empty(p.q_heads, p.q_rows, dtype=torch.float32, device=q.device)
     L = lib()
     ws, nbytes = _attention_scratch(L, p, 0, q, workspace, "attention")
-    _check(L.lowbit_attention(_gpu(q, "q"), _gpu(k, "k"), _gpu(v, "v"),
+    # (all are on q's device)
+    _check(L.lowbit_attention(_gpu(q, "q"), k.data_ptr(), v.data_ptr(),
                               _opt(q_begin, "q_begin"), _opt(k_begin, "k_begin"),
                               _opt(prefix, "prefix"), _opt(slopes, "slopes"), p,
-                              _gpu(out, "out"), lse.data_ptr(), ws, nbytes, _stream(q)),
+                              out.data_ptr(), lse.data_ptr(), ws, nbytes, _stream(q)),
            "lowbit_attention")
     return Attention(out, lse)
 
