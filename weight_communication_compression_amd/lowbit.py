@@ -977,11 +977,18 @@ def _attention_scratch(L, p, backward, like, workspace, what):
 
 
 def _attention_out(t, like, what):
-    if t is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
     if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
         raise LowbitError(EINVAL, f"{what} must match in shape, dtype and device")
-    return t
+
+
+def _attention_grad(t, like, what):
+    """The gradient's tensor and its steps."""
+    if t is None:
+        size = like.shape
+        return torch.empty(size, dtype=like.dtype, device=like.device), size[-2] * size[-1], size[-1]
+    _attention_out(t, like, what)
+    _, row, head = _heads(t, what)
+    return t, row, head
 
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -1042,20 +1049,18 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
         _attention_out(t, q, what)
     if lse.dtype != torch.float32 or lse.numel() != p.q_heads * p.q_rows or lse.device != q.device:
         raise LowbitError(EINVAL, "lse must be the forward call's")
-    dq, dk, dv = (_attention_out(dq, q, "dq"), _attention_out(dk, k, "dk"),
-                  _attention_out(dv, v, "dv"))
     _, p.out_row, p.out_head = _heads(out, "out")
     _, p.dout_row, p.dout_head = _heads(dout, "dout")
-    _, p.dq_row, p.dq_head = _heads(dq, "dq")
-    _, p.dk_row, p.dk_head = _heads(dk, "dk")
-    _, p.dv_row, p.dv_head = _heads(dv, "dv")
+    dq, p.dq_row, p.dq_head = _attention_grad(dq, q, "dq")
+    dk, p.dk_row, p.dk_head = _attention_grad(dk, k, "dk")
+    dv, p.dv_row, p.dv_head = _attention_grad(dv, v, "dv")
     L = lib()
     ws, nbytes = _attention_scratch(L, p, 1, q, workspace, "attention_backward")
     _check(L.lowbit_attention_backward(
-        _gpu(dout, "dout"), _gpu(q, "q"), _gpu(k, "k"), _gpu(v, "v"), _gpu(out, "out"),
+        dout.data_ptr(), _gpu(q, "q"), k.data_ptr(), v.data_ptr(), out.data_ptr(),
         _dev(lse, "lse"), _opt(q_begin, "q_begin"), _opt(k_begin, "k_begin"),
-        _opt(prefix, "prefix"), _opt(slopes, "slopes"), p, _gpu(dq, "dq"), _gpu(dk, "dk"),
-        _gpu(dv, "dv"), ws, nbytes, _stream(q)), "lowbit_attention_backward")
+        _opt(prefix, "prefix"), _opt(slopes, "slopes"), p, dq.data_ptr(), dk.data_ptr(),
+        dv.data_ptr(), ws, nbytes, _stream(q)), "lowbit_attention_backward")
     return AttentionGrads(dq, dk, dv)
 
 
