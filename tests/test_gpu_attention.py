@@ -262,6 +262,23 @@ def test_equal_bits_streams_and_graphs():
         assert all(torch.equal(a, b) for a, b in zip(grads, kept_grads))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("how", [dict(softcap=1e-39), dict(softcap=1e-39, scale=1e30), dict(scale=3e38)])
+def test_factors_beyond_binary32(how, dtype):
+    """Sums of products that are 0 have scores of 0 whatever they are multiplied by."""
+    _, k, v = inputs([70], [70], 2, 1, 64, dtype, False, 10)
+    q = torch.zeros(70, 2, 64, dtype=dtype, device="cuda")
+    got = L.attention(q, k, v, causal=False, **how)
+    ones = L.attention(q, k, v, causal=False)
+    assert torch.equal(got.out, ones.out) and torch.equal(got.lse, ones.lse)
+    dout = torch.ones_like(q)
+    back = L.attention_backward(dout, q, k, v, got.out, got.lse, causal=False, **how)
+    # every score's weight is 1 / 70, of the sum of whose roundings, half a step of dtype and a
+    # few of binary32 each, there are 2 x 70
+    want = 2.0
+    assert (back.dv.double() - want).abs().max() <= want * (torch.finfo(dtype).eps + 1e-5)
+
+
 def test_nothing_to_do():
     e = torch.empty(0, 2, 64, device="cuda")
     assert L.attention(e, e, e).out.shape == (0, 2, 64)

@@ -263,6 +263,7 @@ struct Score {
     factor = !has_cap(MODE) ? fmaxf(scale * unit, 0x1p-100f)
              : DT == kF32   ? scale / g.softcap
                             : scale / g.softcap * (2.0f * kLog2e);
+    factor = fminf(factor, 0x1.fffffep127f);       // (infinity times a sum of 0 would be NaN)
     slope = 0.0f;
   }
   __device__ __forceinline__ void head(const AttnArgs& g, int h) {
