@@ -319,6 +319,9 @@ lowbit_status lowbit_attention(const void* q, const void* k, const void* v,
  * gradient here.  A key that no query sees has dk = dv = 0; rows outside all sequences are left as they
  * were.  For LOWBIT_BF16 the weights and g enter their products rounded to
  * bfloat16, as in the forward call.
+ * Equal calls give equal bits.  Where sums are cut into parts follows from the buffers'
+ * sizes, not from the offsets: the same rows within larger buffers may differ by the rounding of
+ * binary32 additions in another order (so also of the forward call).
  */
 lowbit_status lowbit_attention_backward(const void* dout, const void* q, const void* k,
                                         const void* v, const void* out, const float* lse,
