@@ -31,6 +31,7 @@ static_assert(kRowsPerTile == 32 * kWaves, "");
 // is made good so that results keep binary32's accuracy.
 template <int DT>
 __host__ __device__ constexpr float unit_of() { return DT == kF32 ? 1.0f : kLog2e; }
+// Of binary32 arguments up to 80: beyond, an infinity times a correction of 0 or less would be NaN.
 template <int DT>
 __device__ __forceinline__ float exp_unit(float x) {
   if constexpr (DT == kBF16) return __builtin_amdgcn_exp2f(x);
@@ -281,8 +282,9 @@ struct Score {
       s = __builtin_fmaf(z, s, 1.33333333e-1f);
       s = __builtin_fmaf(z, s, -3.33333333e-1f);
       s = __builtin_fmaf(x * z, s, x);
-      const float e = exp_unit<kF32>(2.0f * fabsf(x));
-      const float l = copysignf(__builtin_fmaf(-2.0f, __builtin_amdgcn_rcpf(e + 1.0f), 1.0f), x);
+      // elsewhere 1 - 2 e / (1 + e) of e = exp(-2 |x|), which falls to 0 for the largest ones
+      const float e = exp_unit<kF32>(-2.0f * fabsf(x));
+      const float l = copysignf(__builtin_fmaf(-2.0f * e, __builtin_amdgcn_rcpf(1.0f + e), 1.0f), x);
       const float t = fabsf(x) < 0.4f ? s : l;
       bend = __builtin_fmaf(-t, t, 1.0f);
       return cap * t;
