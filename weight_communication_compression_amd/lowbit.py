@@ -965,15 +965,15 @@ def _attention_params(q, k, v, q_begin, k_begin, scale, causal, window, prefix, 
 
 
 def _attention_scratch(L, p, backward, like, workspace, what):
-    """The workspace's pointer (torch frees the tensor for work that comes after the call's on
-    its stream) and size."""
+    """The workspace, which the caller holds until its kernels are enqueued (torch then keeps the
+    memory for what comes behind them on the stream), its pointer and size."""
     nbytes = L.lowbit_attention_workspace(p, backward)
     if nbytes < 0 and p.head_dim % 8 == 0 and p.head_dim > 128:
         raise LowbitError(EUNSUPPORTED, f"{what}: head_dim above 128")
     if nbytes == 0 and workspace is None:
-        return None, 0
+        return None, None, 0
     ws = _scratch(nbytes, like, workspace, what)
-    return _dev(ws, "workspace"), ws.numel()
+    return ws, _dev(ws, "workspace"), ws.numel()
 
 
 def _attention_out(t, like, what):
@@ -1022,12 +1022,12 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         _, p.out_row, p.out_head = _heads(out, "out")
     lse = torch.empty(p.q_heads, p.q_rows, dtype=torch.float32, device=q.device)
     L = lib()
-    ws, nbytes = _attention_scratch(L, p, 0, q, workspace, "attention")
+    ws, at, nbytes = _attention_scratch(L, p, 0, q, workspace, "attention")
     # (all are on q's device)
     _check(L.lowbit_attention(_gpu(q, "q"), k.data_ptr(), v.data_ptr(),
                               _opt(q_begin, "q_begin"), _opt(k_begin, "k_begin"),
                               _opt(prefix, "prefix"), _opt(slopes, "slopes"), p,
-                              out.data_ptr(), lse.data_ptr(), ws, nbytes, _stream(q)),
+                              out.data_ptr(), lse.data_ptr(), at, nbytes, _stream(q)),
            "lowbit_attention")
     return Attention(out, lse)
 
@@ -1055,12 +1055,12 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     dk, p.dk_row, p.dk_head = _attention_grad(dk, k, "dk")
     dv, p.dv_row, p.dv_head = _attention_grad(dv, v, "dv")
     L = lib()
-    ws, nbytes = _attention_scratch(L, p, 1, q, workspace, "attention_backward")
+    ws, at, nbytes = _attention_scratch(L, p, 1, q, workspace, "attention_backward")
     _check(L.lowbit_attention_backward(
         dout.data_ptr(), _gpu(q, "q"), k.data_ptr(), v.data_ptr(), out.data_ptr(),
         _dev(lse, "lse"), _opt(q_begin, "q_begin"), _opt(k_begin, "k_begin"),
         _opt(prefix, "prefix"), _opt(slopes, "slopes"), p, dq.data_ptr(), dk.data_ptr(),
-        dv.data_ptr(), ws, nbytes, _stream(q)), "lowbit_attention_backward")
+        dv.data_ptr(), at, nbytes, _stream(q)), "lowbit_attention_backward")
     return AttentionGrads(dq, dk, dv)
 
 
