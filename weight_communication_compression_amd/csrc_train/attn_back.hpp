@@ -480,7 +480,8 @@ lowbit_status launch_back_mode(const AttnArgs& a, hipStream_t s) {
 
 template <int DT>
 lowbit_status launch_attn_back(const AttnArgs& a, hipStream_t s) {
-  switch (score_mode(a)) {
+  switch (score_mode<DT>(a)) {
+    case kWideCapScore: return launch_back_mode<DT, DT == kBF16 ? kWideCapScore : kCapScore>(a, s);
     case kPlainScore: return launch_back_mode<DT, kPlainScore>(a, s);
     case kBiasScore: return launch_back_mode<DT, kBiasScore>(a, s);
     case kCapScore: return launch_back_mode<DT, kCapScore>(a, s);

@@ -239,9 +239,11 @@ template <int DT, int D>
 lowbit_status launch_attn_width(const AttnArgs& a, hipStream_t s) {
   const int tiles = attn_tiles(a.q_rows, a.sequences);
   const int64_t blocks = capped(Items(tiles, a.kv_heads, a.group * a.q_parts).total);
-  const int mode = score_mode(a);
+  const int mode = score_mode<DT>(a);
   const lowbit_status st =
-      mode == kPlainScore  ? launch(&attn_kernel<DT, D, kPlainScore>, blocks, kAttnThreads, s, a, tiles)
+      DT == kBF16 && mode == kWideCapScore
+          ? launch(&attn_kernel<DT, D, DT == kBF16 ? kWideCapScore : kPlainScore>, blocks, kAttnThreads, s, a, tiles)
+      : mode == kPlainScore  ? launch(&attn_kernel<DT, D, kPlainScore>, blocks, kAttnThreads, s, a, tiles)
       : mode == kBiasScore ? launch(&attn_kernel<DT, D, kBiasScore>, blocks, kAttnThreads, s, a, tiles)
       : mode == kCapScore  ? launch(&attn_kernel<DT, D, kCapScore>, blocks, kAttnThreads, s, a, tiles)
                            : launch(&attn_kernel<DT, D, kCapBiasScore>, blocks, kAttnThreads, s, a, tiles);
