@@ -792,6 +792,12 @@ def linear_xent_backward(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
     return LinearXentGrads(dx, dw)
 
 
+def _at_most(n, most: int) -> int:
+    """n for a field of the C ABI, which would keep the low bits of what does not fit: larger ones
+    as `most`, negative ones as -1."""
+    return max(-1, min(int(n), most))
+
+
 _SCALINGS = {None: 0, "linear": 1, "base": 2, "parts": 3}
 _LAYOUTS = {"half": 0, "interleaved": 1}
 
@@ -813,7 +819,7 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[st
     freqs = torch.empty(rot_dim // 2, dtype=torch.float64)
     scale = ctypes.c_float()
     _check(lib().lowbit_rotary_frequencies(int(rot_dim), base, _SCALINGS[scaling], factor,
-                                           int(original_length), slow_turns, fast_turns,
+                                           _at_most(original_length, 2 ** 63 - 1), slow_turns, fast_turns,
                                            freqs.data_ptr(), ctypes.byref(scale)),
            "lowbit_rotary_frequencies")
     return freqs, scale.value
@@ -866,7 +872,7 @@ def _rotary(fn, name, x, freqs, positions, rows_per_sequence, layout, scale, out
         if out.shape != x.shape or out.dtype != x.dtype or out.device != device:
             raise LowbitError(EINVAL, "out must match the input in shape, dtype and device")
         _, y_row, y_head = _heads(out, "out")
-    p = RotaryParams(rows, int(rows_per_sequence) or max(rows, 1), x_row, x_head, y_row, y_head,
+    p = RotaryParams(rows, _at_most(rows_per_sequence, max(rows, 1)) or max(rows, 1), x_row, x_head, y_row, y_head,
                      x.shape[-2], x.shape[-1], 2 * freqs.numel(), _LAYOUTS[layout],
                      _dtype_code(x), scale)
     _check(fn(_gpu(x, what), _dev(freqs, "freqs"),
@@ -958,7 +964,7 @@ def _attention_params(q, k, v, q_begin, k_begin, scale, causal, window, prefix, 
     k_rows, k_row, k_head = _heads(k, "k")
     _, v_row, v_head = _heads(v, "v")
     # (a window beyond 64 bits hides nothing either)
-    return AttentionParams(q_rows, k_rows, max(-1, min(int(window), 1 << 40)), sequences,
+    return AttentionParams(q_rows, k_rows, _at_most(window, 1 << 40), sequences,
                            size[-2], k_size[-2], d, _dtype_code(q), 1 if causal else 0,
                            d ** -0.5 if scale is None else scale, softcap,
                            q_row, q_head, k_row, k_head, v_row, v_head)
@@ -1081,7 +1087,7 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750
     a, b, c = coefficients
     rows, cols = g.shape[-2:]
     p = OrthogonalizeParams(g.numel() // (rows * cols) if rows and cols else 0, max(rows, 1),
-                            max(cols, 1), _dtype_code(g), int(steps), a, b, c, eps, scale)
+                            max(cols, 1), _dtype_code(g), _at_most(steps, 65), a, b, c, eps, scale)
     if out is None:
         out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
     elif out.dtype != torch.bfloat16 or out.shape != g.shape or out.device != g.device:
