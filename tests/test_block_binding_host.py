@@ -1,5 +1,5 @@
 """What the bindings of rotary, attention and orthogonalize make of numbers that do not fit the C
-ABI's fields (no GPU needed: a stand-in for the library looks)."""
+ABI's fields, and of heads without elements (no GPU needed: a stand-in for the library looks)."""
 import pytest
 import torch
 
@@ -69,3 +69,11 @@ def test_an_original_length_beyond_64_bits_is_a_long_one():
     assert torch.equal(far, plain)                    # every pair turns often enough: none is divided
     with pytest.raises(L.LowbitError):
         L.rotary_frequencies(8, scaling="parts", factor=4.0, original_length=-2 ** 64 + 5)
+
+
+def test_heads_without_elements_are_refused():
+    e = torch.zeros(3, 2, 0)
+    for call in (lambda: L.attention(e, e, e), lambda: L.attention(e, e, e, scale=1.0),
+                 lambda: L.attention_backward(e, e, e, e, e, torch.zeros(2, 3))):
+        with pytest.raises(L.LowbitError):
+            call()

@@ -936,8 +936,8 @@ def _attention_params(q, k, v, q_begin, k_begin, scale, causal, window, prefix, 
         raise LowbitError(EINVAL, "q, k and v must be (rows, heads, head_dim), or (batch, length, "
                                   "heads, head_dim) for sequences of equal lengths")
     d = size[-1]
-    if d != k_size[-1]:
-        raise LowbitError(EINVAL, "q, k and v must have one head_dim")
+    if d != k_size[-1] or d < 1:
+        raise LowbitError(EINVAL, "q, k and v must have one head_dim, a multiple of 8 up to 128")
     if size[-2] < 1 or k_size[-2] < 1 or size[-2] % k_size[-2]:
         raise LowbitError(EINVAL, "k's heads must divide q's")
     sequences = 1
