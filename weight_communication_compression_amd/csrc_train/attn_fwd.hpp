@@ -19,7 +19,7 @@ namespace {
 // busy 52 % of the time, no bank of LDS met twice.  With the operands read right before their
 // products 577 us.  Capped scores take two exps and a reciprocal each: nine ragged documents of 8 Ki
 // tokens, 16 heads of 64, window 1024, 82 us (tanh of the mathematical library: 129).
-template <int DT, int D, int MODE>
+template <int DT, int D>
 struct Forward {
   static constexpr int ES = elem_size<DT>(), KT = DT == kF32 ? 32 : 64, NB = KT / 32;
   using T = Tile<DT, D, KT>;
@@ -42,7 +42,7 @@ __device__ __forceinline__ void finish_rows(const AttnArgs& g, const f32x16 (&ac
 
 template <int DT, int D, int MODE>
 __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) attn_kernel(AttnArgs g, int tiles) {
-  using F = Forward<DT, D, MODE>;
+  using F = Forward<DT, D>;
   using T = typename F::T;
   constexpr int KT = F::KT, NB = F::NB, ES = F::ES;
   __shared__ __attribute__((aligned(1024))) char lk0[T::BYTES];

@@ -70,8 +70,8 @@ struct OrthoArgs {
   void* out;
   double* parts;             // batch x kOrthoParts
   float* x;                  // batch x m x ldn
-  void *xh, *xh_next;        // X in binary16, times kOrthoX
-  void *ah, *bh;             // A and b A + c A A in binary16, times kOrthoA and kOrthoB
+  void *xh, *xh_next;        // X in binary16, times a power of two (kX of ortho.hip)
+  void *ah, *bh;             // A and b A + c A A in binary16, times others (kA, kB)
   float* partial;            // sums of parts of tiles that are cut along k
   int32_t k_parts;           // of the product that is launched
   int64_t batch;

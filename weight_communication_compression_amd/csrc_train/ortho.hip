@@ -283,15 +283,14 @@ __global__ void __launch_bounds__(F::THREADS, F::PER_CU * F::W / 4) ortho_tile_k
   constexpr int TM = F::TM, TN = F::TN, W = F::W, I = F::I, J = F::J, S = F::STAGES;
   constexpr bool BO = !kMirrored<KIND>;
   constexpr int K = kRowBytes / 2;
-  constexpr bool OWN_SIDE = F::STAGE < W * 4096;
+  static_assert(F::STAGE >= W * 4096, "");           // (finish_block goes through the first stage)
   __shared__ __attribute__((aligned(1024))) char l0[F::STAGE];
   __shared__ __attribute__((aligned(1024))) char l1[F::STAGE];
   __shared__ __attribute__((aligned(1024))) char l2[S > 2 ? F::STAGE : 16];
   __shared__ __attribute__((aligned(1024))) char l3[S > 3 ? F::STAGE : 16];
-  __shared__ __attribute__((aligned(1024))) char own_side[OWN_SIDE ? W * 4096 : 16];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / F::WN, wn = wave % F::WN;
-  char* const side = (OWN_SIDE ? own_side : l0) + wave * 4096;
+  char* const side = l0 + wave * 4096;
   const int k = KIND == kGram ? g.n : g.m, n = kMirrored<KIND> ? g.m : g.n;
   const int lda = KIND == kGram ? g.ldn : g.ldm, ldb = KIND == kPoly ? g.ldm : g.ldn;
   const int across = (n + TN - 1) / TN, down = (g.m + TM - 1) / TM;
