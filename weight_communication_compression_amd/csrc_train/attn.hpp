@@ -4,6 +4,7 @@
 #pragma once
 
 #include "block.hpp"
+#include "matrix_unit.hpp"
 #include "train_device.hpp"
 #include "../csrc/launch.hpp"
 
@@ -11,14 +12,6 @@ namespace lowbit {
 
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-#define LOWBIT_LDS __attribute__((address_space(3)))
-
-constexpr uint32_t kNowhere = 0x7FFFFFF0u;   // beyond every buffer's records
 constexpr float kLog2e = 1.44269502f;        // log2(e) to binary32
 constexpr float kLn2 = 0.693147182f;
 
@@ -49,18 +42,6 @@ __device__ __forceinline__ float other_half_max(float v) {
 __device__ __forceinline__ float both_halves_sum(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-
-__device__ __forceinline__ void barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
-// All that the wave has loaded, stored or read in LDS is done.
-__device__ __forceinline__ void wait_all() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
 }
 
 // N products whose operands come from LDS: load(i) reads the i-th's, use(i, operands)
@@ -96,24 +77,6 @@ struct Three {
   u32x4 a, b, c;
 };
 
-// d[row of first][column of second] += sum over 32 bytes of k.  Lane l gives row (column)
-// l mod 32 and the (l / 32)-th 16 bytes, and holds of the result column l mod 32
-// and rows 8 (r / 4) + 4 (l / 32) + r mod 4.  For binary32 four instructions take
-// one element of each lane: k in another order, the same for both.
-template <int DT>
-__device__ __forceinline__ f32x16 mma(const u32x4& first, const u32x4& second, f32x16 c) {
-  if constexpr (DT == kBF16) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, first),
-                                                   __builtin_bit_cast(bf16x8, second), c, 0, 0, 0);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(first[j]),
-                                               __uint_as_float(second[j]), c, 0, 0, 0);
-    return c;
-  }
-}
-
 // Of 32 results in rows, those that make one operand along the rows: chunk c's.  The order of
 // k that this gives is that of Tile::column.
 template <int DT>
@@ -128,15 +91,6 @@ __device__ __forceinline__ u32x4 pack_chunk(const f32x16& v, int c) {
 }
 template <int DT>
 __host__ __device__ constexpr int chunks() { return DT == kF32 ? 4 : 2; }   // of 32 rows
-
-// The memory from p on, `records` bytes of it; what lies behind reads as 0.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t open(const void* p, int records) {
-  const uint64_t at = (uint64_t)p;                 // (uniform, but not for the compiler)
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
-  return __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)hi << 32 | lo), 0,
-                                           __builtin_amdgcn_readfirstlane(records), 0x00020000);
-}
 
 // 16 bytes a lane to LDS, in lane order.  (A function of its own: called within a member of
 // a nested class template, this builtin makes the compiler drop host stubs of the kernels.)

@@ -259,7 +259,7 @@ struct Shape {
 // All loads but the last N are done, and all that the wave has read in LDS.
 template <int N>
 __device__ __forceinline__ void wait_loads_but() {
-  if constexpr (N == 0) wait_loads();
+  if constexpr (N == 0) wait_all();
   else {
     static_assert(N < 64, "");
     __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 7 << 4 | 0 << 8);
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(F::THREADS, F::PER_CU * F::W / 4) ortho_tile_k
     if constexpr (S > 3) {
       if (s + 2 < s1) step(l2, l3, s + 2);
     }
-    wait_loads();
+    wait_all();
     barrier();                                     // (nobody reads the buffers any more)
     if (g.k_parts > 1) {
       f32x4* const to = part_of<F>(g.partial, which * g.k_parts + part);
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(256) ortho_short_kernel(OrthoArgs g) {
       fa.next();
       fx.next();
     }
-    wait_loads();
+    wait_all();
     barrier();
     f32x16 acc[I][I];
 #pragma unroll

@@ -3,6 +3,7 @@
 // order of these for the compiler.
 #pragma once
 
+#include "matrix_unit.hpp"
 #include "train_device.hpp"
 #include "xent_cut.hpp"
 
@@ -10,17 +11,9 @@ namespace lowbit {
 
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2_2 __attribute__((ext_vector_type(2), aligned(2)));
-#define LOWBIT_LDS __attribute__((address_space(3)))
 
-constexpr int kF16 = 2;                    // beside kF32 and kBF16: operands of orthogonalize
 constexpr int kRowBytes = kXentRowBytes;   // of k, between two barriers
-constexpr uint32_t kNowhere = 0x7FFFFFF0u; // beyond every buffer's records
 
 // One operand's way into LDS: T rows of the tile by 128 bytes of k, 16 bytes a
 // lane straight from memory, the W waves taking turns.  OUTER: k is the
@@ -71,11 +64,7 @@ struct Feed {
   // The matrix from here on, for the loads of one step (none if !any).
   __device__ __forceinline__ __amdgpu_buffer_rsrc_t open(bool any) const {
     const int records = (int)(left < 0 || !any ? 0 : left > kNowhere ? kNowhere : left);
-    const uint64_t at = (uint64_t)base;            // (uniform, but not for the compiler)
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
-    return __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)hi << 32 | lo), 0,
-                                             __builtin_amdgcn_readfirstlane(records), 0x00020000);
+    return lowbit::open(base, records);
   }
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, char* lds, int wave, int kleft,
                                        int j) const {
@@ -133,26 +122,6 @@ struct Frag {
   }
 };
 
-// The product of 32 rows of n with 32 rows of m over 32 bytes of k.  For
-// binary32 four products take one element of each lane: k in another order, the
-// same for both.
-template <int DT>
-__device__ __forceinline__ f32x16 mma(const u32x4& b, const u32x4& a, f32x16 c) {
-  if constexpr (DT == kF16) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, b),
-                                                  __builtin_bit_cast(f16x8, a), c, 0, 0, 0);
-  } else if constexpr (DT == kBF16) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b),
-                                                   __builtin_bit_cast(bf16x8, a), c, 0, 0, 0);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(b[j]), __uint_as_float(a[j]), c, 0,
-                                               0, 0);
-    return c;
-  }
-}
-
 template <int DT_, int TM_, int TN_, int WM_, int WN_, int SLOTS_>
 struct Form {
   static constexpr int DT = DT_, TM = TM_, TN = TN_, WM = WM_, WN = WN_, SLOTS = SLOTS_;
@@ -163,17 +132,6 @@ __device__ __forceinline__ f32x4 quad(const f32x16& v, int q) {
   return (f32x4){v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
 }
 
-__device__ __forceinline__ void barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
-// All that the wave has loaded, stored or read in LDS is done.
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // Order for the compiler: R reads of LDS, spread over M products.

@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(F::THREADS, F::SLOTS * F::W / 1024) xent_tile_
     mul(1);
     read(1, la, lb, 3);
     mul(0);
-    wait_loads();
+    wait_all();
     barrier();
     read(0, na, nb, 0);
 #pragma unroll
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(F::THREADS, F::SLOTS * F::W / 1024) xent_tile_
             for (int r = 0; r < 4; ++r) acc[i][j][4 * q + r] = v[r];
           }
     }
-    wait_loads();
+    wait_all();
     barrier();
     read(0, la0, lb0, 0);
     __builtin_amdgcn_sched_barrier(0);
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(F::THREADS, F::SLOTS * F::W / 1024) xent_tile_
       step(la1, lb1, la0, lb0, s + 1);
     }
     if (s < s1) step(la0, lb0, la1, lb1, s);
-    wait_loads();
+    wait_all();
     barrier();                                     // nobody reads la0 .. lb1 any more
 
     const int64_t m0 = (int64_t)tm * TM, n0 = (int64_t)tn * TN;
