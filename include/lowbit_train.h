@@ -298,10 +298,9 @@ int64_t lowbit_attention_workspace(const lowbit_attention_params* p, int32_t bac
  *   slopes : q_heads binary32, device, or NULL: 0 for all
  * Rows' strides are multiples of 8 elements from head_dim up to 2^22, heads' strides
  * multiples of 8; two elements of an output share no place.
- * Scores, statistics and sums are binary32; for LOWBIT_BF16 a score under a softcap up to
- * 512 is off by up to 2^-21 softcap, under larger ones as without it.  For LOWBIT_BF16 the
- * weights exp(y - m) (m near the largest so far) enter the product with v rounded to bfloat16,
- * off by up to 2^-8 each, relative.  NaN and infinities of a key or value that a query does not
+ * Scores, statistics and sums are binary32 (of LOWBIT_BF16, scores beyond half their softcap
+ * are off by up to 2^-20, relative).  For LOWBIT_BF16 the weights exp(y - m) (m near the largest
+ * so far) enter the product with v rounded to bfloat16, off by up to 2^-8 each, relative.  NaN and infinities of a key or value that a query does not
  * see reach it only within its own sequence.
  * EINVAL: p == NULL, a size, type, option or stride outside its range, NULL or
  * misaligned pointer with rows and sequences > 0, workspace too small.  EUNSUPPORTED: head_dim above 128.

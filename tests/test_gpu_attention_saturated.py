@@ -100,6 +100,23 @@ def test_factor_beyond_binary32_of_sums_that_are_not_0(dtype):
 
 
 @BOTH
+def test_a_row_beyond_the_cap_changes_no_other(dtype):
+    """Waves in which a score comes near the cap take all of theirs another way: to the same bits."""
+    q, k, v = inputs([100], [100], 2, 1, 64, dtype, False, 15)
+    how = dict(softcap=30.0)
+    want = L.attention(q, k, v, **how)
+    dout = torch.randn(q.shape, generator=torch.Generator().manual_seed(1)).to(dtype).cuda()
+    grads = L.attention_backward(dout, q, k, v, want.out, want.lse, **how)
+    rest = [i for i in range(100) if i != 37]
+    q[37] *= 200
+    got = L.attention(q, k, v, **how)
+    assert torch.equal(got.out[rest], want.out[rest]) and torch.equal(got.lse[:, rest], want.lse[:, rest])
+    again = L.attention_backward(dout, q, k, v, got.out, got.lse, **how)
+    assert torch.equal(again.dq[rest], grads.dq[rest])
+    assert not torch.equal(got.out[37], want.out[37])
+
+
+@BOTH
 def test_nan_stays_nan(dtype):
     q, k, v = inputs([40], [40], 2, 1, 64, dtype, False, 14)
     q[7] = math.nan

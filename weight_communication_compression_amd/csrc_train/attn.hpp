@@ -195,19 +195,9 @@ struct Tile {
   };
 };
 
-// Which scores a kernel is built for: plain ones, ones with a distance bias, capped ones, both; of
-// bfloat16 ones under a cap beyond kWideCap, with or without a bias, in full accuracy (Score::capped).
-enum ScoreMode : int {
-  kPlainScore = 0, kBiasScore = 1, kCapScore = 2, kCapBiasScore = 3, kWideCapScore = 5
-};
-// Up to kWideCap a capped score's error, softcap 2^-21, is at most a sixteenth of the 2^-8 that rounding
-// the weights to bfloat16 leaves.  The accurate form takes about twice the vector instructions: 4096
-// tokens, causal, 16 / 4 heads of 128, 224 us against 126, gradient 549 against 356; nine ragged
-// documents of 8 Ki tokens, 16 heads of 64, window 1024, 146 against 82.
-constexpr float kWideCap = 512.0f;
-template <int DT>
+// Which scores a kernel is built for: plain ones, ones with a distance bias, capped ones, both.
+enum ScoreMode : int { kPlainScore = 0, kBiasScore = 1, kCapScore = 2, kCapBiasScore = 3 };
 inline int score_mode(const AttnArgs& a) {
-  if (DT == kBF16 && a.softcap > kWideCap) return kWideCapScore;
   return a.softcap > 0.0f ? a.slopes ? kCapBiasScore : kCapScore
                           : a.slopes ? kBiasScore : kPlainScore;
 }
@@ -220,80 +210,111 @@ constexpr bool has_bias(int mode) { return mode % 2 == 1; }
 // into the sign of the operand that is held in registers.
 template <int DT, int MODE>
 struct Score {
-  static constexpr bool FULL = DT == kF32 || MODE == kWideCapScore;
-  float factor, cap, slope, straight;
+  float factor, cap, uncap, slope, straight;
   __device__ __forceinline__ explicit Score(const AttnArgs& g) {
     const float unit = unit_of<DT>(), scale = fabsf(g.scale);
-    cap = g.softcap * unit;
+    // (a cap below 2^-100 as that: beside it no score is anything but 0)
+    const float softcap = fmaxf(g.softcap, 0x1p-100f);
+    cap = softcap * unit;
+    uncap = 1.0f / cap;
     // (a scale of 0 as 2^-100: -infinity times it has to stay what it is)
-    factor = !has_cap(MODE) ? fmaxf(scale * unit, 0x1p-100f)
-             : FULL         ? scale / g.softcap
-                            : scale / g.softcap * (2.0f * kLog2e);
+    factor = has_cap(MODE) ? scale / softcap : fmaxf(scale * unit, 0x1p-100f);
     factor = fminf(factor, 0x1.fffffep127f);       // (infinity times a sum of 0 would be NaN)
     straight = fminf(scale * unit, 0x1.fffffep127f);
     slope = 0.0f;
   }
   __device__ __forceinline__ void head(const AttnArgs& g, int h) {
-    if (MODE == kWideCapScore && !g.slopes) return;
     if (has_bias(MODE)) slope = g.slopes[h] * unit_of<DT>();
   }
-  // The capped score of a sum, and the gradient's factor 1 - tanh^2.
-  __device__ __forceinline__ float capped(float x, float& bend) const {
-    const float plain = x * straight;
-    x *= factor;
-    if constexpr (FULL) {
-      // tanh(x) / x by its series where x is small, times the score without a cap: it keeps its
-      // relative accuracy under any cap
-      const float z = x * x;
-      float s = __builtin_fmaf(z, 3.59212803e-3f, -8.86323552e-3f);
-      s = __builtin_fmaf(z, s, 2.18694885e-2f);
-      s = __builtin_fmaf(z, s, -5.39682540e-2f);
-      s = __builtin_fmaf(z, s, 1.33333333e-1f);
-      s = __builtin_fmaf(z, s, -3.33333333e-1f);
-      s = __builtin_fmaf(z, s, 1.0f);
-      // elsewhere 1 - 2 e / (1 + e) of e = exp(-2 |x|), which falls to 0 for the largest ones
-      const float e = exp_unit<kF32>(-2.0f * fabsf(x));
-      const float l = copysignf(__builtin_fmaf(-2.0f * e, __builtin_amdgcn_rcpf(1.0f + e), 1.0f), x);
-      const bool small = fabsf(x) < 0.4f;
-      const float t = small ? x * s : l;
-      bend = __builtin_fmaf(-t, t, 1.0f);
-      return small ? plain * s : cap * l;
+  // Capped scores of N sums, in their place.  Where a sum is small beside the cap, tanh(x) / x by a
+  // series times the score without a cap, which keeps its relative accuracy under any cap; elsewhere,
+  // of bfloat16, by an exp and a reciprocal, off by less than 2^-20, relative.  A wave whose sums are
+  // all below kFlat skips these two, which run at a quarter of the rate (nine ragged documents of 8 Ki
+  // tokens, 16 heads of 64, window 1024: 74 us, gradient 202; 100 and 243 where no wave can).  Both ways
+  // give a score the same bits.
+  static constexpr float kFlat = 0.5f;
+  template <int N>
+  __device__ __forceinline__ void cap_all(f32x16 (&x)[N]) const {
+    if constexpr (DT == kF32) {
+#pragma unroll
+      for (int b = 0; b < N; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[b][r] = capped(x[b][r]);
     } else {
-      // r = (1 - tanh) / 2 = 1 / (exp(2 x) + 1): its exp, sum and reciprocal leave it off by less than
-      // 2^-22 where it is 1/2, and the score by less than softcap 2^-21
-      const float r = __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x) + 1.0f);
-      bend = 4.0f * __builtin_fmaf(-r, r, r);
-      return __builtin_fmaf(-2.0f * cap, r, cap);
+      float largest = 0.0f;
+#pragma unroll
+      for (int b = 0; b < N; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) largest = fmaxf(largest, fabsf(x[b][r]));
+      const bool flat = !__any(largest * factor >= kFlat);
+      // (the factors are taken anew in each branch, or the compiler would take what both have in common
+      // for all sums before it)
+      float f = factor, s = straight;
+      if (flat) {
+        asm volatile("" : "+v"(f), "+v"(s));
+#pragma unroll
+        for (int b = 0; b < N; ++b)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) x[b][r] = series(x[b][r] * f) * (x[b][r] * s);
+      } else {
+        asm volatile("" : "+v"(f), "+v"(s));
+#pragma unroll
+        for (int b = 0; b < N; ++b)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float v = x[b][r] * f;
+            const float small = series(v) * (x[b][r] * s);
+            // tanh = 1 - 2 r, r = 1 / (exp(2 x) + 1)
+            const float e = __builtin_amdgcn_exp2f(v * (2.0f * kLog2e));
+            const float large = __builtin_fmaf(-2.0f * cap, __builtin_amdgcn_rcpf(e + 1.0f), cap);
+            x[b][r] = fabsf(v) < kFlat ? small : large;
+            if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // (or registers run out)
+          }
+      }
     }
   }
+  // tanh(x) / x, off by up to 2^-26 below kFlat
+  static __device__ __forceinline__ float series(float x) {
+    const float z = x * x;
+    float s = __builtin_fmaf(z, 1.72414891e-2f, -5.30454926e-2f);
+    s = __builtin_fmaf(z, s, 1.33258790e-1f);
+    s = __builtin_fmaf(z, s, -3.33331436e-1f);
+    return __builtin_fmaf(z, s, 1.0f);
+  }
+  __device__ __forceinline__ float capped(float x) const {   // binary32
+    const float plain = x * straight;
+    x *= factor;
+    const float z = x * x;
+    float s = __builtin_fmaf(z, 3.59212803e-3f, -8.86323552e-3f);
+    s = __builtin_fmaf(z, s, 2.18694885e-2f);
+    s = __builtin_fmaf(z, s, -5.39682540e-2f);
+    s = __builtin_fmaf(z, s, 1.33333333e-1f);
+    s = __builtin_fmaf(z, s, -3.33333333e-1f);
+    s = __builtin_fmaf(z, s, 1.0f);
+    // 1 - 2 e / (1 + e) of e = exp(-2 |x|), which falls to 0 for the largest ones
+    const float e = exp_unit<kF32>(-2.0f * fabsf(x));
+    const float l = copysignf(__builtin_fmaf(-2.0f * e, __builtin_amdgcn_rcpf(1.0f + e), 1.0f), x);
+    return fabsf(x) < 0.4f ? plain * s : cap * l;
+  }
+  // 1 - tanh^2 of a capped score, which the gradient takes
+  __device__ __forceinline__ float bend(float y) const {
+    if constexpr (!has_cap(MODE)) return 1.0f;
+    const float t = y * uncap;
+    return __builtin_fmaf(-t, t, 1.0f);
+  }
 
-  // x: a sum of products; distance: |distance - c| to the key
-  __device__ __forceinline__ float at(float x, float distance, int c, float& bend) const {
-    bend = 1.0f;
-    if constexpr (!has_bias(MODE)) {
-      return x;
-    } else {
-      float y = x * factor;
-      if constexpr (has_cap(MODE)) y = capped(x, bend);
-      return __builtin_fmaf(-slope, fabsf(distance - (float)c), y);
-    }
+  // x: a sum of products, or its capped score; distance: |distance - c| to the key
+  __device__ __forceinline__ float at(float x, float distance, int c) const {
+    if constexpr (!has_bias(MODE)) return x;
+    return __builtin_fmaf(-slope, fabsf(distance - (float)c), has_cap(MODE) ? x : x * factor);
   }
   // the largest score, in units, from the largest of what `at` gives
   __device__ __forceinline__ float scaled(float y) const {
-    if (MODE == kPlainScore) return y * factor;
-    float bend;
-    if (MODE == kCapScore) return y == -INFINITY ? y : capped(y, bend);
-    return y;
+    return MODE == kPlainScore ? y * factor : y;
   }
-  // exp(score - base); of a masked -infinity 0, but where MODE is kCapScore
-  __device__ __forceinline__ float weight(float y, float base, float& bend) const {
-    if constexpr (MODE == kPlainScore) {
-      return exp_unit<DT>(__builtin_fmaf(y, factor, -base));
-    } else if constexpr (MODE == kCapScore) {
-      return exp_unit<DT>(capped(y, bend) - base);
-    } else {
-      return exp_unit<DT>(y - base);
-    }
+  // exp(score - base); of a masked -infinity 0
+  __device__ __forceinline__ float weight(float y, float base) const {
+    return exp_unit<DT>(MODE == kPlainScore ? __builtin_fmaf(y, factor, -base) : y - base);
   }
 };
 

@@ -93,16 +93,16 @@ __device__ __forceinline__ void attn_dq(const AttnArgs& g, int tiles, int64_t bl
       for (int b = 0; b < NB; ++b) {
         along.refresh();
         down.refresh();
-        f32x16 x, dp;
+        f32x16 x[1], dp;
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          x[r] = lse_in_sum<DT, MODE>() ? lse : 0.0f;
+          x[0][r] = lse_in_sum<DT, MODE>() ? lse : 0.0f;
           dp[r] = minus_d;
         }
         auto rows = [&](int kk) { return Two{along.load(lk, b, kk), along.load(lv, b, kk)}; };
         auto ahead = read_first<3>(rows);
         products<T::STEPS, 3>(ahead, rows, [&](int kk, const Two& f) {
-          x = mma<DT>(f.a, fq[kk], x);
+          x[0] = mma<DT>(f.a, fq[kk], x[0]);
           dp = mma<DT>(f.b, fdo[kk], dp);
         });
         auto key = [&](int i) { return down.load(lk, i % T::BLOCKS, b * chunks<DT>() + i / T::BLOCKS); };
@@ -113,22 +113,21 @@ __device__ __forceinline__ void attn_dq(const AttnArgs& g, int tiles, int64_t bl
           const int j = r / 4 * 8 + r % 4;
           return (j < pre) | ((j >= low) & (j <= high));
         };
-        // (a capped -infinity would be finite: there the weight is cleared)
+        if constexpr (has_cap(MODE)) score.cap_all(x);
         if (!has_cap(MODE) && !whole) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) x[r] = seen(r) ? x[r] : -INFINITY;
+          for (int r = 0; r < 16; ++r) x[0][r] = seen(r) ? x[0][r] : -INFINITY;
         }
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          float bend;
-          const float y = score.at(x[r], distance, 32 * b + r / 4 * 8 + r % 4, bend);
-          float p = score.weight(y, lse_in_sum<DT, MODE>() ? 0.0f : lse, bend);
+          const float y = score.at(x[0][r], distance, 32 * b + r / 4 * 8 + r % 4);
+          float p = score.weight(y, lse_in_sum<DT, MODE>() ? 0.0f : lse);
           if (has_cap(MODE)) p = whole | seen(r) ? p : 0.0f;
-          x[r] = p * dp[r] * bend;
+          x[0][r] = p * dp[r] * score.bend(x[0][r]);
         }
         u32x4 p[chunks<DT>()];
 #pragma unroll
-        for (int c = 0; c < chunks<DT>(); ++c) p[c] = pack_chunk<DT>(x, c);
+        for (int c = 0; c < chunks<DT>(); ++c) p[c] = pack_chunk<DT>(x[0], c);
         products<chunks<DT>() * T::BLOCKS, 4>(keys_ahead, key, [&](int i, const u32x4& f) {
           acc[i % T::BLOCKS] = mma<DT>(f, p[i / T::BLOCKS], acc[i % T::BLOCKS]);
         });
@@ -280,14 +279,14 @@ __device__ __forceinline__ void attn_dkv(const AttnArgs& g, int tiles, int64_t b
         auto info = [&](int which, int c) {
           return *reinterpret_cast<const f32x4*>(li + which * 256 + (32 * b + 8 * c + 4 * half) * 4);
         };
-        f32x16 x, dp;
+        f32x16 x[1], dp;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const f32x4 minus_d = info(1, c);
           const f32x4 lse = lse_in_sum<DT, MODE>() ? info(0, c) : (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[4 * c + e] = lse[e];
+            x[0][4 * c + e] = lse[e];
             dp[4 * c + e] = minus_d[e];
           }
         }
@@ -297,7 +296,7 @@ __device__ __forceinline__ void attn_dkv(const AttnArgs& g, int tiles, int64_t b
         };
         auto ahead = read_first<2>(rows);
         products<T::STEPS, 2>(ahead, rows, [&](int kk, const Three& f) {
-          x = mma<DT>(f.a, fk[kk], x);
+          x[0] = mma<DT>(f.a, fk[kk], x[0]);
           dp = mma<DT>(f.b, f.c, dp);
         });
         auto columns = [&](int i) {
@@ -311,9 +310,10 @@ __device__ __forceinline__ void attn_dkv(const AttnArgs& g, int tiles, int64_t b
           const int i = r / 4 * 8 + r % 4;
           return (i >= from) & (i <= to);
         };
+        if constexpr (has_cap(MODE)) score.cap_all(x);
         if (!has_cap(MODE) && !whole) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) x[r] = seen(r) ? x[r] : -INFINITY;
+          for (int r = 0; r < 16; ++r) x[0][r] = seen(r) ? x[0][r] : -INFINITY;
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -321,18 +321,17 @@ __device__ __forceinline__ void attn_dkv(const AttnArgs& g, int tiles, int64_t b
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int r = 4 * c + e;
-            float bend;
-            const float y = score.at(x[r], distance, -(32 * b + 8 * c + e), bend);
-            float p = score.weight(y, lse[e], bend);
+            const float y = score.at(x[0][r], distance, -(32 * b + 8 * c + e));
+            float p = score.weight(y, lse[e]);
             if (has_cap(MODE)) p = whole | seen(r) ? p : 0.0f;
-            x[r] = p;
-            dp[r] = p * dp[r] * bend;
+            dp[r] = p * dp[r] * score.bend(x[0][r]);
+            x[0][r] = p;
           }
         }
         u32x4 p[chunks<DT>()], d[chunks<DT>()];
 #pragma unroll
         for (int c = 0; c < chunks<DT>(); ++c) {
-          p[c] = pack_chunk<DT>(x, c);
+          p[c] = pack_chunk<DT>(x[0], c);
           d[c] = pack_chunk<DT>(dp, c);
         }
         products<chunks<DT>() * T::BLOCKS, 2>(columns_ahead, columns, [&](int i, const Two& f) {
@@ -480,8 +479,7 @@ lowbit_status launch_back_mode(const AttnArgs& a, hipStream_t s) {
 
 template <int DT>
 lowbit_status launch_attn_back(const AttnArgs& a, hipStream_t s) {
-  switch (score_mode<DT>(a)) {
-    case kWideCapScore: return launch_back_mode<DT, DT == kBF16 ? kWideCapScore : kCapScore>(a, s);
+  switch (score_mode(a)) {
     case kPlainScore: return launch_back_mode<DT, kPlainScore>(a, s);
     case kBiasScore: return launch_back_mode<DT, kBiasScore>(a, s);
     case kCapScore: return launch_back_mode<DT, kCapScore>(a, s);

@@ -17,8 +17,8 @@ namespace {
 // products of 32 cycles and about 260 vector instructions a tile and wave).  8 Ki tokens,
 // causal, 32 / 8 heads of 128 bfloat16: 525 us, 1.05 PFLOP/s of what is visible; matrix units
 // busy 52 % of the time, no bank of LDS met twice.  With the operands read right before their
-// products 577 us.  Capped scores take two exps and a reciprocal each: nine ragged documents of 8 Ki
-// tokens, 16 heads of 64, window 1024, 82 us (tanh of the mathematical library: 129).
+// products 577 us.  Nine ragged documents of 8 Ki tokens, 16 heads of 64, window 1024, capped scores:
+// 74 us, and 100 where scores are beyond half the cap (Score::cap_all).
 template <int DT, int D>
 struct Forward {
   static constexpr int ES = elem_size<DT>(), KT = DT == kF32 ? 32 : 64, NB = KT / 32;
@@ -99,8 +99,7 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
     float top = -INFINITY, sum = 0.0f;             // sum: of this half's keys
     score.head(g, head);
 
-    auto compute = [&](const char* lk, const char* lv, int t, auto whole_tile) {
-      const bool whole = whole_tile;
+    auto compute = [&](const char* lk, const char* lv, int t, bool whole) {
       along.refresh();
       down.refresh();
       f32x16 x[NB];
@@ -117,13 +116,14 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
       const int j0 = t * KT;
       const float distance = (float)(i + shift - j0 - 4 * half);
       float most = -INFINITY;
+      if constexpr (has_cap(MODE)) score.cap_all(x);
+      if constexpr (has_bias(MODE)) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          float bend;
-          x[b][r] = score.at(x[b][r], distance, 32 * b + r / 4 * 8 + r % 4, bend);
-        }
+          for (int r = 0; r < 16; ++r)
+            x[b][r] = score.at(x[b][r], distance, 32 * b + r / 4 * 8 + r % 4);
+      }
       const int base_key = j0 + 4 * half;
       const int low = see.low - base_key, high = see.high - base_key, pre = see.prefix - base_key;
       auto seen = [&](int j) { return (j < pre) | ((j >= low) & (j <= high)); };
@@ -155,14 +155,7 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          float bend;
-          x[b][r] = score.weight(x[b][r], base, bend);
-        }
-        if (MODE == kCapScore && !whole) {
-#pragma unroll
-          for (int r = 0; r < 16; ++r) x[b][r] = seen(32 * b + r / 4 * 8 + r % 4) ? x[b][r] : 0.0f;
-        }
+        for (int r = 0; r < 16; ++r) x[b][r] = score.weight(x[b][r], base);
 #pragma unroll
         for (int r = 0; r < 16; ++r) sum += x[b][r];
 #pragma unroll
@@ -180,11 +173,7 @@ __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2) at
       issue(keys.tile(u + 1), nk, nv, u + 1 < keys.count);
       const int t = keys.tile(u), j0 = t * KT;
       const bool whole = (j0 + KT <= q.prefix) || (j0 >= wh.low && j0 + KT - 1 <= wl.high);
-      // (capped scores are masked twice, so that the compiler would take the masks of whole tiles
-      // too: a build for each)
-      if (MODE != kCapScore) compute(lk, lv, t, whole);
-      else if (whole) compute(lk, lv, t, std::true_type());
-      else compute(lk, lv, t, std::false_type());
+      compute(lk, lv, t, whole);
     };
     issue(keys.tile(0), lk0, lv0, keys.count > 0);
     int u = 0;
@@ -239,11 +228,9 @@ template <int DT, int D>
 lowbit_status launch_attn_width(const AttnArgs& a, hipStream_t s) {
   const int tiles = attn_tiles(a.q_rows, a.sequences);
   const int64_t blocks = capped(Items(tiles, a.kv_heads, a.group * a.q_parts).total);
-  const int mode = score_mode<DT>(a);
+  const int mode = score_mode(a);
   const lowbit_status st =
-      DT == kBF16 && mode == kWideCapScore
-          ? launch(&attn_kernel<DT, D, DT == kBF16 ? kWideCapScore : kPlainScore>, blocks, kAttnThreads, s, a, tiles)
-      : mode == kPlainScore  ? launch(&attn_kernel<DT, D, kPlainScore>, blocks, kAttnThreads, s, a, tiles)
+      mode == kPlainScore  ? launch(&attn_kernel<DT, D, kPlainScore>, blocks, kAttnThreads, s, a, tiles)
       : mode == kBiasScore ? launch(&attn_kernel<DT, D, kBiasScore>, blocks, kAttnThreads, s, a, tiles)
       : mode == kCapScore  ? launch(&attn_kernel<DT, D, kCapScore>, blocks, kAttnThreads, s, a, tiles)
                            : launch(&attn_kernel<DT, D, kCapBiasScore>, blocks, kAttnThreads, s, a, tiles);
