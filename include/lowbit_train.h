@@ -289,7 +289,8 @@ int64_t lowbit_attention_workspace(const lowbit_attention_params* p, int32_t bac
  *   lse    : q_heads x q_rows binary32, dense
  *   q_begin, k_begin : sequences + 1 int32, device, not decreasing, from 0 up to at
  *            most q_rows (k_rows); values beyond are cut to that.  Rows before the
- *            first and behind the last sequence are neither read nor written.  Both
+ *            first and behind the last sequence are not written, and nothing depends on
+ *            what they hold.  Both
  *            NULL: sequences of q_rows / sequences queries and k_rows / sequences keys
  *            each (they have to divide); k_begin NULL: the same as q_begin (then
  *            k_rows == q_rows); q_begin NULL alone: queries in equal sequences.
@@ -349,8 +350,8 @@ int64_t lowbit_orthogonalize_workspace(const lowbit_orthogonalize_params* p);
  * Newton-Schulz.  Of each matrix
  *     X = g / (sqrt(sum g^2) + eps);   `steps` times  A = X X^T, X = a X + (b A + c A A) X;
  *     out = scale X                    (for rows > cols: of g's transpose, turned back)
- * With a = 3.4445, b = -4.7750, c = 2.0315 five steps bring all but the smallest
- * singular values to between 0.7 and 1.2.
+ * With a = 3.4445, b = -4.7750, c = 2.0315 (the coefficients that K. Jordan published with the
+ * Muon optimizer, 2024) five steps bring all but the smallest singular values to between 0.7 and 1.2.
  *   g   : batch x rows x cols, of p->type
  *   out : batch x rows x cols bfloat16 (written); may be g where that is bfloat16
  * X is held in binary32 throughout.  The products' operands (X, A, b A + c A A) are rounded

@@ -22,8 +22,7 @@ struct Back {
 
 // dq: four waves, each 32 queries, as in the forward pass; the scores and dout.v
 // are taken again, transposed, and their gradient is, as it lies, the operand
-// of the product with the keys.  8 Ki tokens, causal, 32 / 8 heads of 128 bfloat16: three
-// products in 695 us alone, 1.19 PFLOP/s.
+// of the product with the keys: three products.
 template <int DT, int D, int MODE>
 __device__ __forceinline__ void attn_dq(const AttnArgs& g, int tiles, int64_t block, int64_t blocks,
                                         char* lk0, char* lv0, char* lk1, char* lv1) {
@@ -181,9 +180,7 @@ struct Keys {
 // pass by in tiles.  A key a lane and queries down the registers, so that the weights
 // and the scores' gradient are operands as they lie here too.  Where there are too few
 // tiles of keys for the chip, the queries of all heads are shared out in g.k_parts
-// even parts, whose sums a second kernel adds in order.  The same 8 Ki tokens: four products in 990
-// us alone, 1.11 PFLOP/s (uncut, 512 workgroups whose work falls from twice the mean to nothing,
-// 1964 us).
+// even parts, whose sums a second kernel adds in order: four products.
 template <int DT, int D, int MODE>
 __device__ __forceinline__ void attn_dkv(const AttnArgs& g, int tiles, int64_t block, int64_t blocks,
                                          char* lq0, char* ld0, char* li0, char* lq1, char* ld1,
@@ -422,8 +419,10 @@ __device__ __forceinline__ void attn_dkv_sum(const AttnArgs& g, int tiles, int64
 }
 
 // Both halves in one launch: neither waits for the other's last workgroups.  The first k_blocks
-// workgroups, whose work is longer, take dk and dv.  8 Ki tokens as above 1620 to 1660 us (in two
-// launches 1680 to 1740), five ragged documents 95 us (98), three binary32 sequences 93 (110).
+// workgroups, whose work is longer, take dk and dv.  Bound by the matrix units where they are
+// full: 8 Ki tokens, causal, 32 / 8 heads of 128 bfloat16, 1590 us of the gradient's 1650 (in two launches
+// 1680 to 1740), 1.21 PFLOP/s of the seven products, matrix units busy 64 % of the cycles, 0.1 % of
+// LDS's in conflicts.  Five ragged documents 95 us (98), three binary32 sequences 93 (110).
 template <int DT, int D, int MODE>
 __global__ void __launch_bounds__(kAttnThreads, DT == kF32 && D > 64 ? 1 : 2)
     attn_back_kernel(AttnArgs g, int q_tiles, int k_tiles, int k_blocks) {

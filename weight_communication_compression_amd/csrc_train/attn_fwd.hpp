@@ -15,8 +15,8 @@ namespace {
 // Bound by the matrix units and the vector ALU together, at the clock that power leaves: two
 // workgroups a CU, two waves a SIMD, one of which takes exps while the other multiplies (32
 // products of 32 cycles and about 260 vector instructions a tile and wave).  8 Ki tokens,
-// causal, 32 / 8 heads of 128 bfloat16: 525 us, 1.05 PFLOP/s of what is visible; matrix units
-// busy 52 % of the time, no bank of LDS met twice.  With the operands read right before their
+// causal, 32 / 8 heads of 128 bfloat16: 512 us, 1.07 PFLOP/s of what is visible; matrix units
+// busy 54 % of the cycles, no bank conflict counted.  With the operands read right before their
 // products 577 us.  Nine ragged documents of 8 Ki tokens, 16 heads of 64, window 1024, capped scores:
 // 74 us, and 100 where scores are beyond half the cap (Score::cap_all).
 template <int DT, int D>

@@ -139,10 +139,14 @@ struct AttnPlan {
 // The chip holds 512 workgroups at one time.  Where there are fewer tiles of
 // queries, their keys are cut, down to 256 on average.  By k and v the gradient's workgroups
 // take from nothing to twice the mean of a causal sequence, so that more than one round of them
-// is wanted, the long ones first; their queries are cut, down to as many of all heads.  (Five
-// ragged documents, 144 tiles of keys, gradient by k and v and the parts' sums: 8 parts 78 us, 6
-// 70, 5 67, 4 72; by q, 432 tiles: 1 part 55 us, 2 54, 3 61.)  Of binary32 products take eight times as long, so that parts go down to
-// 64, and of wide heads a CU holds one workgroup: as many parts as fill one round.
+// is wanted, the long ones first; their queries are cut, down to as many of all heads.  Of binary32
+// products take eight times as long, so that parts go down to 64, and of wide heads a CU holds one
+// workgroup: as many parts as fill one round.  Whole gradients, parts by q and by k and v, the rule's
+// first: five ragged documents (432 and 144 tiles) 2 and 5 106 us, 2 and 4 103, 1 and 3 105, 1 and 4
+// 106, 1 and 6 117, 3 and 5 116, 1 and 2 140, uncut 234; 8 Ki tokens of 32 / 8 heads (2080 and 520) 1 and 2
+// 1645, 1 and 3 1662, uncut 1690; three binary32 sequences, wide heads (54 and 78) 4 and 3 102, 3 and 2 108, 3
+// and 3 112, uncut 182; 2048 binary32 tokens of 8 heads of 64 (136 and 136) 6 and 5 169, 4 and 4 170, 2 and 4 242,
+// uncut 304.
 AttnPlan attn_plan(const lowbit_attention_params* p, bool backward) {
   AttnPlan w{};
   const int64_t each = std::max(p->sequences, 1), group = p->q_heads / p->kv_heads;
