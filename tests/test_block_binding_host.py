@@ -28,7 +28,8 @@ def library(monkeypatch):
     monkeypatch.setattr(L, "_lib", stand_in)
     monkeypatch.setattr(L, "_dev", lambda t, what: t.data_ptr())
     monkeypatch.setattr(L, "_gpu", lambda t, what: t.data_ptr())
-    monkeypatch.setattr(L, "_stream", lambda t: 0)
+    monkeypatch.setattr(L, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(L, "_current_device", lambda: -1)       # host tensors'
     return stand_in
 
 

@@ -39,7 +39,8 @@ def library(monkeypatch):
     monkeypatch.setattr(L, "_scratch", scratch)
     monkeypatch.setattr(L, "_dev", lambda t, what: t.data_ptr())
     monkeypatch.setattr(L, "_gpu", lambda t, what: t.data_ptr())
-    monkeypatch.setattr(L, "_stream", lambda t: 0)
+    monkeypatch.setattr(L, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(L, "_current_device", lambda: -1)       # host tensors'
     return stand_in
 
 

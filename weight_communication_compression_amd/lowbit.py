@@ -3,7 +3,8 @@ the training-step operators, ``include/lowbit_train.h``).
 
 Argument marshalling only: every step runs in the gfx950 HIP kernels behind the
 C ABI.  torch is used for device memory (tensors) and for
-the current HIP stream.  If the library is missing or a call fails, a
+the current HIP stream.  A call goes to the device of its tensors, whatever the
+current one is, on the current stream there.  If the library is missing or a call fails, a
 ``LowbitError`` is raised -- there is no CPU fallback.
 
 Wire format of the returned tensors:
@@ -196,15 +197,11 @@ def _dev(t: torch.Tensor, what: str) -> int:
     return t.data_ptr()
 
 
-# The current stream's handle without the Stream object around it (0.15 instead of
-# 2 us a call); torch versions without it take the long way.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream(t: torch.Tensor) -> int:
-    if _raw_stream is not None:
-        return _raw_stream(t.get_device())
-    return torch.cuda.current_stream(t.device).cuda_stream
+# The current device, and its current stream's handle without the Stream object around it (0.15
+# instead of 2 us a call); torch versions without these take the long way.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _qp(bitwidth, block_size, stochastic=False, seed=0, index_offset=0, hints=0) -> QParams:
@@ -215,6 +212,19 @@ def _qp(bitwidth, block_size, stochastic=False, seed=0, index_offset=0, hints=0)
 def _check(status: int, what: str) -> None:
     if status != OK:
         raise LowbitError(status, what)
+
+
+def _launch(fn, like: torch.Tensor, *args) -> None:
+    """fn(*args, stream) on like's device, with the current stream there.  (A kernel goes to the
+    current device, where the stream of another one, or its default stream, would be a wrong one.)"""
+    device = like.get_device()
+    if device == _current_device():
+        status = fn(*args, _raw_stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(device))
+    if status != OK:
+        raise LowbitError(status, fn.__name__)
 
 
 def _need_codes(t: torch.Tensor, n: int, bitwidth: int, what: str) -> None:
@@ -255,9 +265,8 @@ def quantize_pack(x: torch.Tensor, bitwidth: int, block_size: int, stochastic: b
     scales = _out_scales(n, block_size, x, scales)
     qp = _qp(bitwidth, block_size, stochastic, seed, index_offset,
              HINT_INPUT_REUSED if input_reused else 0)
-    _check(lib().lowbit_quantize_pack(_dev(x, "x"), _dtype_code(x), n, ctypes.byref(qp),
-                                      _dev(codes, "codes"), _dev(scales, "scales"), _stream(x)),
-           "lowbit_quantize_pack")
+    _launch(lib().lowbit_quantize_pack, x, _dev(x, "x"), _dtype_code(x), n, ctypes.byref(qp),
+            _dev(codes, "codes"), _dev(scales, "scales"))
     return codes, scales
 
 
@@ -271,9 +280,8 @@ def unpack_dequant(codes: torch.Tensor, scales: torch.Tensor, n: int, bitwidth: 
     if out.dtype != torch.float32 or out.numel() < n:
         raise LowbitError(EINVAL, "out must be float32 with >= n elements")
     qp = _qp(bitwidth, block_size)
-    _check(lib().lowbit_unpack_dequant(_dev(codes, "codes"), _dev(scales, "scales"), n,
-                                       ctypes.byref(qp), _dev(out, "out"), _stream(codes)),
-           "lowbit_unpack_dequant")
+    _launch(lib().lowbit_unpack_dequant, codes, _dev(codes, "codes"), _dev(scales, "scales"), n,
+            ctypes.byref(qp), _dev(out, "out"))
     return out
 
 
@@ -290,9 +298,8 @@ def hadamard_quantize_pack(x: torch.Tensor, bitwidth: int, block_size: int,
     scales = _out_scales(n, block_size, x, scales)
     qp = _qp(bitwidth, block_size, stochastic, seed, index_offset,
              HINT_INPUT_REUSED if input_reused else 0)
-    _check(lib().lowbit_hadamard_quantize_pack(_dev(x, "x"), _dtype_code(x), n, ctypes.byref(qp),
-                                               _dev(codes, "codes"), _dev(scales, "scales"),
-                                               _stream(x)), "lowbit_hadamard_quantize_pack")
+    _launch(lib().lowbit_hadamard_quantize_pack, x, _dev(x, "x"), _dtype_code(x), n,
+            ctypes.byref(qp), _dev(codes, "codes"), _dev(scales, "scales"))
     return codes, scales
 
 
@@ -306,9 +313,8 @@ def hadamard_unpack_dequant(codes: torch.Tensor, scales: torch.Tensor, n: int, b
     if out.dtype != torch.float32 or out.numel() < n:
         raise LowbitError(EINVAL, "out must be float32 with >= n elements")
     qp = _qp(bitwidth, block_size)
-    _check(lib().lowbit_hadamard_unpack_dequant(_dev(codes, "codes"), _dev(scales, "scales"), n,
-                                                ctypes.byref(qp), _dev(out, "out"),
-                                                _stream(codes)), "lowbit_hadamard_unpack_dequant")
+    _launch(lib().lowbit_hadamard_unpack_dequant, codes, _dev(codes, "codes"),
+            _dev(scales, "scales"), n, ctypes.byref(qp), _dev(out, "out"))
     return out
 
 
@@ -322,9 +328,8 @@ def ef_compress(g: torch.Tensor, residual: torch.Tensor, bitwidth: int, block_si
     codes = _out_codes(n, bitwidth, g, codes)
     scales = _out_scales(n, block_size, g, scales)
     qp = _qp(bitwidth, block_size, stochastic, seed, index_offset)
-    _check(lib().lowbit_ef_compress(_dev(g, "g"), _dtype_code(g), _dev(residual, "residual"), n,
-                                    ctypes.byref(qp), _dev(codes, "codes"),
-                                    _dev(scales, "scales"), _stream(g)), "lowbit_ef_compress")
+    _launch(lib().lowbit_ef_compress, g, _dev(g, "g"), _dtype_code(g), _dev(residual, "residual"),
+            n, ctypes.byref(qp), _dev(codes, "codes"), _dev(scales, "scales"))
     return codes, scales
 
 
@@ -338,9 +343,8 @@ def ef21_compress(g: torch.Tensor, state: torch.Tensor, bitwidth: int, block_siz
     codes = _out_codes(n, bitwidth, g, codes)
     scales = _out_scales(n, block_size, g, scales)
     qp = _qp(bitwidth, block_size, stochastic, seed, index_offset)
-    _check(lib().lowbit_ef21_compress(_dev(g, "g"), _dtype_code(g), _dev(state, "state"), n,
-                                      ctypes.byref(qp), _dev(codes, "codes"),
-                                      _dev(scales, "scales"), _stream(g)), "lowbit_ef21_compress")
+    _launch(lib().lowbit_ef21_compress, g, _dev(g, "g"), _dtype_code(g), _dev(state, "state"), n,
+            ctypes.byref(qp), _dev(codes, "codes"), _dev(scales, "scales"))
     return codes, scales
 
 
@@ -369,20 +373,15 @@ def _reduce(peer_codes, peer_scales, n, bitwidth, block_size, stochastic, seed, 
     qi = _qp(bitwidth, block_size, hints=HINT_INPUT_REUSED if input_reused else 0)
     qo = _qp(ob, oB, stochastic, seed, index_offset)
     tail = (_dev(out_codes, "out_codes"), _dev(out_scales, "out_scales"),
-            _dev(out_sum, "out_sum") if out_sum is not None else None, _stream(like))
+            _dev(out_sum, "out_sum") if out_sum is not None else None)
+    head = (ctypes.cast(cp, ctypes.c_void_p), ctypes.cast(sp, ctypes.c_void_p), P, n,
+            ctypes.byref(qi), ctypes.byref(qo))
     if residual is None:
-        _check(lib().lowbit_reduce_requant(ctypes.cast(cp, ctypes.c_void_p),
-                                           ctypes.cast(sp, ctypes.c_void_p), P, n,
-                                           ctypes.byref(qi), ctypes.byref(qo), *tail),
-               "lowbit_reduce_requant")
+        _launch(lib().lowbit_reduce_requant, like, *head, *tail)
     else:
         if residual.dtype != torch.float32 or residual.numel() != n:
             raise LowbitError(EINVAL, "residual must be float32 with n elements")
-        _check(lib().lowbit_reduce_requant_ef(ctypes.cast(cp, ctypes.c_void_p),
-                                              ctypes.cast(sp, ctypes.c_void_p), P, n,
-                                              ctypes.byref(qi), ctypes.byref(qo),
-                                              _dev(residual, "residual"), *tail),
-               "lowbit_reduce_requant_ef")
+        _launch(lib().lowbit_reduce_requant_ef, like, *head, _dev(residual, "residual"), *tail)
     return out_codes, out_scales, out_sum
 
 
@@ -430,10 +429,8 @@ def wdiff_compress(w_new: torch.Tensor, w_old: torch.Tensor, bitwidth: int, bloc
     codes = _out_codes(n, bitwidth, w_new, codes)
     scales = _out_scales(n, block_size, w_new, scales)
     qp = _qp(bitwidth, block_size, stochastic, seed, index_offset)
-    _check(lib().lowbit_wdiff_compress(_dev(w_new, "w_new"), _dev(w_old, "w_old"),
-                                       _dtype_code(w_new), n, ctypes.byref(qp),
-                                       _dev(codes, "codes"), _dev(scales, "scales"),
-                                       _stream(w_new)), "lowbit_wdiff_compress")
+    _launch(lib().lowbit_wdiff_compress, w_new, _dev(w_new, "w_new"), _dev(w_old, "w_old"),
+            _dtype_code(w_new), n, ctypes.byref(qp), _dev(codes, "codes"), _dev(scales, "scales"))
     return codes, scales
 
 
@@ -448,10 +445,8 @@ def wdiff_apply(w_old: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, 
     if out.dtype != w_old.dtype or out.numel() != n:
         raise LowbitError(EINVAL, "out must match w_old")
     qp = _qp(bitwidth, block_size)
-    _check(lib().lowbit_wdiff_apply(_dev(w_old, "w_old"), _dev(codes, "codes"),
-                                    _dev(scales, "scales"), n, ctypes.byref(qp),
-                                    _dev(out, "out"), _dtype_code(w_old), _stream(w_old)),
-           "lowbit_wdiff_apply")
+    _launch(lib().lowbit_wdiff_apply, w_old, _dev(w_old, "w_old"), _dev(codes, "codes"),
+            _dev(scales, "scales"), n, ctypes.byref(qp), _dev(out, "out"), _dtype_code(w_old))
     return out
 
 
@@ -459,8 +454,7 @@ def copy_f32(x: torch.Tensor, y: torch.Tensor) -> torch.Tensor:
     """Plain float32 copy kernel (bandwidth reference, not a codec step)."""
     if x.dtype != torch.float32 or y.dtype != torch.float32 or y.numel() != x.numel():
         raise LowbitError(EINVAL, "copy_f32 needs two float32 tensors of equal size")
-    _check(lib().lowbit_copy_f32(_dev(x, "x"), _dev(y, "y"), x.numel(), _stream(x)),
-           "lowbit_copy_f32")
+    _launch(lib().lowbit_copy_f32, x, _dev(x, "x"), _dev(y, "y"), x.numel())
     return y
 
 
@@ -469,8 +463,7 @@ def add_inplace_f32(x: torch.Tensor, y: torch.Tensor) -> torch.Tensor:
     pattern (bandwidth reference for that kernel, not a codec step)."""
     if x.dtype != torch.float32 or y.dtype != torch.float32 or y.numel() != x.numel():
         raise LowbitError(EINVAL, "add_inplace_f32 needs two float32 tensors of equal size")
-    _check(lib().lowbit_add_inplace_f32(_dev(x, "x"), _dev(y, "y"), x.numel(), _stream(y)),
-           "lowbit_add_inplace_f32")
+    _launch(lib().lowbit_add_inplace_f32, y, _dev(x, "x"), _dev(y, "y"), x.numel())
     return y
 
 
@@ -484,8 +477,8 @@ def xor_streams(streams: Sequence[torch.Tensor], out: torch.Tensor) -> torch.Ten
     if not 1 <= P <= 16:
         raise LowbitError(EINVAL, "xor_streams needs 1 to 16 streams")
     sp = (ctypes.c_void_p * P)(*[_dev(t, "stream") for t in streams])
-    _check(lib().lowbit_xor_streams_u32(ctypes.cast(sp, ctypes.c_void_p), P, n, _dev(out, "out"),
-                                        _stream(out)), "lowbit_xor_streams_u32")
+    _launch(lib().lowbit_xor_streams_u32, out, ctypes.cast(sp, ctypes.c_void_p), P, n,
+            _dev(out, "out"))
     return out
 
 
@@ -500,8 +493,7 @@ def fold_f32(x: torch.Tensor, bitwidth: int, out: Optional[torch.Tensor] = None)
         out = torch.empty(nw, dtype=torch.int32, device=x.device)
     elif out.dtype != torch.int32 or out.numel() < nw:
         raise LowbitError(EINVAL, f"out must be int32 with >= {nw} words")
-    _check(lib().lowbit_fold_f32(_dev(x, "x"), n, int(bitwidth), _dev(out, "out"), _stream(x)),
-           "lowbit_fold_f32")
+    _launch(lib().lowbit_fold_f32, x, _dev(x, "x"), n, int(bitwidth), _dev(out, "out"))
     return out
 
 
@@ -520,9 +512,8 @@ def stream_probe(op: int, dst: torch.Tensor, src: Optional[torch.Tensor] = None,
     if op == PROBE_COPY and dst.numel() < nwords:
         raise LowbitError(EINVAL, "dst too small")
     sp = _dev(src, "src") if src is not None else None
-    _check(lib().lowbit_stream_probe_u32(int(op), sp, _dev(dst, "dst"), nwords,
-                                         int(value) & 0xFFFFFFFF, int(waves), int(bool(nontemporal)),
-                                         _stream(dst)), "lowbit_stream_probe_u32")
+    _launch(lib().lowbit_stream_probe_u32, dst, int(op), sp, _dev(dst, "dst"), nwords,
+            int(value) & 0xFFFFFFFF, int(waves), int(bool(nontemporal)))
     return dst
 
 
@@ -580,9 +571,8 @@ def dropout(x: torch.Tensor, p: float, seed: int, residual: Optional[torch.Tenso
         raise LowbitError(EINVAL, "residual must match x in dtype, size and device")
     dt = _dtype_code(x)
     out = _out_like(x, out, "out")
-    _check(lib().lowbit_dropout(_dev(x, "x"), _opt(residual, "residual"), dt, x.numel(), p,
-                                int(seed) & _U64, int(index_offset), _dev(out, "out"), _stream(x)),
-           "lowbit_dropout")
+    _launch(lib().lowbit_dropout, x, _dev(x, "x"), _opt(residual, "residual"), dt, x.numel(), p,
+            int(seed) & _U64, int(index_offset), _dev(out, "out"))
     return out
 
 
@@ -592,9 +582,8 @@ def dropout_backward(dy: torch.Tensor, p: float, seed: int, index_offset: int = 
     (The residual's gradient is dy.)  `out` may be dy."""
     dt = _dtype_code(dy)
     out = _out_like(dy, out, "out")
-    _check(lib().lowbit_dropout_backward(_dev(dy, "dy"), dt, dy.numel(), p, int(seed) & _U64,
-                                         int(index_offset), _dev(out, "out"), _stream(dy)),
-           "lowbit_dropout_backward")
+    _launch(lib().lowbit_dropout_backward, dy, _dev(dy, "dy"), dt, dy.numel(), p, int(seed) & _U64,
+            int(index_offset), _dev(out, "out"))
     return out
 
 
@@ -678,9 +667,8 @@ def block_join(f: torch.Tensor, x: torch.Tensor, post_weight: Optional[torch.Ten
     x_out = _out_like(x, x_out, "x_out")
     z = _out_like(f, z, "z")
     stats = torch.empty(q.rows, 4, dtype=torch.float32, device=f.device)
-    _check(lib().lowbit_block_join(_dev(f, "f"), _dev(x, "x"), *[_opt(t, n) for n, t in named], q,
-                                   _dev(x_out, "x_out"), _dev(z, "z"), _dev(stats, "stats"),
-                                   _stream(f)), "lowbit_block_join")
+    _launch(lib().lowbit_block_join, f, _dev(f, "f"), _dev(x, "x"), *[_opt(t, n) for n, t in named],
+            q, _dev(x_out, "x_out"), _dev(z, "z"), _dev(stats, "stats"))
     return BlockJoin(x_out, z, stats)
 
 
@@ -714,11 +702,10 @@ def block_join_backward(dx_out: torch.Tensor, dz: torch.Tensor, f: torch.Tensor,
     if nbytes < 0 and q.cols > 16384:
         raise LowbitError(EUNSUPPORTED, "block_join_backward: more than 16384 columns")
     ws = _scratch(nbytes, f, workspace, "block_join_backward")
-    _check(L.lowbit_block_join_backward(
-        _dev(dx_out, "dx_out"), _dev(dz, "dz"), _dev(f, "f"), _dev(x_out, "x_out"),
-        _dev(stats, "stats"), *[_opt(t, n) for n, t in named[:4]], q, _dev(df, "df"),
-        _dev(dx, "dx"), *[None if g is None else g.data_ptr() for g in grads],
-        _dev(ws, "workspace"), ws.numel(), _stream(f)), "lowbit_block_join_backward")
+    _launch(L.lowbit_block_join_backward, f, _dev(dx_out, "dx_out"), _dev(dz, "dz"), _dev(f, "f"),
+            _dev(x_out, "x_out"), _dev(stats, "stats"), *[_opt(t, n) for n, t in named[:4]], q,
+            _dev(df, "df"), _dev(dx, "dx"), *[None if g is None else g.data_ptr() for g in grads],
+            _dev(ws, "workspace"), ws.numel())
     return BlockJoinGrads(df, dx, *grads)
 
 
@@ -762,9 +749,8 @@ def linear_xent(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, ignore_
     ws = _scratch(L.lowbit_linear_xent_workspace(q, 0), x, workspace, "linear_xent")
     loss = torch.empty(targets.shape, dtype=torch.float32, device=x.device)
     lse = torch.empty_like(loss)
-    _check(L.lowbit_linear_xent(_dev(x, "x"), _dev(w, "w"), _dev(targets, "targets"), q,
-                                loss.data_ptr(), lse.data_ptr(), _dev(ws, "workspace"), ws.numel(),
-                                _stream(x)), "lowbit_linear_xent")
+    _launch(L.lowbit_linear_xent, x, _dev(x, "x"), _dev(w, "w"), _dev(targets, "targets"), q,
+            loss.data_ptr(), lse.data_ptr(), _dev(ws, "workspace"), ws.numel())
     return LinearXent(loss, lse)
 
 
@@ -785,10 +771,9 @@ def linear_xent_backward(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
     dw = _out_like(w, dw, "dw") if need_dw else None
     L = lib()
     ws = _scratch(L.lowbit_linear_xent_workspace(q, 1), x, workspace, "linear_xent_backward")
-    _check(L.lowbit_linear_xent_backward(
-        _dev(x, "x"), _dev(w, "w"), _dev(targets, "targets"), _dev(lse, "lse"),
-        _dev(dloss, "dloss"), _opt(dlse, "dlse"), q, _opt(dx, "dx"), _opt(dw, "dw"),
-        _dev(ws, "workspace"), ws.numel(), _stream(x)), "lowbit_linear_xent_backward")
+    _launch(L.lowbit_linear_xent_backward, x, _dev(x, "x"), _dev(w, "w"), _dev(targets, "targets"),
+            _dev(lse, "lse"), _dev(dloss, "dloss"), _opt(dlse, "dlse"), q, _opt(dx, "dx"),
+            _opt(dw, "dw"), _dev(ws, "workspace"), ws.numel())
     return LinearXentGrads(dx, dw)
 
 
@@ -855,7 +840,7 @@ def _heads(t: torch.Tensor, what: str):
     return rows, row if rows > 1 else heads * dim, step[-2] if heads > 1 else dim
 
 
-def _rotary(fn, name, x, freqs, positions, rows_per_sequence, layout, scale, out, what):
+def _rotary(fn, x, freqs, positions, rows_per_sequence, layout, scale, out, what):
     if layout not in _LAYOUTS:
         raise LowbitError(EINVAL, "layout must be 'half' or 'interleaved'")
     rows, x_row, x_head = _heads(x, what)
@@ -875,9 +860,8 @@ def _rotary(fn, name, x, freqs, positions, rows_per_sequence, layout, scale, out
     p = RotaryParams(rows, _at_most(rows_per_sequence, max(rows, 1)) or max(rows, 1), x_row, x_head, y_row, y_head,
                      x.shape[-2], x.shape[-1], 2 * freqs.numel(), _LAYOUTS[layout],
                      _dtype_code(x), scale)
-    _check(fn(_gpu(x, what), _dev(freqs, "freqs"),
-              None if positions is None else _dev(positions, "positions"), p, out.data_ptr(),
-              _stream(x)), name)
+    _launch(fn, x, _gpu(x, what), _dev(freqs, "freqs"),
+            None if positions is None else _dev(positions, "positions"), p, out.data_ptr())
     return out
 
 
@@ -894,7 +878,8 @@ def rotary(x: torch.Tensor, freqs: torch.Tensor, positions: Optional[torch.Tenso
     (0: never).  `out` may be x."""
     if x.requires_grad:
         _outside_autograd("rotary")
-    return _rotary(lib().lowbit_rotary, "lowbit_rotary", x, freqs, positions, rows_per_sequence, layout, scale, out, "x")
+    return _rotary(lib().lowbit_rotary, x, freqs, positions, rows_per_sequence, layout, scale, out,
+                   "x")
 
 
 def rotary_backward(dy: torch.Tensor, freqs: torch.Tensor,
@@ -902,8 +887,8 @@ def rotary_backward(dy: torch.Tensor, freqs: torch.Tensor,
                     layout: str = "half", scale: float = 1.0,
                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of `rotary` by x, with its options.  `out` may be dy."""
-    return _rotary(lib().lowbit_rotary_backward, "lowbit_rotary_backward", dy, freqs, positions,
-                   rows_per_sequence, layout, scale, out, "dy")
+    return _rotary(lib().lowbit_rotary_backward, dy, freqs, positions, rows_per_sequence, layout,
+                   scale, out, "dy")
 
 
 class Attention(NamedTuple):
@@ -1030,11 +1015,9 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     L = lib()
     ws, at, nbytes = _attention_scratch(L, p, 0, q, workspace, "attention")
     # (all are on q's device)
-    _check(L.lowbit_attention(_gpu(q, "q"), k.data_ptr(), v.data_ptr(),
-                              _opt(q_begin, "q_begin"), _opt(k_begin, "k_begin"),
-                              _opt(prefix, "prefix"), _opt(slopes, "slopes"), p,
-                              out.data_ptr(), lse.data_ptr(), at, nbytes, _stream(q)),
-           "lowbit_attention")
+    _launch(L.lowbit_attention, q, _gpu(q, "q"), k.data_ptr(), v.data_ptr(),
+            _opt(q_begin, "q_begin"), _opt(k_begin, "k_begin"), _opt(prefix, "prefix"),
+            _opt(slopes, "slopes"), p, out.data_ptr(), lse.data_ptr(), at, nbytes)
     return Attention(out, lse)
 
 
@@ -1062,11 +1045,10 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     dv, p.dv_row, p.dv_head = _attention_grad(dv, v, "dv")
     L = lib()
     ws, at, nbytes = _attention_scratch(L, p, 1, q, workspace, "attention_backward")
-    _check(L.lowbit_attention_backward(
-        dout.data_ptr(), _gpu(q, "q"), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-        _dev(lse, "lse"), _opt(q_begin, "q_begin"), _opt(k_begin, "k_begin"),
-        _opt(prefix, "prefix"), _opt(slopes, "slopes"), p, dq.data_ptr(), dk.data_ptr(),
-        dv.data_ptr(), at, nbytes, _stream(q)), "lowbit_attention_backward")
+    _launch(L.lowbit_attention_backward, q, dout.data_ptr(), _gpu(q, "q"), k.data_ptr(),
+            v.data_ptr(), out.data_ptr(), _dev(lse, "lse"), _opt(q_begin, "q_begin"),
+            _opt(k_begin, "k_begin"), _opt(prefix, "prefix"), _opt(slopes, "slopes"), p,
+            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), at, nbytes)
     return AttentionGrads(dq, dk, dv)
 
 
@@ -1094,6 +1076,6 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750
         raise LowbitError(EINVAL, "out must be bfloat16, of g's shape and device")
     L = lib()
     ws = _scratch(L.lowbit_orthogonalize_workspace(p), g, workspace, "orthogonalize")
-    _check(L.lowbit_orthogonalize(_dev(g, "g"), p, _dev(out, "out"), _dev(ws, "workspace"),
-                                  ws.numel(), _stream(g)), "lowbit_orthogonalize")
+    _launch(L.lowbit_orthogonalize, g, _dev(g, "g"), p, _dev(out, "out"), _dev(ws, "workspace"),
+            ws.numel())
     return out
