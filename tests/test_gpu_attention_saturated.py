@@ -100,6 +100,15 @@ def test_factor_beyond_binary32_of_sums_that_are_not_0(dtype):
 
 
 @BOTH
+@pytest.mark.parametrize("softcap", [1e-20, 1e-32, 1e-36])
+def test_small_caps_of_small_products(softcap, dtype):
+    """Scores that are nothing beside 1, but up to some tens of times their cap: the gradient by q
+    knows the difference."""
+    run([70, 40], softcap=softcap, scale=1.0, grow=softcap, dtype=dtype)
+    run([70, 40], softcap=softcap, scale=0.05, grow=softcap, dtype=dtype, slopes=True)
+
+
+@BOTH
 def test_a_row_beyond_the_cap_changes_no_other(dtype):
     """Waves in which a score comes near the cap take all of theirs another way: to the same bits."""
     q, k, v = inputs([100], [100], 2, 1, 64, dtype, False, 15)

@@ -213,8 +213,8 @@ struct Score {
   float factor, cap, uncap, slope, straight;
   __device__ __forceinline__ explicit Score(const AttnArgs& g) {
     const float unit = unit_of<DT>(), scale = fabsf(g.scale);
-    // (a cap below 2^-100 as that: beside it no score is anything but 0)
-    const float softcap = fmaxf(g.softcap, 0x1p-100f);
+    // (a subnormal cap as 2^-126, whose reciprocal binary32 holds)
+    const float softcap = fmaxf(g.softcap, 0x1p-126f);
     cap = softcap * unit;
     uncap = 1.0f / cap;
     // (a scale of 0 as 2^-100: -infinity times it has to stay what it is)
